@@ -123,6 +123,40 @@ sffn_status check_decode_args(const void *x, int B, const sffn_ffn_weights *w, i
     return SFFN_OK;
 }
 
+// Head layout of the attention calls.
+sffn_status check_heads(int n_heads, int n_kv_heads, int head_dim) {
+    if (n_kv_heads < 1 || n_heads < n_kv_heads || n_heads > 1024 || n_heads % n_kv_heads != 0) return SFFN_ERR_SHAPE;
+    if (n_heads / n_kv_heads > 64) return SFFN_ERR_SHAPE;
+    if (head_dim != 64 && head_dim != 128) return SFFN_ERR_SHAPE;
+    return SFFN_OK;
+}
+
+// Rows of `heads` heads, `stride` elements of `es` bytes apart.
+sffn_status check_rows(const void *p, int64_t stride, int heads, int head_dim, int es) {
+    if (stride < (int64_t)heads * head_dim || stride > (int64_t)1 << 32) return SFFN_ERR_SHAPE;
+    if (!aligned16(p) || (stride * es) % 16 != 0) return SFFN_ERR_ALIGNMENT;
+    return SFFN_OK;
+}
+
+sffn_status check_cache(const sffn_kv_cache *c, int dtype, int n_kv_heads, int head_dim) {
+    if (c->dtype != dtype) return SFFN_ERR_INVALID_ARG;
+    if (c->n_kv_heads != n_kv_heads || c->head_dim != head_dim) return SFFN_ERR_SHAPE;
+    if (c->page_size < 8 || c->page_size > 65536 || (c->page_size & (c->page_size - 1)) != 0) return SFFN_ERR_SHAPE;
+    if (c->n_pages < 1 || (int64_t)c->n_pages * c->n_kv_heads * c->page_size >= (int64_t)1 << 31) return SFFN_ERR_SHAPE;
+    if (!c->k || !c->v) return SFFN_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v)) return SFFN_ERR_ALIGNMENT;
+    return SFFN_OK;
+}
+
+int log2_of(int v) {
+    int n = 0;
+    while ((1 << n) < v) ++n;
+    return n;
+}
+
+constexpr int kPromptMaxSeq = 65536;
+constexpr int kTreeMaxT = 65536;
+
 }  // namespace
 
 namespace sffn {
@@ -424,6 +458,170 @@ sffn_status sffn_prefill(const void *x, const void *y_attn, int L, const sffn_ff
     st = check_ws(workspace, ws_bytes, p.total);
     if (st != SFFN_OK) return st;
     st = run_prefill(x, y_attn, L, w, sel_idx, n_sel, out, workspace, p, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+// ---- the attention half of the layer ----
+
+size_t sffn_attn_workspace_size(int which, int T, int n_seq, int n_heads, int n_kv_heads, int head_dim) {
+    if (T < 0 || T > (1 << 20) || check_heads(n_heads, n_kv_heads, head_dim) != SFFN_OK) return 0;
+    if (which == 0) return kAlign;
+    if (which == 1) return n_seq < 1 || n_seq > kPromptMaxSeq ? 0 : kAlign;
+    if (which == 2) {
+        if (T > kTreeMaxT || n_seq < 1 || n_seq > kTreeMaxSeq || device_sm_count() <= 0) return 0;
+        return make_tree_plan(T, n_heads, n_kv_heads, head_dim).total;
+    }
+    return 0;
+}
+
+sffn_status sffn_qk_norm_rope(int dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, int T, int n_heads, int n_kv_heads, int head_dim,
+                              const void *q_weight, const void *k_weight, float eps, const float *table, int rot_dim,
+                              int max_pos, int style, const int32_t *positions, void *q_out, void *k_out,
+                              const sffn_kv_cache *cache, const int32_t *slots, void *workspace, size_t ws_bytes,
+                              sffn_stream_t stream) {
+    if (dtype != SFFN_F32 && dtype != SFFN_BF16) return SFFN_ERR_INVALID_ARG;
+    if (style != SFFN_ROPE_HALF && style != SFFN_ROPE_INTERLEAVED) return SFFN_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || std::isinf(eps)) return SFFN_ERR_INVALID_ARG;
+    sffn_status st = check_heads(n_heads, n_kv_heads, head_dim);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > (1 << 20)) return SFFN_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 16 != 0) return SFFN_ERR_SHAPE;
+    if ((cache == nullptr) != (slots == nullptr)) return SFFN_ERR_INVALID_ARG;
+    if (cache) {
+        st = check_cache(cache, dtype, n_kv_heads, head_dim);
+        if (st != SFFN_OK) return st;
+    }
+    if (T == 0) return SFFN_OK;
+    if (!q || !k || !q_out || (cache && !v) || (!cache && !k_out)) return SFFN_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!table || !positions || max_pos < 1)) return SFFN_ERR_INVALID_ARG;
+    const int es = dtype == SFFN_BF16 ? 2 : 4;
+    if ((st = check_rows(q, q_stride, n_heads, head_dim, es)) != SFFN_OK) return st;
+    if ((st = check_rows(k, k_stride, n_kv_heads, head_dim, es)) != SFFN_OK) return st;
+    if (cache && (st = check_rows(v, v_stride, n_kv_heads, head_dim, es)) != SFFN_OK) return st;
+    if (!aligned16(q_weight) || !aligned16(k_weight) || !aligned16(table) || !aligned16(q_out) || !aligned16(k_out))
+        return SFFN_ERR_ALIGNMENT;
+    st = check_ws(workspace, ws_bytes, kAlign);
+    if (st != SFFN_OK) return st;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.table = table;
+    a.rot = rot_dim;
+    a.max_pos = max_pos;
+    a.style = style;
+    a.positions = positions;
+    a.T = T;
+    a.hq = n_heads;
+    a.hkv = n_kv_heads;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    if (cache) {
+        a.ck = cache->k;
+        a.cv = cache->v;
+        a.slots = slots;
+        a.page_shift = log2_of(cache->page_size);
+        a.n_pages = cache->n_pages;
+    }
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_qk_norm_rope(a, dtype, head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+sffn_status sffn_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int T, int n_heads, int n_kv_heads, int head_dim,
+                             const int32_t *cu_seqlens, int n_seq, float scale, void *out, void *workspace,
+                             size_t ws_bytes, sffn_stream_t stream) {
+    sffn_status st = check_heads(n_heads, n_kv_heads, head_dim);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > (1 << 20) || n_seq < 1 || n_seq > kPromptMaxSeq) return SFFN_ERR_SHAPE;
+    if (!(scale > 0.f) || std::isinf(scale)) return SFFN_ERR_INVALID_ARG;
+    if (T == 0) return SFFN_OK;
+    if (!q || !k || !v || !cu_seqlens || !out) return SFFN_ERR_INVALID_ARG;
+    if ((st = check_rows(q, q_stride, n_heads, head_dim, 2)) != SFFN_OK) return st;
+    if ((st = check_rows(k, k_stride, n_kv_heads, head_dim, 2)) != SFFN_OK) return st;
+    if ((st = check_rows(v, v_stride, n_kv_heads, head_dim, 2)) != SFFN_OK) return st;
+    if (!aligned16(out)) return SFFN_ERR_ALIGNMENT;
+    st = check_ws(workspace, ws_bytes, kAlign);
+    if (st != SFFN_OK) return st;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    PromptArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.T = T;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.group = n_heads / n_kv_heads;
+    a.cu_seqlens = cu_seqlens;
+    a.n_seq = n_seq;
+    a.scale = scale;
+    a.out = out;
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_attn_prompt(a, head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                           const int32_t *page_table, int table_width, const int32_t *ctx_lens,
+                           const int32_t *cu_tokens, int n_seq, const uint64_t *tree_mask, float scale, void *out,
+                           void *workspace, size_t ws_bytes, sffn_stream_t stream) {
+    if (!cache) return SFFN_ERR_INVALID_ARG;
+    sffn_status st = check_heads(n_heads, cache->n_kv_heads, cache->head_dim);
+    if (st != SFFN_OK) return st;
+    if (cache->dtype != SFFN_F32 && cache->dtype != SFFN_BF16) return SFFN_ERR_INVALID_ARG;
+    st = check_cache(cache, cache->dtype, cache->n_kv_heads, cache->head_dim);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > kTreeMaxT || n_seq < 1 || n_seq > kTreeMaxSeq || table_width < 1) return SFFN_ERR_SHAPE;
+    if (!(scale > 0.f) || std::isinf(scale)) return SFFN_ERR_INVALID_ARG;
+    if (T == 0) return SFFN_OK;
+    if (!q || !page_table || !ctx_lens || !cu_tokens || !out) return SFFN_ERR_INVALID_ARG;
+    st = check_rows(q, q_stride, n_heads, cache->head_dim, cache->dtype == SFFN_BF16 ? 2 : 4);
+    if (st != SFFN_OK) return st;
+    if (!aligned16(out)) return SFFN_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return SFFN_ERR_ALIGNMENT;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    TreePlan p = make_tree_plan(T, n_heads, cache->n_kv_heads, cache->head_dim);
+    st = check_ws(workspace, ws_bytes, p.total);
+    if (st != SFFN_OK) return st;
+    TreeArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.n_heads = n_heads;
+    a.n_kv_heads = cache->n_kv_heads;
+    a.group = n_heads / cache->n_kv_heads;
+    a.ck = cache->k;
+    a.cv = cache->v;
+    a.page_shift = log2_of(cache->page_size);
+    a.n_pages = cache->n_pages;
+    a.page_table = page_table;
+    a.table_width = table_width;
+    a.ctx_lens = ctx_lens;
+    a.cu_tokens = cu_tokens;
+    a.n_seq = n_seq;
+    a.tree_mask = tree_mask;
+    a.scale = scale;
+    a.out = out;
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
+    a.tile_tokens = p.tile_tokens;
+    a.rows_max = p.rows_max;
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_attn_tree(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
     return st;
 }

@@ -148,4 +148,63 @@ PrefillPlan make_prefill_plan(int L, int d, int F);
 sffn_status run_prefill(const void *x, const void *y_attn, int L, const sffn_ffn_weights *w, const int32_t *sel_idx,
                         const int32_t *n_sel, void *out, void *ws, const PrefillPlan &p, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Attention half of the layer
+// ---------------------------------------------------------------------------
+
+struct RopeArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;  // elements between tokens
+    const void *q_weight, *k_weight;
+    float eps;
+    const float *table;                      // [max_pos, rot]: cos | sin
+    int rot, max_pos, style;
+    const int32_t *positions;
+    int T, hq, hkv;
+    void *q_out, *k_out;
+    void *ck, *cv;                           // cache (null: none)
+    const int32_t *slots;
+    int page_shift, n_pages;
+    int32_t *err;
+};
+sffn_status run_qk_norm_rope(const RopeArgs &a, int dtype, int head_dim, cudaStream_t s);
+
+struct PromptArgs {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    int T, n_heads, n_kv_heads, group;
+    const int32_t *cu_seqlens;
+    int n_seq;
+    float scale;
+    void *out;
+    int32_t *err;
+};
+sffn_status run_attn_prompt(const PromptArgs &a, int head_dim, cudaStream_t s);
+
+constexpr int kTreeMaxSeq = 1024;  // sequences of one sffn_attn_tree call
+struct TreeArgs {
+    const void *q;
+    long long q_stride;
+    int T, n_heads, n_kv_heads, group;
+    const void *ck, *cv;
+    int page_shift, n_pages;
+    const int32_t *page_table;
+    int table_width;
+    const int32_t *ctx_lens, *cu_tokens;
+    int n_seq;
+    const uint64_t *tree_mask;
+    float scale;
+    void *out;
+    float *part;       // partial results of cut items
+    int tile_tokens;   // new tokens of a row tile
+    int rows_max;      // rows of a partial result slot
+    int32_t *err;
+};
+struct TreePlan {
+    int grid, tile_tokens, rows_max;
+    size_t off_part, total;
+};
+TreePlan make_tree_plan(int T, int n_heads, int n_kv_heads, int head_dim);
+sffn_status run_attn_tree(const TreeArgs &a, const TreePlan &p, int dtype, int head_dim, cudaStream_t s);
+
 }  // namespace sffn

@@ -26,6 +26,8 @@ WS_DECODE, WS_SELECT, WS_PREFILL = 0, 1, 2
 PRESET_SPEED, PRESET_BALANCED, PRESET_QUALITY, PRESET_DENSE = 0, 1, 2, 3
 _PRESET = {"speed": PRESET_SPEED, "balanced": PRESET_BALANCED, "quality": PRESET_QUALITY, "dense": PRESET_DENSE}
 NOALLOC_SCRATCH_BYTES = 4 << 20
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+WS_QK_NORM_ROPE, WS_ATTN_PROMPT, WS_ATTN_TREE = 0, 1, 2
 
 _WDTYPE = {"f32": F32, "bf16": BF16, "int4_g64": INT4_G64}
 _ACT = {"relu": ACT_RELU, "silu": ACT_SILU}
@@ -50,6 +52,11 @@ class FFNSchedule(C.Structure):
 
     def as_dict(self) -> dict:
         return {k: getattr(self, k) for k, _ in self._fields_}
+
+
+class KVCacheStruct(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+                ("n_pages", C.c_int32), ("k", C.c_void_p), ("v", C.c_void_p)]
 
 
 _lib = None
@@ -110,6 +117,16 @@ def lib():
         L.sffn_prefill_layers_workspace_size.restype = S
         L.sffn_prefill_layers.argtypes = [P, C.POINTER(C.c_void_p), I, I, W, SP, I, P, P, P, P, S, P]
         L.sffn_prefill_layers.restype = I
+        I64, KV = C.c_int64, C.POINTER(KVCacheStruct)
+        L.sffn_attn_workspace_size.argtypes = [I, I, I, I, I, I]
+        L.sffn_attn_workspace_size.restype = S
+        L.sffn_qk_norm_rope.argtypes = [I, P, I64, P, I64, P, I64, I, I, I, I, P, P, F, P, I, I, I, P, P, P, KV, P, P,
+                                        S, P]
+        L.sffn_qk_norm_rope.restype = I
+        L.sffn_attn_prompt.argtypes = [P, I64, P, I64, P, I64, I, I, I, I, P, I, F, P, P, S, P]
+        L.sffn_attn_prompt.restype = I
+        L.sffn_attn_tree.argtypes = [P, I64, I, I, KV, P, I, P, P, I, P, F, P, P, S, P]
+        L.sffn_attn_tree.restype = I
         _lib = L
     return _lib
 
@@ -435,3 +452,153 @@ def prefill_layers(x: torch.Tensor, y_attn: list, weights: list, s: FFNSchedule,
                                    _ptr(n_sel), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "sffn_prefill_layers")
     return out, sel_idx, n_sel
+
+
+# ---- the attention half of the layer ----
+
+_TDTYPE = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _need(ok: bool, status: int, where: str):
+    if not ok:
+        raise SffnError(status, where)
+
+
+def _rows(t: torch.Tensor, where: str) -> int:
+    """Token stride of a [T, heads, head_dim] tensor or view; its heads must be contiguous."""
+    _need(t.dim() == 3 and t.is_cuda and (t.shape[0] == 0 or (t.stride(2) == 1 and t.stride(1) == t.shape[2])),
+          ERR_INVALID_ARG, where)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _vec(t, n: int, dtype, where: str):
+    """A contiguous device array of n (or more) elements of one type, or None."""
+    _need(t is None or (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= n), ERR_INVALID_ARG, where)
+
+
+class KVCache:
+    """A paged key/value cache: k and v [n_pages, n_kv_heads, page_size, head_dim], fp32
+    or bf16, contiguous.  Keeps the tensors alive and the C struct."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in _TDTYPE and k.is_cuda
+              and v.is_cuda and k.is_contiguous() and v.is_contiguous(), ERR_INVALID_ARG, "KVCache")
+        self.k, self.v = k, v
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
+        self.c = KVCacheStruct(_TDTYPE[k.dtype], self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
+                               _ptr(k), _ptr(v))
+
+    def ref(self):
+        return C.byref(self.c)
+
+
+def attn_workspace_size(which: int, T: int, n_seq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(lib().sffn_attn_workspace_size(int(which), int(T), int(n_seq), int(n_heads), int(n_kv_heads),
+                                              int(head_dim)))
+
+
+def alloc_attn_workspace(which: int, T: int, n_seq: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                         device=None) -> torch.Tensor:
+    nbytes = attn_workspace_size(which, T, n_seq, n_heads, n_kv_heads, head_dim)
+    if nbytes == 0:
+        raise SffnError(ERR_SHAPE, "sffn_attn_workspace_size")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos | sin [max_pos, rot_dim] fp32 of the angles p * base^(-2 i / rot_dim), made in 64 bits."""
+    inv = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)
+    ang = torch.arange(max_pos, dtype=torch.float64)[:, None] * inv[None, :]
+    return torch.cat([ang.cos(), ang.sin()], dim=1).float().to(device)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v, table, positions, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, style: int = ROPE_HALF, cache: KVCache | None = None, slots=None, q_out=None,
+                 k_out=None, workspace=None, stream=None):
+    """Head norms and rotation of q [T, n_heads, D] and k [T, n_kv_heads, D] (views of a fused
+    projection are fine); with a cache, k and v rows go to their slots.  table [max_pos, rot_dim]
+    (see rope_table; None: no rotation).  Returns (q_out, k_out); k_out is None when the
+    keys go to the cache only (a cache and no k_out given)."""
+    T, hq, D = q.shape
+    hkv = k.shape[1]
+    where = "sffn_qk_norm_rope"
+    qs, ks = _rows(q, where), _rows(k, where)
+    vs = 0 if v is None else _rows(v, where)
+    dt = q.dtype
+    _need(dt in _TDTYPE and k.dtype == dt and (v is None or v.dtype == dt), ERR_INVALID_ARG, where)
+    _need(k.shape[0] == T and k.shape[2] == D and (v is None or v.shape == k.shape), ERR_SHAPE, where)
+    _vec(q_weight, D, dt, where)
+    _vec(k_weight, D, dt, where)
+    _vec(positions, T, torch.int32, where)
+    _vec(slots, T, torch.int32, where)
+    max_pos = rot = 0
+    if table is not None:
+        _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.is_cuda,
+              ERR_INVALID_ARG, where)
+        max_pos, rot = table.shape
+    if q_out is None:
+        q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+    if k_out is None and cache is None:
+        k_out = torch.empty((T, hkv, D), dtype=dt, device=q.device)
+    _vec(q_out, T * hq * D, dt, where)
+    _vec(k_out, T * hkv * D, dt, where)
+    if workspace is None:
+        workspace = alloc_attn_workspace(WS_QK_NORM_ROPE, T, 1, hq, hkv, D, q.device)
+    st = lib().sffn_qk_norm_rope(_TDTYPE[dt], _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, hq, hkv, D, _ptr(q_weight),
+                                 _ptr(k_weight), float(eps), _ptr(table), rot, max_pos, int(style), _ptr(positions),
+                                 _ptr(q_out), _ptr(k_out), None if cache is None else cache.ref(), _ptr(slots),
+                                 _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, where)
+    return q_out, k_out
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, scale=None, out=None,
+                workspace=None, stream=None):
+    """Causal attention over packed prompts: q [T, n_heads, D], k and v [T, n_kv_heads, D] bf16
+    (views of a fused projection are fine), cu_seqlens int32 [n_seq + 1].  Returns out [T, n_heads, D]."""
+    where = "sffn_attn_prompt"
+    T, hq, D = q.shape
+    hkv = k.shape[1]
+    qs, ks, vs = _rows(q, where), _rows(k, where), _rows(v, where)
+    _need(q.dtype == k.dtype == v.dtype == torch.bfloat16, ERR_UNSUPPORTED, where)
+    _need(k.shape == v.shape and k.shape[0] == T and k.shape[2] == D, ERR_SHAPE, where)
+    _vec(cu_seqlens, 2, torch.int32, where)
+    n_seq = cu_seqlens.numel() - 1
+    if out is None:
+        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    _vec(out, T * hq * D, q.dtype, where)
+    if workspace is None:
+        workspace = alloc_attn_workspace(WS_ATTN_PROMPT, T, n_seq, hq, hkv, D, q.device)
+    st = lib().sffn_attn_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, hq, hkv, D, _ptr(cu_seqlens), n_seq,
+                                float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(workspace),
+                                workspace.numel(), _stream(stream))
+    _check(st, where)
+    return out
+
+
+def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_lens: torch.Tensor,
+              cu_tokens: torch.Tensor, tree_mask=None, scale=None, out=None, workspace=None, stream=None):
+    """Attention of each sequence's new tokens (at most 64; one: plain decode) over its paged
+    context and the new tokens of tree_mask (int64 bit sets [T]; None: a chain).
+    q [T, n_heads, D], page_table int32 [n_seq, width], ctx_lens int32 [n_seq], cu_tokens int32
+    [n_seq + 1].  Returns out [T, n_heads, D]."""
+    where = "sffn_attn_tree"
+    T, hq, D = q.shape
+    qs = _rows(q, where)
+    _need(q.dtype == cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
+    _need(page_table.dim() == 2 and page_table.is_contiguous() and page_table.dtype == torch.int32
+          and page_table.is_cuda, ERR_INVALID_ARG, where)
+    n_seq, width = page_table.shape
+    _vec(ctx_lens, n_seq, torch.int32, where)
+    _vec(cu_tokens, n_seq + 1, torch.int32, where)
+    _vec(tree_mask, T, torch.int64, where)
+    if out is None:
+        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    _vec(out, T * hq * D, q.dtype, where)
+    if workspace is None:
+        workspace = alloc_attn_workspace(WS_ATTN_TREE, T, n_seq, hq, cache.n_kv_heads, D, q.device)
+    st = lib().sffn_attn_tree(_ptr(q), qs, T, hq, cache.ref(), _ptr(page_table), width, _ptr(ctx_lens),
+                              _ptr(cu_tokens), n_seq, _ptr(tree_mask), float(D ** -0.5 if scale is None else scale),
+                              _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(st, where)
+    return out

@@ -378,6 +378,121 @@ sffn_status sffn_prefill_layers(const void *x, const void *const *y_attn, int L,
                                 void *out, int32_t *sel_idx, int32_t *n_sel, void *workspace,
                                 size_t ws_bytes, sffn_stream_t stream);
 
+/* ---- The attention half of the layer ----
+ *
+ * The FFN calls take a layer's attention output; these calls make it.
+ *   sffn_qk_norm_rope  norms queries and keys per head, rotates them by position
+ *                      and writes keys and values into a paged cache, in one pass;
+ *   sffn_attn_prompt   causal attention over packed prompts (its rows, after the
+ *                      output projection, are sffn_token_select's y_attn);
+ *   sffn_attn_tree     attention of a few drafted tokens of each sequence (one:
+ *                      the plain decode step) over the paged cache.
+ * Query head h reads key/value head h / (n_heads / n_kv_heads).  head_dim is 64 or
+ * 128; n_kv_heads divides n_heads, n_heads <= 1024, n_heads / n_kv_heads <= 64.
+ * Q, K and V rows may be views of one fused projection: a tensor's heads are
+ * contiguous ([head, head_dim]) and its tokens lie `stride` elements apart
+ * (stride >= heads * head_dim, stride * element size a multiple of 16 bytes).
+ * Outputs are contiguous [T, heads, head_dim], in the inputs' type. */
+
+/* A paged key/value cache.  Host struct holding device pointers.  A logical
+ * position p of a sequence lives in page page_table[p / page_size] of that
+ * sequence's row, at offset p % page_size; a slot is page * page_size + offset. */
+typedef struct {
+    int32_t dtype;      /* SFFN_F32 or SFFN_BF16                                      */
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t page_size;  /* tokens per page: a power of two, 8 .. 65536                */
+    int32_t n_pages;    /* n_pages * n_kv_heads * page_size < 2^31                    */
+    void *k;            /* [n_pages, n_kv_heads, page_size, head_dim]                 */
+    void *v;            /* same shape                                                 */
+} sffn_kv_cache;
+
+typedef enum {
+    SFFN_ROPE_HALF = 0,       /* pairs (i, i + rot_dim / 2)  */
+    SFFN_ROPE_INTERLEAVED = 1 /* pairs (2 i, 2 i + 1)        */
+} sffn_rope_style;
+
+/* Bytes of workspace of the three calls.  which: 0 = sffn_qk_norm_rope,
+ * 1 = sffn_attn_prompt, 2 = sffn_attn_tree; T tokens of n_seq sequences (n_seq is
+ * ignored for 0).  Returns 0 for an invalid request.  The size depends on the
+ * device's SM count (current device).  The workspace's control block is the
+ * library's common one: zero-filled once, errors read with sffn_read_device_error. */
+size_t sffn_attn_workspace_size(int which, int T, int n_seq, int n_heads, int n_kv_heads, int head_dim);
+
+/* Per-head RMS norm and position rotation of T tokens' queries and keys, and the
+ * cache's new rows, in one pass.  For each head row x of q and k:
+ *   y = x * w / sqrt(mean(x^2) + eps)     (no weight given: y = x)
+ *   for each pair (a, b) of the first rot_dim elements, i its index, p the position:
+ *     (y_a cos_i(p) - y_b sin_i(p),  y_b cos_i(p) + y_a sin_i(p));
+ * elements from rot_dim on are not rotated.  32-bit arithmetic, one rounding.
+ *   dtype       SFFN_F32 or SFFN_BF16: type of q, k, v, the weights and the outputs.
+ *   q, k, v     device, token strides q_stride, k_stride, v_stride in elements.  v
+ *               goes to the cache as it is; NULL without a cache.
+ *   q_weight, k_weight  [head_dim], or NULL (that tensor is not normed).  eps >= 0.
+ *   table       fp32 [max_pos, rot_dim]: row p holds cos_i(p), then sin_i(p), for i in
+ *               [0, rot_dim / 2).  rot_dim: a multiple of 16, <= head_dim, or 0 (no
+ *               rotation: table and positions may be NULL).
+ *   positions   int32 [T], device.  A token whose position is outside [0, max_pos) is
+ *               skipped (none of its rows is written) and recorded (SFFN_ERR_DEVICE).
+ *   q_out       [T, n_heads, head_dim]; may be q itself if q is contiguous.
+ *   k_out       [T, n_kv_heads, head_dim], may be k itself likewise; NULL with a cache:
+ *               keys go to the cache only.
+ *   cache, slots  the paged cache (same dtype, n_kv_heads and head_dim) and int32 [T]
+ *               slots; or both NULL.  Slot -1: that token is not cached.  Other slots
+ *               outside the cache are skipped and recorded.  Slots are distinct.
+ * 0 <= T <= 1048576; T = 0 is a no-op. */
+sffn_status sffn_qk_norm_rope(int dtype, const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const void *v, int64_t v_stride, int T, int n_heads, int n_kv_heads, int head_dim,
+                              const void *q_weight, const void *k_weight, float eps, const float *table, int rot_dim,
+                              int max_pos, int style, const int32_t *positions, void *q_out, void *k_out,
+                              const sffn_kv_cache *cache, const int32_t *slots, void *workspace, size_t ws_bytes,
+                              sffn_stream_t stream);
+
+/* Causal attention over n_seq packed prompts, bf16:
+ *   out_i = sum_{j <= i} softmax_j(scale * q_i . k_j) v_j   within each sequence.
+ *   cu_seqlens  int32 [n_seq + 1], device: sequence s is rows cu_seqlens[s] ..
+ *               cu_seqlens[s + 1] - 1 of the T packed rows; ascending, from 0 to T
+ *               (empty sequences are fine).  A sequence outside [0, T] or of negative
+ *               length is skipped and recorded (SFFN_ERR_DEVICE).
+ *   scale       finite, > 0 (usually 1 / sqrt(head_dim)).
+ *   out         [T, n_heads, head_dim]; not one of the inputs.
+ * Scores, the softmax's sums and the output accumulate in 32 bits; the weights
+ * enter the second product as bf16.  Rows of other sequences and later rows of the
+ * same one have no influence, whatever they hold (infinities and NaN included).
+ * 0 <= T <= 1048576 (0: a no-op), 1 <= n_seq <= 65536. */
+sffn_status sffn_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, int T, int n_heads, int n_kv_heads, int head_dim,
+                             const int32_t *cu_seqlens, int n_seq, float scale, void *out, void *workspace,
+                             size_t ws_bytes, sffn_stream_t stream);
+
+/* Attention of drafted tokens over the paged cache; with one token per sequence,
+ * the plain decode step.  Sequence s has ctx_lens[s] committed tokens at logical
+ * positions 0 .. ctx - 1 and its new tokens cu_tokens[s] .. cu_tokens[s + 1] - 1 (64
+ * at most) at positions ctx, ctx + 1, ...; all their keys and values are in the
+ * cache already (sffn_qk_norm_rope).  A new token sees every committed position
+ * and the new tokens of its mask.
+ *   q           [T, n_heads, head_dim] in the cache's dtype, token stride q_stride.
+ *   page_table  int32 [n_seq, table_width], device.
+ *   ctx_lens    int32 [n_seq], device.  cu_tokens  int32 [n_seq + 1], device, from 0
+ *               to T.
+ *   tree_mask   uint64 [T], device: bit j of token i = it sees new token j of its
+ *               sequence (the token itself and its ancestors in a draft tree, say);
+ *               bits from the number of new tokens on are ignored.  NULL: a chain
+ *               (j <= i).  A token that sees nothing at all gets a row of zeros.
+ *   scale       finite, > 0.
+ *   out         [T, n_heads, head_dim].
+ * A sequence with a negative ctx_lens, more than 64 new tokens, tokens outside [0, T]
+ * or more positions than its table's row holds is skipped (its rows are not
+ * written) and recorded (SFFN_ERR_DEVICE); a page outside the cache reads as zeros
+ * and is recorded.  Cache contents that a token does not see have no influence,
+ * whatever they hold.  The split of the work over the device depends on the lengths
+ * alone: equal calls give equal bits.
+ * 0 <= T <= 65536 (0: a no-op), 1 <= n_seq <= 1024, 1 <= table_width. */
+sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                           const int32_t *page_table, int table_width, const int32_t *ctx_lens,
+                           const int32_t *cu_tokens, int n_seq, const uint64_t *tree_mask, float scale, void *out,
+                           void *workspace, size_t ws_bytes, sffn_stream_t stream);
+
 /* Copy the workspace's device error word to *code (host) and clear it; waits
  * for `stream`.  0 = no error; otherwise an sffn_status value. */
 sffn_status sffn_read_device_error(void *workspace, int32_t *code, sffn_stream_t stream);
