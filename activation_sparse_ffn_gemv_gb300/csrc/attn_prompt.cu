@@ -1,68 +1,191 @@
-// attn_prompt.cu -- causal attention over packed prompts (sm_103a).
-#include "attn_rows.cuh"
+// attn_prompt.cu -- causal attention over packed prompts (sm_103a): attn_tc.cuh over
+// contiguous keys.
+//
+// Bound: the tensor cores for long prompts (4 D operations a visible (query, key)
+// pair), latency for short ones.
+//
+// Work.  An item is 2 TB tokens (TB = 128 / G) of one sequence with every query head
+// of one key head; it runs over the keys up to its last token.  The longest items go
+// first: a sequence's tokens form blocks 0, 1, ... of growing cost, and the items are
+// taken by falling block number over all sequences, dealt to the CTAs in turn,
+// forwards and backwards alternately (two successive rounds cancel the difference
+// between the first and the last CTA of a round).  The order needs no sort: the number of
+// blocks at or above a number is known from the lengths, and a warp walks down the
+// distinct block counts (PromptPolicy::next).
+#include "attn_tc.cuh"
 
 namespace sffn {
 
 namespace {
 
-// One CTA: a row tile (64 / G tokens, every query head of a key head) of one sequence.
 template <int D>
-__global__ void __launch_bounds__(rows::kThreads, 1) k_prompt_rows(const PromptArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    rows::Smem<D> &sm = *reinterpret_cast<rows::Smem<D> *>(smem_raw);
-    typedef __nv_bfloat16 T;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int G = a.group, TT = rows::kRows / G;
-    const int h = blockIdx.y;
-    // tile number -> sequence (a walk: this is the plain kernel)
-    int left = blockIdx.x, t0 = 0, n = 0, s = 0;
-    for (; s < a.n_seq; ++s) {
+struct PromptPolicy {
+    const PromptArgs &a;
+    int G, TB;
+    // A warp's place: blocks [nxt, top] of the `cnt` sequences that have them; `before` pairs
+    // (sequence, block) come ahead of this stretch.
+    struct Walk {
+        long long before;
+        int round, top, nxt, cnt;
+    };
+
+    SFFN_DEV PromptPolicy(const PromptArgs &args) : a(args), G(args.group), TB(128 / args.group) {}
+
+    SFFN_DEV void seq(int s, int &t0, int &n) const {
         t0 = a.cu_seqlens[s];
-        n = a.cu_seqlens[s + 1] - t0;
-        if (t0 < 0 || n < 0 || t0 + n > a.T) {
-            if (h == 0 && threadIdx.x == 0) record_error(a.err, SFFN_ERR_DEVICE);
+        const int t1 = a.cu_seqlens[s + 1];
+        n = t1 - t0;
+        if (t0 < 0 || t1 > a.T || t1 < t0) {
+            if (blockIdx.x == 0) record_error(a.err, SFFN_ERR_DEVICE);
             n = 0;
         }
-        const int tiles = (n + TT - 1) / TT;
-        if (left < tiles) break;
-        left -= tiles;
     }
-    if (s == a.n_seq) return;
-    const int i0 = left * TT, nt = min(TT, n - i0);
-    rows::Acc<D> acc;
-    rows::attend<T, D>(
-        sm, acc, nt * G, 0, i0 + nt, a.scale,
-        [&](int r) {
-            return static_cast<const T *>(a.q) + (size_t)(t0 + i0 + r / G) * a.q_stride + (size_t)(h * G + r % G) * D;
-        },
-        [&](long long j, int which) -> const T * {
-            return which ? static_cast<const T *>(a.v) + (size_t)(t0 + j) * a.v_stride + (size_t)h * D
-                         : static_cast<const T *>(a.k) + (size_t)(t0 + j) * a.k_stride + (size_t)h * D;
-        },
-        [&](int r, long long j) { return j <= i0 + r / G; });
-    const int tid = threadIdx.x, c = (tid % rows::Acc<D>::CT) * 4, g = tid / rows::Acc<D>::CT;
+    SFFN_DEV int blocks(int s) const {
+        int t0, n;
+        seq(s, t0, n);
+        return (n + 2 * TB - 1) / (2 * TB);
+    }
+    // Sequences with `limit` blocks or more, and the largest count below it.
+    SFFN_DEV void stretch(int limit, int &cnt, int &nxt) const {
+        int above = 0, below = 0;
+        for (int s = threadIdx.x & 31; s < a.n_seq; s += 32) {
+            const int b = blocks(s);
+            if (b >= limit) ++above;
+            else below = max(below, b);
+        }
+        cnt = __reduce_add_sync(0xffffffffu, above);
+        nxt = __reduce_max_sync(0xffffffffu, below);
+    }
+    SFFN_DEV void start(Walk &k) const {
+        int cnt, nxt;
+        stretch(0x7fffffff, cnt, nxt);  // nxt: the largest count
+        const int top = nxt - 1;
+        if (top >= 0) stretch(top + 1, cnt, nxt);
+        k.before = 0;
+        k.round = 0;
+        k.top = top;
+        k.nxt = nxt;
+        k.cnt = cnt;
+    }
+    SFFN_DEV bool next(atc::Work &w, Walk &k) const {
+        const int W = gridDim.x, round = k.round;
+        const long long idx = (long long)round * W + ((round & 1) ? W - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        const long long pair = idx / a.n_kv_heads;
+        long long before = k.before;
+        int top = k.top, nxt = k.nxt, cnt = k.cnt;
+        __syncwarp();
+        while (top >= 0 && pair >= before + (long long)cnt * (top - nxt + 1)) {
+            before += (long long)cnt * (top - nxt + 1);
+            top = nxt - 1;
+            if (top >= 0) stretch(top + 1, cnt, nxt);
+        }
+        k.before = before;
+        k.round = round + 1;
+        k.top = top;
+        k.nxt = nxt;
+        k.cnt = cnt;
+        if (top < 0) return false;
+        const long long off = pair - before;
+        const int block = top - (int)(off / cnt);
+        int rank = (int)(off % cnt);
+        // the rank-th sequence that has this block
+        const int lane = threadIdx.x & 31;
+        int s = 0;
+        for (int s0 = 0; s0 < a.n_seq; s0 += 32) {
+            const bool has = s0 + lane < a.n_seq && blocks(s0 + lane) > top;
+            uint32_t m = __ballot_sync(0xffffffffu, has);
+            const int n = __popc(m);
+            if (rank < n) {
+                while (rank--) m &= m - 1;
+                s = s0 + __ffs(m) - 1;
+                break;
+            }
+            rank -= n;
+        }
+        int t0, n;
+        seq(s, t0, n);
+        const int i0 = block * 2 * TB, nt = min(2 * TB, n - i0), k1 = i0 + nt;
+        w.h = (int)(idx - pair * a.n_kv_heads);
+        w.i0 = i0;
+        w.base = t0;
+        w.q_row = t0 + i0;
+        w.nt = nt;
+        w.k0 = 0;
+        w.k1 = k1;
+        w.exist = n;
+        w.n[0] = (min(i0 + TB, n) + atc::kKeys - 1) / atc::kKeys;
+        w.n[1] = nt > TB ? (k1 + atc::kKeys - 1) / atc::kKeys : 0;
+        w.mask_from[0] = (i0 + 1) / atc::kKeys;
+        w.mask_from[1] = (i0 + TB + 1) / atc::kKeys;
+        return true;
+    }
+    SFFN_DEV void load_kv(const atc::Work &w, int j, const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int lane,
+                          uint64_t pol) const {
+        if (lane != 0) return;
+        mbar_arrive_expect_tx(bar, atc::Cfg<D>::kTile);
+        for (int c = 0; c < atc::Cfg<D>::kHalves; ++c)
+            tc::tma_load_3d(dst + c * atc::Cfg<D>::kBlock, map, c * 64, w.h, w.base + j * atc::kKeys, bar, pol);
+    }
+
+    struct RowInfo {
+        int pos;        // the row's position
+        float inv;
+        uint16_t *dst;
+    };
+    SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const { return RowInfo{w.i0 + tok, 0.f, nullptr}; }
+    SFFN_DEV void visible(const atc::Work &, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
+        const int n = r.pos + 1 - j * atc::kKeys;
 #pragma unroll
-    for (int i = 0; i < rows::Acc<D>::RPT; ++i) {
-        const int r = g + i * rows::Acc<D>::RG;
-        if (r < nt * G) {
-            const float inv = 1.f / sm.l[r];
-            const float4 o = acc.o[i];
-            rows::store4<T>(static_cast<T *>(a.out) +
-                                ((size_t)(t0 + i0 + r / G) * a.n_heads + (size_t)(h * G + r % G)) * D + c,
-                            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        for (int i = 0; i < 4; ++i) vis[i] = atc::low_bits(n - 32 * i);
+    }
+    SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &r, int key) const {
+        if (key > r.pos) return nullptr;
+        return static_cast<const uint16_t *>(a.v) + (size_t)(w.base + key) * a.v_stride + (size_t)w.h * D;
+    }
+    SFFN_DEV void begin_row(const atc::Work &w, RowInfo &r, int tok, int head, bool valid, float, float l) const {
+        r.inv = 1.f / l;
+        r.dst = static_cast<uint16_t *>(a.out) +
+                (valid ? ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D : 0);
+    }
+    SFFN_DEV void store(const atc::Work &, const RowInfo &r, int q, const uint32_t (&o)[32]) const {
+        uint4 *dst = reinterpret_cast<uint4 *>(r.dst + q * 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                p[e] = atc::pack_bf16(__uint_as_float(o[i * 8 + 2 * e]) * r.inv, __uint_as_float(o[i * 8 + 2 * e + 1]) * r.inv);
+            dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
         }
     }
+};
+
+template <int D>
+__global__ void __launch_bounds__(atc::kThreads, 1)
+    k_attn_prompt(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    PromptPolicy<D> policy(a);
+    atc::attention_cta<D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
 }
 
 template <int D>
 sffn_status launch_prompt(const PromptArgs &a, cudaStream_t s) {
-    const int TT = rows::kRows / a.group;
-    const long long tiles = (long long)a.T / TT + a.n_seq;  // at most: a partial tile per sequence
-    cudaError_t e = set_max_smem((const void *)k_prompt_rows<D>, (int)sizeof(rows::Smem<D>));
+    const int G = a.group, TB = 128 / G;
+    CUtensorMap mq, mk, mv;
+    const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, dk[3] = {D, (uint64_t)a.n_kv_heads, (uint64_t)a.T};
+    const uint64_t sq[2] = {D * 2, (uint64_t)a.q_stride * 2}, sk[2] = {D * 2, (uint64_t)a.k_stride * 2},
+                   sv[2] = {D * 2, (uint64_t)a.v_stride * 2};
+    const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[3] = {64, 1, atc::kKeys};
+    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.k, 3, dk, sk, bk) ||
+        !make_map_bf16(&mv, a.v, 3, dk, sv, bk))
+        return SFFN_ERR_UNSUPPORTED;
+    // at most one partial block per sequence
+    const long long items = ((long long)a.T / (2 * TB) + a.n_seq) * a.n_kv_heads;
+    const int grid = (int)(items < device_sm_count() ? items : device_sm_count());
+    cudaError_t e = set_max_smem((const void *)k_attn_prompt<D>, atc::Cfg<D>::kSmem);
     if (e == cudaSuccess)
-        e = launch_k(k_prompt_rows<D>, dim3((unsigned)tiles, a.n_kv_heads), dim3(rows::kThreads),
-                     sizeof(rows::Smem<D>), s, a);
+        e = launch_k(k_attn_prompt<D>, dim3(grid), dim3(atc::kThreads), atc::Cfg<D>::kSmem, s, mq, mk, mv, a);
     return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
 }
 

@@ -1,0 +1,415 @@
+// attn_tc.cuh -- softmax attention of bf16 queries on the tensor cores (tcgen05,
+// TMEM, TMA), shared by the packed prompts and the paged cache.
+//
+//   o_i = sum_j w_ij v_j / sum_j w_ij,  w_ij = exp(scale q_i . k_j - m_i)
+//
+// for any m_i that keeps the exponentials in range; the running maximum is used and
+// moved only when a row's scores pass it by more than 2^8, so the accumulator is
+// rarely rescaled (the sums stay exact in either case: both carry the same m_i).
+//
+// Rows.  The G query heads of a key head read the same keys, so a row is a (token,
+// query head) pair and a 128-row tile holds TB = 128 / G tokens (one TMA box of TB
+// tokens x G heads x 64 elements lays them out as rows).  An item has two such tiles.
+//
+// One CTA per SM, ten warps, no CTA-wide barrier between items:
+//   warp 0      loads: queries, then the ring of 128-key K and V tiles
+//   warp 1      issues the tcgen05.mma: S_t = Q_t K^T into TMEM (fp32), later O_t += P_t V
+//   warps 2-5   softmax of tile 0: a thread owns a row; S_t from TMEM, weights P_t (bf16)
+//   warps 6-9   softmax of tile 1  back to TMEM over S_t, where the second product reads
+//               them as its A operand; at the end O_t / sum to global memory
+// While one tile's softmax runs, the tensor cores work on the other tile.
+//
+// A weight of zero times an infinite or NaN value would be NaN, so in a tile with
+// masked keys the softmax warps look through V in shared memory before the second
+// product: non-finite elements become zero, and where they belong to existing keys the
+// rows that do see them get them added at the end (fix_row).  Rows that do not see
+// them come out bit for bit as without them.
+#pragma once
+
+#include "attn.cuh"
+#include "tcgen05.cuh"
+
+namespace sffn {
+namespace atc {
+
+constexpr int kThreads = 320;
+constexpr int kKeys = 128;                   // keys of a tile
+constexpr float kLazyLog2 = 8.f;             // the running maximum moves when passed by 2^8
+
+template <int D>
+struct Cfg {
+    static constexpr int kHalves = D / 64;                      // 64-element (128-byte) column blocks
+    static constexpr int kBlock = 128 * 128;                    // bytes of a column block: 128 rows x 128 bytes
+    static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
+    static constexpr int kStages = D == 128 ? 5 : 10;           // K and V tiles of the ring
+    static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
+    static constexpr int kSmem = (2 + kStages) * kTile + 1024 /*alignment*/;
+};
+
+// One item, the same for every warp.
+struct Work {
+    int q_row;          // first token (row of q and out)
+    int nt;             // tokens
+    int h;              // key head
+    int n[2];           // key tiles of each row tile
+    int mask_from[2];   // first of them with masked keys
+    int k0, k1;         // keys [k0, k1) (logical positions)
+    int exist;          // keys below this one exist
+    int i0;             // prompt: position of the first token
+    int base;           // prompt: row of key 0
+    int ctx;            // tree: committed positions
+    int seq, tok0;      // tree: sequence, first token of the item within its new tokens
+    bool whole;         // tree: the item's every key (else a partial result)
+    int slot;           // tree: partial result slot
+};
+
+SFFN_DEV float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+SFFN_DEV uint32_t pack_bf16(float lo, float hi) {
+    __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&p);
+}
+
+// The bf16 halves of w that are infinite or NaN (their sign bits), as a mask of 0x8000s.
+SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+// Low 32 bits with the first n set (n clamped to 0 .. 32).
+SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
+
+// P: the policy (prompts or tree).  It gives
+//   bool next(Work &, Walk &)  the CTA's items in turn, the same in every warp; each warp
+//                          keeps its item and its place in shared memory (the softmax
+//                          warps need their registers for a row's 128 scores)
+//   load_q / load_kv       the producer's loads
+//   visible words, value rows, the epilogue's destination (see attn_prompt.cu / attn_tree.cu)
+template <int D, typename P>
+SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
+                            float scale, int G, int32_t *err, unsigned char *smem_raw) {
+    using C = Cfg<D>;
+    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char *sm_q = sm, *sm_kv = sm + 2 * C::kTile;
+    constexpr int NS = C::kStages;
+    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], mdone;
+    __shared__ uint32_t tmem_slot;
+    __shared__ volatile int s_abort, s_bad;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) mbar_init(&kv_full[i], 1), mbar_init(&kv_empty[i], 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 1);
+            mbar_init(&q_empty[t], 1);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_ready[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(&mdone, 1);
+        s_abort = 0;
+        s_bad = 0;
+        mbar_fence_init();
+        tc::prefetch_tensormap(&map_q);
+        tc::prefetch_tensormap(&map_k);
+        tc::prefetch_tensormap(&map_v);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(&tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = tmem_slot;
+
+    // Bounded wait of a whole warp; false: the kernel gives up.
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        const bool ok = mbar_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ok && !s_abort)) return true;
+        if (!ok && lane == 0) {
+            s_abort = 1;
+            record_error(err, SFFN_ERR_TIMEOUT);
+        }
+        return false;
+    };
+
+    griddep_wait();
+    const int TB = 128 / G;
+    __shared__ Work s_work[kThreads / 32];
+    __shared__ typename P::Walk s_walk[kThreads / 32];
+    Work &w = s_work[warp];
+    typename P::Walk &walk = s_walk[warp];
+    policy.start(walk);
+    griddep_launch_dependents();
+    // the next item; the warp's lanes agree on it before and after
+    auto next = [&]() -> bool {
+        __syncwarp();
+        const bool more = policy.next(w, walk);
+        __syncwarp();
+        return more;
+    };
+
+    if (warp == 0) {
+        // ---------------- loads ----------------
+        int it = 0, qn[2] = {0, 0};
+        bool run = true;
+        const uint64_t keep = tc::l2_evict_last_policy();
+        while (run && next()) {
+            const int nmax = max(w.n[0], w.n[1]);
+            for (int j = 0; j < nmax && run; ++j) {
+                for (int part = 0; part < 2 && run; ++part) {
+                    // the item's queries: tile 0 before the first K, tile 1 after it
+                    if (j == 0 && w.n[part] > 0) {
+                        if (!(run = wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1)))) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
+                            for (int c = 0; c < C::kHalves; ++c)
+                                tc::tma_load_3d(sm_q + part * C::kTile + c * C::kBlock, &map_q, c * 64, w.h * G,
+                                                w.q_row + part * TB, &q_full[part], keep);
+                        }
+                        ++qn[part];
+                    }
+                    const int s = it % NS;
+                    if (!(run = wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1)))) break;
+                    policy.load_kv(w, j, part ? &map_v : &map_k, sm_kv + s * C::kTile, &kv_full[s], lane, keep);
+                    ++it;
+                }
+            }
+        }
+        if (!run && lane == 0) {  // let the copies in flight land before the CTA can exit
+            for (int j = max(0, it - NS); j < it; ++j) mbar_wait(&kv_full[j % NS], (uint32_t)((j / NS) & 1));
+            for (int t = 0; t < 2; ++t)
+                if (qn[t]) mbar_wait(&q_full[t], (uint32_t)((qn[t] - 1) & 1));
+        }
+    } else if (warp == 1) {
+        // ---------------- tensor cores ----------------
+        constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
+        constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
+        int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
+        bool run = true;
+        const uint32_t q_addr = smem_u32(sm_q), kv_addr = smem_u32(sm_kv);
+        auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
+            if (lane != 0) return;
+            const uint32_t a = q_addr + t * C::kTile, b = kv_addr + slot * C::kTile;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * C::kBlock + (kk & 3) * 32;
+                tc::mma_bf16(tmem + t * 128, tc::smem_desc_sw128(a + off, 16, 1024), tc::smem_desc_sw128(b + off, 16, 1024),
+                             idesc_s, kk != 0);
+            }
+            tc::mma_commit(&s_full[t]);
+        };
+        auto values = [&](int t, int slot, bool acc) {  // O_t (+)= P_t V
+            if (lane != 0) return;
+            const uint32_t b = kv_addr + slot * C::kTile;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc::mma_bf16_ts(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8,
+                                tc::smem_desc_sw128(b + kk * 2048, C::kBlock, 1024), idesc_o, acc || kk != 0);
+        };
+        while (run && next()) {
+            const int nmax = max(w.n[0], w.n[1]);
+            auto k_wait = [&](int j) {
+                const int i = base + 2 * j;
+                const bool ok = wait(&kv_full[i % NS], (uint32_t)((i / NS) & 1));
+                tc::fence_after_sync();
+                return ok;
+            };
+            auto k_slot = [&](int j) { return (base + 2 * j) % NS; };
+            if (!(run = k_wait(0))) break;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (w.n[t] > 0 && run) {
+                    if (!(run = wait(&q_full[t], (uint32_t)(qn[t] & 1)))) break;
+                    ++qn[t];
+                    tc::fence_after_sync();
+                    scores(t, k_slot(0));
+                    if (w.n[t] == 1 && lane == 0) tc::mma_commit(&q_empty[t]);
+                }
+            }
+            if (!run) break;
+            if (lane == 0) tc::mma_commit(&kv_empty[k_slot(0)]);
+            for (int j = 0; j < nmax && run; ++j) {
+                const int iv = base + 2 * j + 1, vs = iv % NS;
+                if (!(run = wait(&kv_full[vs], (uint32_t)((iv / NS) & 1)))) break;
+                if (j + 1 < nmax && !(run = k_wait(j + 1))) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (j < w.n[t] && run) {
+                        if (!(run = wait(&p_ready[t], (uint32_t)(pn[t] & 1)))) break;
+                        ++pn[t];
+                        tc::fence_after_sync();
+                        values(t, vs, j > 0);
+                        if (j + 1 == w.n[t] && lane == 0) tc::mma_commit(&o_full[t]);
+                    }
+                    if (t == 1 && lane == 0) tc::mma_commit(&kv_empty[vs]);
+                    if (j + 1 < w.n[t] && run) {
+                        scores(t, k_slot(j + 1));
+                        if (j + 2 == w.n[t] && lane == 0) tc::mma_commit(&q_empty[t]);
+                    }
+                }
+                if (j + 1 < nmax && lane == 0) tc::mma_commit(&kv_empty[k_slot(j + 1)]);
+            }
+            base += 2 * nmax;
+        }
+        // every product of this CTA has completed before teardown
+        if (lane == 0) {
+            tc::mma_commit(&mdone);
+            mbar_wait(&mdone, 0);
+        }
+    } else {
+        // ---------------- softmax of row tile t ----------------
+        const int t = (warp - 2) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const int tok = row / G, head = row - tok * G;  // token of the tile, query head of the group
+        const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + t * 128;
+        const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
+        const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
+        int sn = 0, on = 0, base = 0;
+        bool run = true;
+        while (run && next()) {
+            const int n = w.n[t], nmax = max(w.n[0], w.n[1]);
+            const int item_tok = t * TB + tok;          // token of the item
+            const bool valid = tok < TB && item_tok < w.nt;
+            typename P::RowInfo ri = policy.row_info(w, valid ? item_tok : 0);
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n && run; ++j) {
+                const bool masked = j >= w.mask_from[t];
+                if (masked) {
+                    // non-finite values of this tile: zero (and noted, if their keys exist)
+                    const int iv = base + 2 * j + 1, vs = iv % NS;
+                    if (!(run = wait(&kv_full[vs], (uint32_t)((iv / NS) & 1)))) break;
+                    uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
+                    const int kb = w.k0 + j * kKeys;
+                    for (int i = tid - 64 - t * 128; i < C::kTile / 16; i += 128) {
+                        uint4 x = v[i];
+                        const uint32_t b0 = nonfinite_bits(x.x), b1 = nonfinite_bits(x.y), b2 = nonfinite_bits(x.z),
+                                       b3 = nonfinite_bits(x.w);
+                        if (b0 | b1 | b2 | b3) {
+                            if (kb + ((i >> 3) & 127) < w.exist) {
+                                s_bad = 1;
+                                __threadfence_block();
+                            }
+                            // (bit >> 15) * 0xffff: the whole half
+                            x.x &= ~((b0 >> 15) * 0xffffu);
+                            x.y &= ~((b1 >> 15) * 0xffffu);
+                            x.z &= ~((b2 >> 15) * 0xffffu);
+                            x.w &= ~((b3 >> 15) * 0xffffu);
+                            v[i] = x;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!(run = wait(&s_full[t], (uint32_t)(sn & 1)))) break;
+                ++sn;
+                tc::fence_after_sync();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + q * 32, s[q]);
+                tc::tmem_wait_ld();
+                if (masked) {
+                    uint32_t vis[4];
+                    policy.visible(w, ri, j, vis);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s[q][i] = (vis[q] >> i) & 1u ? s[q][i] : 0xff800000u;  // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                    for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                }
+                const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const bool up = (mnew - m) * c > kLazyLog2;
+                if (__any_sync(0xffffffffu, up)) {
+                    const float alpha = up ? ex2((m - mnew) * c) : 1.f;
+                    if (up) m = mnew;
+                    l *= alpha;
+                    if (j > 0) {
+                        // the product of tile j - 1 is complete: it was issued before S_t(j)
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            tc::tmem_ld16(to + q * 16, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tc::tmem_st16(to + q * 16, o);
+                        }
+                    }
+                }
+                const float mc = (m == -INFINITY ? 0.f : m) * c;  // nothing seen yet: every weight is 2^-inf = 0
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float e0 = ex2(fmaf(__uint_as_float(s[q][2 * i]), c, -mc));
+                        const float e1 = ex2(fmaf(__uint_as_float(s[q][2 * i + 1]), c, -mc));
+                        sum[i & 1] += e0;
+                        sum[2 + (i & 1)] += e1;
+                        p[i] = pack_bf16(e0, e1);
+                    }
+                    tc::tmem_st16(ts + q * 16, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[t]);
+            }
+            if (run && n > 0) {
+                if (!(run = wait(&o_full[t], (uint32_t)(on & 1)))) break;
+                ++on;
+                tc::fence_after_sync();
+                const bool bad = s_bad != 0;
+                policy.begin_row(w, ri, item_tok, head, valid, m, l);
+#pragma unroll 1
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(to + q * 32, o);
+                    tc::tmem_wait_ld();
+                    if (valid) {
+                        if (bad) {
+                            // the masked tiles' non-finite values that this row sees
+                            const int from = w.k0 + min(w.mask_from[0], w.mask_from[1]) * kKeys;
+                            for (int key = from; key < w.k1; ++key) {
+                                const uint4 *vr = reinterpret_cast<const uint4 *>(policy.value_row(w, ri, key));
+                                if (!vr) continue;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint4 x = vr[q * 4 + i];
+                                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const uint32_t nb = nonfinite_bits(xs[e]);
+                                        uint32_t &lo = o[i * 8 + e * 2], &hi = o[i * 8 + e * 2 + 1];
+                                        if (nb & 0x8000u) lo = __float_as_uint(__uint_as_float(lo) + bf16lo(xs[e]));
+                                        if (nb & 0x80000000u) hi = __float_as_uint(__uint_as_float(hi) + bf16hi(xs[e]));
+                                    }
+                                }
+                            }
+                        }
+                        policy.store(w, ri, q, o);
+                    }
+                }
+                tc::fence_before_sync();  // O_t has been read: the next item's product may overwrite it
+            }
+            base += 2 * nmax;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace atc
+}  // namespace sffn
