@@ -470,7 +470,10 @@ size_t sffn_attn_workspace_size(int which, int T, int n_seq, int n_heads, int n_
     if (which == 1) return n_seq < 1 || n_seq > kPromptMaxSeq ? 0 : kAlign;
     if (which == 2) {
         if (T > kTreeMaxT || n_seq < 1 || n_seq > kTreeMaxSeq || device_sm_count() <= 0) return 0;
-        return make_tree_plan(T, n_heads, n_kv_heads, head_dim).total;
+        // either type's
+        const size_t b = make_tree_plan(SFFN_BF16, T, n_heads, n_kv_heads, head_dim).total,
+                     f = make_tree_plan(SFFN_F32, T, n_heads, n_kv_heads, head_dim).total;
+        return b > f ? b : f;
     }
     return 0;
 }
@@ -595,7 +598,7 @@ sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, 
     if (!aligned16(out)) return SFFN_ERR_ALIGNMENT;
     if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return SFFN_ERR_ALIGNMENT;
     if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
-    TreePlan p = make_tree_plan(T, n_heads, cache->n_kv_heads, cache->head_dim);
+    TreePlan p = make_tree_plan(cache->dtype, T, n_heads, cache->n_kv_heads, cache->head_dim);
     st = check_ws(workspace, ws_bytes, p.total);
     if (st != SFFN_OK) return st;
     TreeArgs a = {};

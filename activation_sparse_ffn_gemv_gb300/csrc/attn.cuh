@@ -22,6 +22,7 @@ namespace sffn {
 
 constexpr int kTreeUnit = 64;
 constexpr int kTreeMaxTokens = 64;
+constexpr int kTreeMaxCtx = 0x7fff0000;  // positions stay below 2^31 with room for a tile
 
 struct TreeSeq {
     int t0, n, ctx;   // first new token, new tokens, committed positions
@@ -36,7 +37,7 @@ SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
     q.ctx = a.ctx_lens[s];
     const long long n = (long long)t1 - q.t0;
     const bool ok = q.t0 >= 0 && t1 <= a.T && n >= 0 && n <= kTreeMaxTokens && q.ctx >= 0 &&
-                    q.ctx + n <= ((long long)a.table_width << a.page_shift);
+                    q.ctx + n <= ((long long)a.table_width << a.page_shift) && q.ctx <= kTreeMaxCtx;
     if (!ok) {
         if (record) record_error(a.err, SFFN_ERR_DEVICE);
         q.t0 = q.n = q.ctx = q.tiles = q.units = 0;

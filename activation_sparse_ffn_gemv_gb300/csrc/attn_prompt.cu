@@ -19,6 +19,9 @@ namespace sffn {
 namespace {
 
 template <int D>
+using Cfg = atc::Cfg<D, D == 128 ? 5 : 10>;  // all of the shared memory: 227 KB
+
+template <int D>
 struct PromptPolicy {
     const PromptArgs &a;
     int G, TB;
@@ -122,9 +125,9 @@ struct PromptPolicy {
     SFFN_DEV void load_kv(const atc::Work &w, int j, const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int lane,
                           uint64_t pol) const {
         if (lane != 0) return;
-        mbar_arrive_expect_tx(bar, atc::Cfg<D>::kTile);
-        for (int c = 0; c < atc::Cfg<D>::kHalves; ++c)
-            tc::tma_load_3d(dst + c * atc::Cfg<D>::kBlock, map, c * 64, w.h, w.base + j * atc::kKeys, bar, pol);
+        mbar_arrive_expect_tx(bar, Cfg<D>::kTile);
+        for (int c = 0; c < Cfg<D>::kHalves; ++c)
+            tc::tma_load_3d(dst + c * Cfg<D>::kBlock, map, c * 64, w.h, w.base + j * atc::kKeys, bar, pol);
     }
 
     struct RowInfo {
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
     extern __shared__ unsigned char smem_raw[];
     PromptPolicy<D> policy(a);
-    atc::attention_cta<D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
+    atc::attention_cta<D, Cfg<D>::kStages>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
 }
 
 template <int D>
@@ -183,9 +186,9 @@ sffn_status launch_prompt(const PromptArgs &a, cudaStream_t s) {
     // at most one partial block per sequence
     const long long items = ((long long)a.T / (2 * TB) + a.n_seq) * a.n_kv_heads;
     const int grid = (int)(items < device_sm_count() ? items : device_sm_count());
-    cudaError_t e = set_max_smem((const void *)k_attn_prompt<D>, atc::Cfg<D>::kSmem);
+    cudaError_t e = set_max_smem((const void *)k_attn_prompt<D>, Cfg<D>::kSmem);
     if (e == cudaSuccess)
-        e = launch_k(k_attn_prompt<D>, dim3(grid), dim3(atc::kThreads), atc::Cfg<D>::kSmem, s, mq, mk, mv, a);
+        e = launch_k(k_attn_prompt<D>, dim3(grid), dim3(atc::kThreads), Cfg<D>::kSmem, s, mq, mk, mv, a);
     return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
 }
 

@@ -36,12 +36,12 @@ constexpr int kThreads = 320;
 constexpr int kKeys = 128;                   // keys of a tile
 constexpr float kLazyLog2 = 8.f;             // the running maximum moves when passed by 2^8
 
-template <int D>
+template <int D, int STAGES>
 struct Cfg {
     static constexpr int kHalves = D / 64;                      // 64-element (128-byte) column blocks
     static constexpr int kBlock = 128 * 128;                    // bytes of a column block: 128 rows x 128 bytes
     static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
-    static constexpr int kStages = D == 128 ? 5 : 10;           // K and V tiles of the ring
+    static constexpr int kStages = STAGES;                      // K and V tiles of the ring
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
     static constexpr int kSmem = (2 + kStages) * kTile + 1024 /*alignment*/;
 };
@@ -86,10 +86,10 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 //                          warps need their registers for a row's 128 scores)
 //   load_q / load_kv       the producer's loads
 //   visible words, value rows, the epilogue's destination (see attn_prompt.cu / attn_tree.cu)
-template <int D, typename P>
+template <int D, int STAGES, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                             float scale, int G, int32_t *err, unsigned char *smem_raw) {
-    using C = Cfg<D>;
+    using C = Cfg<D, STAGES>;
     unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *sm_q = sm, *sm_kv = sm + 2 * C::kTile;
     constexpr int NS = C::kStages;

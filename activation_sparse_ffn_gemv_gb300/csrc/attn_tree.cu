@@ -4,6 +4,7 @@
 // Bound: HBM, the cached keys and values, each read once for all the new tokens and
 // all the query heads that share them.
 #include "attn_rows.cuh"
+#include "attn_tc.cuh"
 
 namespace sffn {
 
@@ -84,6 +85,158 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
     }
 }
 
+// ---------------------------------------------------------------------------
+// bf16: attn_tc.cuh over the paged cache
+// ---------------------------------------------------------------------------
+
+template <int D>
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8>;
+
+template <int D>
+struct TreePolicy {
+    const TreeArgs &a;
+    long long *pre;         // units before each sequence (shared memory)
+    long long u1;           // end of this CTA's units
+    int G, TB, box;         // box: cache rows of one copy (a page's, 64 at most)
+
+    struct Walk {
+        long long u;
+    };
+    struct RowInfo {
+        uint64_t mask;
+        float inv;
+        void *dst;
+    };
+
+    long long *scratch;
+
+    SFFN_DEV TreePolicy(const TreeArgs &args, long long *prefix, long long *scan)
+        : a(args), pre(prefix), G(args.group), TB(128 / args.group), box(min(64, 1 << args.page_shift)), scratch(scan) {}
+
+    SFFN_DEV void start(Walk &k) {
+        tree_prefix(a, pre, scratch, blockIdx.x == 0);
+        const long long total = pre[a.n_seq];
+        const int W = tree_ctas(total, gridDim.x), b = blockIdx.x;
+        k.u = b < W ? tree_cut(total, b, W) : 0;
+        u1 = b < W ? tree_cut(total, b + 1, W) : 0;
+    }
+    SFFN_DEV bool next(atc::Work &w, Walk &k) const {
+        const long long u = k.u;
+        if (u >= u1) return false;
+        const int s = tree_find(pre, a.n_seq, u);
+        const TreeSeq q = tree_seq(a, s, false);
+        const long long local = u - pre[s];
+        const int item = (int)(local / q.units), un0 = (int)(local - (long long)item * q.units);
+        const int un1 = (int)min((long long)q.units, un0 + (u1 - u));
+        const int tile = item / a.n_kv_heads, tk0 = tile * a.tile_tokens;
+        const int k0 = un0 * kTreeUnit, k1 = min(q.ctx + q.n, un1 * kTreeUnit);
+        const int n = (k1 - k0 + atc::kKeys - 1) / atc::kKeys;
+        __syncwarp();
+        k.u = u + (un1 - un0);
+        w.h = item - tile * a.n_kv_heads;
+        w.q_row = q.t0 + tk0;
+        w.nt = min(a.tile_tokens, q.n - tk0);
+        w.k0 = k0;
+        w.k1 = w.exist = k1;
+        w.n[0] = n;
+        w.n[1] = w.nt > TB ? n : 0;
+        w.mask_from[0] = w.mask_from[1] = max(0, min(q.ctx, k1) - k0) / atc::kKeys;
+        w.ctx = q.ctx;
+        w.seq = s;
+        w.tok0 = tk0;
+        w.whole = un0 == 0 && un1 == q.units;
+        w.slot = 2 * blockIdx.x + (un0 > 0 ? 0 : 1);
+        return true;
+    }
+    // Row of the cache (head h's) that holds key `key`; past the end if its page is not one.
+    SFFN_DEV long long cache_row(const atc::Work &w, int key) const {
+        const int pg = a.page_table[(size_t)w.seq * a.table_width + (key >> a.page_shift)];
+        if (pg < 0 || pg >= a.n_pages) {
+            record_error(a.err, SFFN_ERR_DEVICE);
+            return ((long long)a.n_pages * a.n_kv_heads) << a.page_shift;
+        }
+        return (((long long)pg * a.n_kv_heads + w.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
+    }
+    SFFN_DEV void load_kv(const atc::Work &w, int j, const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int lane,
+                          uint64_t pol) const {
+        constexpr int H = Cfg<D>::kHalves;
+        const int kb = w.k0 + j * atc::kKeys, left = min(atc::kKeys, w.k1 - kb);
+        const int boxes = (left + box - 1) / box, b = lane / H, c = lane % H;  // boxes <= 16
+        int row = 0;
+        if (b < boxes) row = (int)cache_row(w, kb + b * box);
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * H));
+        __syncwarp();
+        if (b < boxes) tc::tma_load_2d(dst + c * Cfg<D>::kBlock + b * box * 128, map, c * 64, row, bar, pol);
+    }
+    SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
+        const int i = w.tok0 + tok;
+        const uint64_t m = a.tree_mask ? a.tree_mask[w.q_row + tok] : (i == 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
+        return RowInfo{m, 0.f, nullptr};
+    }
+    SFFN_DEV void visible(const atc::Work &w, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
+        const int kb = w.k0 + j * atc::kKeys;
+        const int all = min(w.ctx, w.k1) - kb, end = w.k1 - kb, d0 = kb - w.ctx;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int sh = d0 + 32 * i;  // new token of the word's first key
+            uint32_t bits = 0;
+            if (sh >= 0 && sh < 64) bits = (uint32_t)(r.mask >> sh);
+            else if (sh < 0 && sh > -32) bits = (uint32_t)(r.mask << -sh);
+            vis[i] = atc::low_bits(all - 32 * i) | (bits & atc::low_bits(end - 32 * i));
+        }
+    }
+    SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &r, int key) const {
+        if (key >= w.ctx && !((r.mask >> (key - w.ctx)) & 1)) return nullptr;
+        const long long row = cache_row(w, key);
+        if (row >= ((long long)a.n_pages * a.n_kv_heads) << a.page_shift) return nullptr;
+        return static_cast<const uint16_t *>(a.cv) + (size_t)row * D;
+    }
+    SFFN_DEV void begin_row(const atc::Work &w, RowInfo &r, int tok, int head, bool valid, float m, float l) const {
+        if (!valid) return;
+        if (w.whole) {
+            r.inv = l == 0.f ? 0.f : 1.f / l;
+            r.dst = static_cast<uint16_t *>(a.out) +
+                    ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D;
+        } else {
+            float *slot = a.part + tree_slot_floats(a.rows_max, D) * (size_t)w.slot;
+            const int row = tok * G + head;
+            r.dst = slot + (size_t)row * D;
+            *reinterpret_cast<float2 *>(slot + (size_t)a.rows_max * D + 2 * row) = make_float2(m * a.scale, l);
+        }
+    }
+    SFFN_DEV void store(const atc::Work &w, const RowInfo &r, int q, const uint32_t (&o)[32]) const {
+        if (w.whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(r.dst) + q * 32);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    p[e] = atc::pack_bf16(__uint_as_float(o[i * 8 + 2 * e]) * r.inv,
+                                          __uint_as_float(o[i * 8 + 2 * e + 1]) * r.inv);
+                dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(r.dst) + q * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+    }
+};
+
+constexpr size_t kPrefixBytes = (kTreeMaxSeq + 1) * sizeof(long long);
+
+template <int D>
+__global__ void __launch_bounds__(atc::kThreads, 1)
+    k_tree_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v, const TreeArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __shared__ long long scratch[33];
+    TreePolicy<D> policy(a, reinterpret_cast<long long *>(smem_raw), scratch);
+    atc::attention_cta<D, Cfg<D>::kStages>(policy, map_q, map_k, map_v, a.scale, a.group, a.err,
+                                           smem_raw + kPrefixBytes);
+}
+
 // Joins the pieces of cut items: for each row, M = max of the pieces' maxima,
 // out = sum(exp(m_i - M) o_i) / sum(exp(m_i - M) l_i), the pieces in the order of
 // their CTAs.  One warp a row (token, query head).
@@ -143,26 +296,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_tree_join(const TreeArgs a,
 }
 
 template <typename T, int D>
-sffn_status launch_tree(const TreeArgs &a, int W, cudaStream_t s) {
-    const size_t pre = (size_t)(a.n_seq + 1) * sizeof(long long);
-    const size_t smem = sizeof(rows::Smem<D>) + pre;
-    cudaError_t e = set_max_smem((const void *)k_tree_rows<T, D>, (int)(sizeof(rows::Smem<D>) + (kTreeMaxSeq + 1) * 8));
-    if (e == cudaSuccess) e = launch_k(k_tree_rows<T, D>, dim3(W), dim3(rows::kThreads), smem, s, a);
+cudaError_t launch_join(const TreeArgs &a, int grid, cudaStream_t s) {
     const long long rows = (long long)a.T * a.n_heads;
+    return launch_k(k_tree_join<T, D>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(32 * kJoinWarps),
+                    (size_t)(a.n_seq + 1) * sizeof(long long), s, a, grid);
+}
+
+template <int D>
+sffn_status launch_tree_f32(const TreeArgs &a, int grid, cudaStream_t s) {
+    cudaError_t e = set_max_smem((const void *)k_tree_rows<float, D>, (int)(sizeof(rows::Smem<D>) + kPrefixBytes));
     if (e == cudaSuccess)
-        e = launch_k(k_tree_join<T, D>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(32 * kJoinWarps),
-                     pre, s, a, W);
+        e = launch_k(k_tree_rows<float, D>, dim3(grid), dim3(rows::kThreads),
+                     sizeof(rows::Smem<D>) + (size_t)(a.n_seq + 1) * sizeof(long long), s, a);
+    if (e == cudaSuccess) e = launch_join<float, D>(a, grid, s);
+    return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
+}
+
+template <int D>
+sffn_status launch_tree_bf16(const TreeArgs &a, int grid, cudaStream_t s) {
+    const int G = a.group, TB = 128 / G, ps = 1 << a.page_shift;
+    CUtensorMap mq, mk, mv;
+    const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, sq[2] = {D * 2, (uint64_t)a.q_stride * 2};
+    const uint64_t dk[2] = {D, (uint64_t)a.n_pages * a.n_kv_heads * ps}, sk[1] = {D * 2};
+    const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[2] = {64, (uint32_t)(ps < 64 ? ps : 64)};
+    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 2, dk, sk, bk) ||
+        !make_map_bf16(&mv, a.cv, 2, dk, sk, bk))
+        return SFFN_ERR_UNSUPPORTED;
+    constexpr int smem = Cfg<D>::kSmem + (int)kPrefixBytes;
+    cudaError_t e = set_max_smem((const void *)k_tree_tc<D>, smem);
+    if (e == cudaSuccess) e = launch_k(k_tree_tc<D>, dim3(grid), dim3(atc::kThreads), smem, s, mq, mk, mv, a);
+    if (e == cudaSuccess) e = launch_join<__nv_bfloat16, D>(a, grid, s);
     return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
 }
 
 }  // namespace
 
-TreePlan make_tree_plan(int T, int n_heads, int n_kv_heads, int head_dim) {
+TreePlan make_tree_plan(int dtype, int T, int n_heads, int n_kv_heads, int head_dim) {
     TreePlan p = {};
     const int G = n_heads / n_kv_heads;
     p.grid = device_sm_count();
-    p.tile_tokens = rows::kRows / G;
-    p.rows_max = (T < p.tile_tokens ? T : p.tile_tokens) * G;
+    p.tile_tokens = dtype == SFFN_BF16 ? 2 * (128 / G) : rows::kRows / G;
+    int tokens = T < kTreeMaxTokens ? T : kTreeMaxTokens;
+    if (tokens > p.tile_tokens) tokens = p.tile_tokens;
+    p.rows_max = tokens * G;
     size_t o = 0;
     o = align_up(o + kControlBytes);
     p.off_part = o;
@@ -173,9 +349,8 @@ TreePlan make_tree_plan(int T, int n_heads, int n_kv_heads, int head_dim) {
 
 sffn_status run_attn_tree(const TreeArgs &a, const TreePlan &p, int dtype, int head_dim, cudaStream_t s) {
     if (dtype == SFFN_BF16)
-        return head_dim == 128 ? launch_tree<__nv_bfloat16, 128>(a, p.grid, s)
-                               : launch_tree<__nv_bfloat16, 64>(a, p.grid, s);
-    return head_dim == 128 ? launch_tree<float, 128>(a, p.grid, s) : launch_tree<float, 64>(a, p.grid, s);
+        return head_dim == 128 ? launch_tree_bf16<128>(a, p.grid, s) : launch_tree_bf16<64>(a, p.grid, s);
+    return head_dim == 128 ? launch_tree_f32<128>(a, p.grid, s) : launch_tree_f32<64>(a, p.grid, s);
 }
 
 }  // namespace sffn

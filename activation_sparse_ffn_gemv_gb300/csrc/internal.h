@@ -204,7 +204,7 @@ struct TreePlan {
     int grid, tile_tokens, rows_max;
     size_t off_part, total;
 };
-TreePlan make_tree_plan(int T, int n_heads, int n_kv_heads, int head_dim);
+TreePlan make_tree_plan(int dtype, int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_tree(const TreeArgs &a, const TreePlan &p, int dtype, int head_dim, cudaStream_t s);
 
 }  // namespace sffn
