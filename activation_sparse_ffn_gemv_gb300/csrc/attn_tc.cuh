@@ -124,15 +124,25 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     tc::fence_after_sync();
     const uint32_t tmem = tmem_slot;
 
-    // Bounded wait of a whole warp; false: the kernel gives up.
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = mbar_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok && !s_abort)) return true;
-        if (!ok && lane == 0) {
-            s_abort = 1;
-            record_error(err, SFFN_ERR_TIMEOUT);
-        }
+    // Bounded wait of a whole warp, and of one thread; false: the kernel gives up.  The quick
+    // way is one try and one vote (the waits are on the path between the products).
+    auto give_up = [&]() -> bool {
+        s_abort = 1;
+        record_error(err, SFFN_ERR_TIMEOUT);
         return false;
+    };
+    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar, parity))
+            if (s_abort || globaltimer_ns() - t0 > kWaitLimitNs) return give_up();
+        return true;
+    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        bool ok = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if (!ok) ok = wait1(bar, parity);
+        return __all_sync(0xffffffffu, ok);
     };
 
     griddep_wait();
@@ -187,11 +197,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         // ---------------- tensor cores ----------------
         constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
         constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
-        int base = 0, qn[2] = {0, 0}, pn[2] = {0, 0};
-        bool run = true;
         const uint32_t q_addr = smem_u32(sm_q), kv_addr = smem_u32(sm_kv);
+        // one thread issues everything: no vote or shuffle between two products
         auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
-            if (lane != 0) return;
             const uint32_t a = q_addr + t * C::kTile, b = kv_addr + slot * C::kTile;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -202,57 +210,65 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             tc::mma_commit(&s_full[t]);
         };
         auto values = [&](int t, int slot, bool acc) {  // O_t (+)= P_t V
-            if (lane != 0) return;
             const uint32_t b = kv_addr + slot * C::kTile;
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
                 tc::mma_bf16_ts(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8,
                                 tc::smem_desc_sw128(b + kk * 2048, C::kBlock, 1024), idesc_o, acc || kk != 0);
         };
-        while (run && next()) {
-            const int nmax = max(w.n[0], w.n[1]);
-            auto k_wait = [&](int j) {
-                const int i = base + 2 * j;
-                const bool ok = wait(&kv_full[i % NS], (uint32_t)((i / NS) & 1));
-                tc::fence_after_sync();
-                return ok;
-            };
-            auto k_slot = [&](int j) { return (base + 2 * j) % NS; };
-            if (!(run = k_wait(0))) break;
+        int slot = 0;                                        // ring position and its parity
+        uint32_t par = 0, q_par[2] = {0, 0}, p_par[2] = {0, 0};
+        auto step = [&]() {
+            if (++slot == NS) slot = 0, par ^= 1;
+        };
+        auto item = [&](const int n0, const int n1) -> bool {
+            const int n[2] = {n0, n1}, nmax = max(n0, n1);
+            if (!wait1(&kv_full[slot], par)) return false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                if (w.n[t] > 0 && run) {
-                    if (!(run = wait(&q_full[t], (uint32_t)(qn[t] & 1)))) break;
-                    ++qn[t];
+                if (n[t] > 0) {
+                    if (!wait1(&q_full[t], q_par[t])) return false;
+                    q_par[t] ^= 1;
                     tc::fence_after_sync();
-                    scores(t, k_slot(0));
-                    if (w.n[t] == 1 && lane == 0) tc::mma_commit(&q_empty[t]);
+                    scores(t, slot);
+                    if (n[t] == 1) tc::mma_commit(&q_empty[t]);
                 }
             }
-            if (!run) break;
-            if (lane == 0) tc::mma_commit(&kv_empty[k_slot(0)]);
-            for (int j = 0; j < nmax && run; ++j) {
-                const int iv = base + 2 * j + 1, vs = iv % NS;
-                if (!(run = wait(&kv_full[vs], (uint32_t)((iv / NS) & 1)))) break;
-                if (j + 1 < nmax && !(run = k_wait(j + 1))) break;
+            tc::mma_commit(&kv_empty[slot]);
+            step();
+            for (int j = 0; j < nmax; ++j) {
+                const int vs = slot;
+                if (!wait1(&kv_full[vs], par)) return false;
+                step();
+                const bool more = j + 1 < nmax;
+                if (more && !wait1(&kv_full[slot], par)) return false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (j < w.n[t] && run) {
-                        if (!(run = wait(&p_ready[t], (uint32_t)(pn[t] & 1)))) break;
-                        ++pn[t];
+                    if (j < n[t]) {
+                        if (!wait1(&p_ready[t], p_par[t])) return false;
+                        p_par[t] ^= 1;
                         tc::fence_after_sync();
                         values(t, vs, j > 0);
-                        if (j + 1 == w.n[t] && lane == 0) tc::mma_commit(&o_full[t]);
+                        if (j + 1 == n[t]) tc::mma_commit(&o_full[t]);
                     }
-                    if (t == 1 && lane == 0) tc::mma_commit(&kv_empty[vs]);
-                    if (j + 1 < w.n[t] && run) {
-                        scores(t, k_slot(j + 1));
-                        if (j + 2 == w.n[t] && lane == 0) tc::mma_commit(&q_empty[t]);
+                    if (j + 1 < n[t]) {
+                        scores(t, slot);
+                        if (j + 2 == n[t]) tc::mma_commit(&q_empty[t]);
                     }
+                    if (t == 1) tc::mma_commit(&kv_empty[vs]);
                 }
-                if (j + 1 < nmax && lane == 0) tc::mma_commit(&kv_empty[k_slot(j + 1)]);
+                if (more) {
+                    tc::mma_commit(&kv_empty[slot]);
+                    step();
+                }
             }
-            base += 2 * nmax;
+            return true;
+        };
+        bool run = true;
+        while (run && next()) {
+            const int n0 = w.n[0], n1 = w.n[1];
+            if (lane == 0) run = item(n0, n1);
+            run = __shfl_sync(0xffffffffu, (int)run, 0) != 0;
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
