@@ -90,8 +90,8 @@ template <int D, int STAGES, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                             float scale, int G, int32_t *err, unsigned char *smem_raw) {
     using C = Cfg<D, STAGES>;
-    unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *sm_q = sm, *sm_kv = sm + 2 * C::kTile;
+    const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + 2 * C::kTile;
+    unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile;
     constexpr int NS = C::kStages;
     __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], mdone;
     __shared__ uint32_t tmem_slot;
@@ -122,7 +122,11 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    constexpr uint32_t tmem = 0;  // the CTA owns all 512 columns, so they start at 0
+    if (tid == 0 && tmem_slot != tmem) {
+        s_abort = 1;
+        record_error(err, SFFN_ERR_DEVICE);
+    }
 
     // Bounded wait of a whole warp, and of one thread; false: the kernel gives up.  The quick
     // way is one try and one vote (the waits are on the path between the products).
@@ -197,68 +201,68 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         // ---------------- tensor cores ----------------
         constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
         constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
-        const uint32_t q_addr = smem_u32(sm_q), kv_addr = smem_u32(sm_kv);
-        // one thread issues everything: no vote or shuffle between two products
-        auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
-            const uint32_t a = q_addr + t * C::kTile, b = kv_addr + slot * C::kTile;
+        // The whole warp runs this code, uniformly; one lane issues each instruction.
+        const uint64_t hi = tc::smem_desc_sw128(0, 16, 1024), hi_v = tc::smem_desc_sw128(0, C::kBlock, 1024);
+        auto scores = [&](int t, uint32_t tile) {  // S_t = Q_t K^T
+            const uint64_t a = hi | ((q_addr + t * C::kTile) >> 4), b = hi | (tile >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * C::kBlock + (kk & 3) * 32;
-                tc::mma_bf16(tmem + t * 128, tc::smem_desc_sw128(a + off, 16, 1024), tc::smem_desc_sw128(b + off, 16, 1024),
-                             idesc_s, kk != 0);
+                const uint32_t off = ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4;
+                tc::mma_bf16_warp(tmem + t * 128, a + off, b + off, idesc_s, kk != 0);
             }
-            tc::mma_commit(&s_full[t]);
+            tc::mma_commit_warp(&s_full[t]);
         };
-        auto values = [&](int t, int slot, bool acc) {  // O_t (+)= P_t V
-            const uint32_t b = kv_addr + slot * C::kTile;
+        auto values = [&](int t, uint32_t tile, bool acc) {  // O_t (+)= P_t V
+            const uint64_t b = hi_v | (tile >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc::mma_bf16_ts(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8,
-                                tc::smem_desc_sw128(b + kk * 2048, C::kBlock, 1024), idesc_o, acc || kk != 0);
+                tc::mma_bf16_ts_warp(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
+                                     acc || kk != 0);
         };
         int slot = 0;                                        // ring position and its parity
         uint32_t par = 0, q_par[2] = {0, 0}, p_par[2] = {0, 0};
         auto step = [&]() {
             if (++slot == NS) slot = 0, par ^= 1;
         };
+        auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
         auto item = [&](const int n0, const int n1) -> bool {
             const int n[2] = {n0, n1}, nmax = max(n0, n1);
-            if (!wait1(&kv_full[slot], par)) return false;
+            if (!wait(&kv_full[slot], par)) return false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (n[t] > 0) {
-                    if (!wait1(&q_full[t], q_par[t])) return false;
+                    if (!wait(&q_full[t], q_par[t])) return false;
                     q_par[t] ^= 1;
                     tc::fence_after_sync();
-                    scores(t, slot);
-                    if (n[t] == 1) tc::mma_commit(&q_empty[t]);
+                    scores(t, tile_of(slot));
+                    if (n[t] == 1) tc::mma_commit_warp(&q_empty[t]);
                 }
             }
-            tc::mma_commit(&kv_empty[slot]);
+            tc::mma_commit_warp(&kv_empty[slot]);
             step();
             for (int j = 0; j < nmax; ++j) {
                 const int vs = slot;
-                if (!wait1(&kv_full[vs], par)) return false;
+                if (!wait(&kv_full[vs], par)) return false;
                 step();
                 const bool more = j + 1 < nmax;
-                if (more && !wait1(&kv_full[slot], par)) return false;
+                if (more && !wait(&kv_full[slot], par)) return false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < n[t]) {
-                        if (!wait1(&p_ready[t], p_par[t])) return false;
+                        if (!wait(&p_ready[t], p_par[t])) return false;
                         p_par[t] ^= 1;
                         tc::fence_after_sync();
-                        values(t, vs, j > 0);
-                        if (j + 1 == n[t]) tc::mma_commit(&o_full[t]);
+                        values(t, tile_of(vs), j > 0);
+                        if (j + 1 == n[t]) tc::mma_commit_warp(&o_full[t]);
                     }
                     if (j + 1 < n[t]) {
-                        scores(t, slot);
-                        if (j + 2 == n[t]) tc::mma_commit(&q_empty[t]);
+                        scores(t, tile_of(slot));
+                        if (j + 2 == n[t]) tc::mma_commit_warp(&q_empty[t]);
                     }
-                    if (t == 1) tc::mma_commit(&kv_empty[vs]);
+                    if (t == 1) tc::mma_commit_warp(&kv_empty[vs]);
                 }
                 if (more) {
-                    tc::mma_commit(&kv_empty[slot]);
+                    tc::mma_commit_warp(&kv_empty[slot]);
                     step();
                 }
             }
@@ -266,9 +270,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         };
         bool run = true;
         while (run && next()) {
-            const int n0 = w.n[0], n1 = w.n[1];
-            if (lane == 0) run = item(n0, n1);
-            run = __shfl_sync(0xffffffffu, (int)run, 0) != 0;
+            // uniform by construction; the reductions tell the compiler so
+            const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
+            run = item(n0, n1);
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
