@@ -69,6 +69,24 @@ SFFN_DEV float ex2(float x) {
     return y;
 }
 
+// Two fp32 at a time: (a.x b.x + c.x, a.y b.y + c.y), and the sum.
+SFFN_DEV uint64_t f32x2(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+SFFN_DEV void split(uint64_t v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+SFFN_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SFFN_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 SFFN_DEV uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
@@ -93,7 +111,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + 2 * C::kTile;
     unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile;
     constexpr int NS = C::kStages;
-    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], mdone;
+    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
 
@@ -104,7 +122,8 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             mbar_init(&q_full[t], 1);
             mbar_init(&q_empty[t], 1);
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_ready[t], 4);
+            mbar_init(&p_ready[0][t], 4);  // [half of the tile's keys][row tile]
+            mbar_init(&p_ready[1][t], 4);
             mbar_init(&o_full[t], 1);
         }
         mbar_init(&mdone, 1);
@@ -128,25 +147,20 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         record_error(err, SFFN_ERR_DEVICE);
     }
 
-    // Bounded wait of a whole warp, and of one thread; false: the kernel gives up.  The quick
-    // way is one try and one vote (the waits are on the path between the products).
-    auto give_up = [&]() -> bool {
-        s_abort = 1;
-        record_error(err, SFFN_ERR_TIMEOUT);
-        return false;
-    };
-    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
+    // Bounded wait.  A wait that gives up records the error and goes on as if its phase had come (the
+    // results are not valid then), and every later wait passes at once: all loops still end,
+    // and a wait that is over costs one look and one branch, which counts between two products.
+    auto wait_slow = [&](uint64_t *bar, uint32_t parity) {
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar, parity))
-            if (s_abort || globaltimer_ns() - t0 > kWaitLimitNs) return give_up();
-        return true;
+        while (!mbar_try_wait(bar, parity) && !s_abort)
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                s_abort = 1;
+                record_error(err, SFFN_ERR_TIMEOUT);
+            }
     };
-    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        bool ok = mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if (!ok) ok = wait1(bar, parity);
-        return __all_sync(0xffffffffu, ok);
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity);
+        __syncwarp();
     };
 
     griddep_wait();
@@ -168,15 +182,14 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     if (warp == 0) {
         // ---------------- loads ----------------
         int it = 0, qn[2] = {0, 0};
-        bool run = true;
         const uint64_t keep = tc::l2_evict_last_policy();
-        while (run && next()) {
-            const int nmax = max(w.n[0], w.n[1]);
-            for (int j = 0; j < nmax && run; ++j) {
-                for (int part = 0; part < 2 && run; ++part) {
+        while (next()) {
+            const int n0 = w.n[0], n1 = w.n[1], nmax = max(n0, n1);
+            for (int j = 0; j < nmax; ++j) {
+                for (int part = 0; part < 2; ++part) {
                     // the item's queries: tile 0 before the first K, tile 1 after it
-                    if (j == 0 && w.n[part] > 0) {
-                        if (!(run = wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1)))) break;
+                    if (j == 0 && (part ? n1 : n0) > 0) {
+                        wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1));
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
                             for (int c = 0; c < C::kHalves; ++c)
@@ -186,13 +199,13 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         ++qn[part];
                     }
                     const int s = it % NS;
-                    if (!(run = wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1)))) break;
+                    wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1));
                     policy.load_kv(w, j, part ? &map_v : &map_k, sm_kv + s * C::kTile, &kv_full[s], lane, keep);
                     ++it;
                 }
             }
         }
-        if (!run && lane == 0) {  // let the copies in flight land before the CTA can exit
+        if (s_abort && lane == 0) {  // let the copies in flight land before the CTA can exit
             for (int j = max(0, it - NS); j < it; ++j) mbar_wait(&kv_full[j % NS], (uint32_t)((j / NS) & 1));
             for (int t = 0; t < 2; ++t)
                 if (qn[t]) mbar_wait(&q_full[t], (uint32_t)((qn[t] - 1) & 1));
@@ -212,10 +225,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             }
             tc::mma_commit_warp(&s_full[t]);
         };
-        auto values = [&](int t, uint32_t tile, bool acc) {  // O_t (+)= P_t V
+        auto values = [&](int t, int half, uint32_t tile, bool acc) {  // O_t (+)= P_t V over half of the keys
             const uint64_t b = hi_v | (tile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
+            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
                 tc::mma_bf16_ts_warp(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
                                      acc || kk != 0);
         };
@@ -225,54 +238,45 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (++slot == NS) slot = 0, par ^= 1;
         };
         auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
-        auto item = [&](const int n0, const int n1) -> bool {
-            const int n[2] = {n0, n1}, nmax = max(n0, n1);
-            if (!wait(&kv_full[slot], par)) return false;
+        // The ring's tiles are given back by the softmax warps, which see S_t(j) arrive after their last
+        // reader: no tcgen05.commit but the one per score product.
+        while (next()) {
+            // uniform by construction; the reductions tell the compiler so
+            const int n[2] = {__reduce_max_sync(0xffffffffu, w.n[0]), __reduce_max_sync(0xffffffffu, w.n[1])};
+            const int nmax = max(n[0], n[1]);
+            wait(&kv_full[slot], par);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 if (n[t] > 0) {
-                    if (!wait(&q_full[t], q_par[t])) return false;
+                    wait(&q_full[t], q_par[t]);
                     q_par[t] ^= 1;
                     tc::fence_after_sync();
                     scores(t, tile_of(slot));
-                    if (n[t] == 1) tc::mma_commit_warp(&q_empty[t]);
                 }
             }
-            tc::mma_commit_warp(&kv_empty[slot]);
             step();
             for (int j = 0; j < nmax; ++j) {
                 const int vs = slot;
-                if (!wait(&kv_full[vs], par)) return false;
+                wait(&kv_full[vs], par);
                 step();
                 const bool more = j + 1 < nmax;
-                if (more && !wait(&kv_full[slot], par)) return false;
+                if (more) wait(&kv_full[slot], par);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < n[t]) {
-                        if (!wait(&p_ready[t], p_par[t])) return false;
+                        wait(&p_ready[0][t], p_par[t]);
+                        tc::fence_after_sync();
+                        values(t, 0, tile_of(vs), j > 0);
+                        wait(&p_ready[1][t], p_par[t]);
                         p_par[t] ^= 1;
                         tc::fence_after_sync();
-                        values(t, tile_of(vs), j > 0);
+                        values(t, 1, tile_of(vs), true);
                         if (j + 1 == n[t]) tc::mma_commit_warp(&o_full[t]);
                     }
-                    if (j + 1 < n[t]) {
-                        scores(t, tile_of(slot));
-                        if (j + 2 == n[t]) tc::mma_commit_warp(&q_empty[t]);
-                    }
-                    if (t == 1) tc::mma_commit_warp(&kv_empty[vs]);
+                    if (j + 1 < n[t]) scores(t, tile_of(slot));
                 }
-                if (more) {
-                    tc::mma_commit_warp(&kv_empty[slot]);
-                    step();
-                }
+                if (more) step();
             }
-            return true;
-        };
-        bool run = true;
-        while (run && next()) {
-            // uniform by construction; the reductions tell the compiler so
-            const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
-            run = item(n0, n1);
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
@@ -288,19 +292,19 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
         int sn = 0, on = 0, base = 0;
-        bool run = true;
-        while (run && next()) {
+        while (next()) {
             const int n = w.n[t], nmax = max(w.n[0], w.n[1]);
             const int item_tok = t * TB + tok;          // token of the item
             const bool valid = tok < TB && item_tok < w.nt;
             typename P::RowInfo ri = policy.row_info(w, valid ? item_tok : 0);
+            const bool releases = t == (w.n[1] > 0 ? 1 : 0);
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < n && run; ++j) {
+            for (int j = 0; j < n; ++j) {
                 const bool masked = j >= w.mask_from[t];
                 if (masked) {
                     // non-finite values of this tile: zero (and noted, if their keys exist)
                     const int iv = base + 2 * j + 1, vs = iv % NS;
-                    if (!(run = wait(&kv_full[vs], (uint32_t)((iv / NS) & 1)))) break;
+                    wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
                     uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
                     const int kb = w.k0 + j * kKeys;
                     for (int i = tid - 64 - t * 128; i < C::kTile / 16; i += 128) {
@@ -322,8 +326,17 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     }
                     fence_proxy_async_smem();
                 }
-                if (!(run = wait(&s_full[t], (uint32_t)(sn & 1)))) break;
+                wait(&s_full[t], (uint32_t)(sn & 1));
                 ++sn;
+                if (lane == 0 && quad == 0) {
+                    // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
+                    // before it are, once the later row tile's products are through
+                    if (j + 1 == n) mbar_arrive(&q_empty[t]);
+                    if (releases) {
+                        mbar_arrive(&kv_empty[(base + 2 * j) % NS]);
+                        if (j > 0) mbar_arrive(&kv_empty[(base + 2 * j - 1) % NS]);
+                    }
+                }
                 tc::fence_after_sync();
                 uint32_t s[4][32];
 #pragma unroll
@@ -365,29 +378,36 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     }
                 }
                 const float mc = (m == -INFINITY ? 0.f : m) * c;  // nothing seen yet: every weight is 2^-inf = 0
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)),
+                               mc2 = f32x2(__float_as_uint(-mc), __float_as_uint(-mc));
+                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const float e0 = ex2(fmaf(__uint_as_float(s[q][2 * i]), c, -mc));
-                        const float e1 = ex2(fmaf(__uint_as_float(s[q][2 * i + 1]), c, -mc));
-                        sum[i & 1] += e0;
-                        sum[2 + (i & 1)] += e1;
+                        float x0, x1;
+                        split(fma2(f32x2(s[q][2 * i], s[q][2 * i + 1]), c2, mc2), x0, x1);
+                        const float e0 = ex2(x0), e1 = ex2(x1);
+                        sum[i & 1] = add2(sum[i & 1], f32x2(__float_as_uint(e0), __float_as_uint(e1)));
                         p[i] = pack_bf16(e0, e1);
                     }
                     tc::tmem_st16(ts + q * 16, p);
+                    if (q & 1) {  // the weights of 64 keys are there: their product may start
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_ready[q >> 1][t]);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tmem_wait_st();
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[t]);
+                float l0, l1;
+                split(add2(sum[0], sum[1]), l0, l1);
+                l += l0 + l1;
             }
-            if (run && n > 0) {
-                if (!(run = wait(&o_full[t], (uint32_t)(on & 1)))) break;
+            if (n > 0) {
+                wait(&o_full[t], (uint32_t)(on & 1));
                 ++on;
+                if (releases && lane == 0 && quad == 0) mbar_arrive(&kv_empty[(base + 2 * n - 1) % NS]);
                 tc::fence_after_sync();
                 const bool bad = s_bad != 0;
                 policy.begin_row(w, ri, item_tok, head, valid, m, l);

@@ -78,6 +78,18 @@ SFFN_DEV bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// Whether the phase is complete, without waiting.
+SFFN_DEV bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Wait for the barrier phase with the given parity to complete; gives up after
 // limit_ns of wall time and returns false (the caller records a timeout).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s
