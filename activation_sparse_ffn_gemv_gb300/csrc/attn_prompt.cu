@@ -19,18 +19,15 @@ namespace sffn {
 namespace {
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 5 : 10>;  // all of the shared memory: 227 KB
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8>;  // 208 KB and 176 KB of shared memory
 
 template <int D>
 struct PromptPolicy {
     const PromptArgs &a;
     int G, TB;
-    // A warp's place: blocks [nxt, top] of the `cnt` sequences that have them; `before` pairs
-    // (sequence, block) come ahead of this stretch.
-    struct Walk {
-        long long before;
-        int round, top, nxt, cnt;
-    };
+    // The walk's place: blocks [nxt, top] of the `cnt` sequences that have them; `before` pairs
+    // (sequence, block) come ahead of this stretch.  Items stay below 2^30: T <= 2^20, 1024 heads.
+    int before, round, top, nxt, cnt;
 
     SFFN_DEV PromptPolicy(const PromptArgs &args) : a(args), G(args.group), TB(128 / args.group) {}
 
@@ -59,38 +56,26 @@ struct PromptPolicy {
         cnt = __reduce_add_sync(0xffffffffu, above);
         nxt = __reduce_max_sync(0xffffffffu, below);
     }
-    SFFN_DEV void start(Walk &k) const {
-        int cnt, nxt;
+    SFFN_DEV void start() {
+        before = round = cnt = nxt = 0;
+        top = -1;
+        if (threadIdx.x >= 32) return;
         stretch(0x7fffffff, cnt, nxt);  // nxt: the largest count
-        const int top = nxt - 1;
+        top = nxt - 1;
         if (top >= 0) stretch(top + 1, cnt, nxt);
-        k.before = 0;
-        k.round = 0;
-        k.top = top;
-        k.nxt = nxt;
-        k.cnt = cnt;
     }
-    SFFN_DEV bool next(atc::Work &w, Walk &k) const {
-        const int W = gridDim.x, round = k.round;
-        const long long idx = (long long)round * W + ((round & 1) ? W - 1 - (int)blockIdx.x : (int)blockIdx.x);
-        const long long pair = idx / a.n_kv_heads;
-        long long before = k.before;
-        int top = k.top, nxt = k.nxt, cnt = k.cnt;
-        __syncwarp();
-        while (top >= 0 && pair >= before + (long long)cnt * (top - nxt + 1)) {
-            before += (long long)cnt * (top - nxt + 1);
+    SFFN_DEV bool next(atc::Work &w) {
+        const int W = gridDim.x, idx = round * W + ((round & 1) ? W - 1 - (int)blockIdx.x : (int)blockIdx.x);
+        const int pair = idx / a.n_kv_heads;
+        ++round;
+        while (top >= 0 && pair - before >= cnt * (top - nxt + 1)) {
+            before += cnt * (top - nxt + 1);
             top = nxt - 1;
             if (top >= 0) stretch(top + 1, cnt, nxt);
         }
-        k.before = before;
-        k.round = round + 1;
-        k.top = top;
-        k.nxt = nxt;
-        k.cnt = cnt;
         if (top < 0) return false;
-        const long long off = pair - before;
-        const int block = top - (int)(off / cnt);
-        int rank = (int)(off % cnt);
+        const int off = pair - before, down = off / cnt, block = top - down;
+        int rank = off - down * cnt;
         // the rank-th sequence that has this block
         const int lane = threadIdx.x & 31;
         int s = 0;
@@ -108,7 +93,7 @@ struct PromptPolicy {
         int t0, n;
         seq(s, t0, n);
         const int i0 = block * 2 * TB, nt = min(2 * TB, n - i0), k1 = i0 + nt;
-        w.h = (int)(idx - pair * a.n_kv_heads);
+        w.h = idx - pair * a.n_kv_heads;
         w.i0 = i0;
         w.base = t0;
         w.q_row = t0 + i0;
@@ -131,11 +116,9 @@ struct PromptPolicy {
     }
 
     struct RowInfo {
-        int pos;        // the row's position
-        float inv;
-        uint16_t *dst;
+        int pos;  // the row's position
     };
-    SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const { return RowInfo{w.i0 + tok, 0.f, nullptr}; }
+    SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const { return RowInfo{w.i0 + tok}; }
     SFFN_DEV void visible(const atc::Work &, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
         const int n = r.pos + 1 - j * atc::kKeys;
 #pragma unroll
@@ -145,21 +128,13 @@ struct PromptPolicy {
         if (key > r.pos) return nullptr;
         return static_cast<const uint16_t *>(a.v) + (size_t)(w.base + key) * a.v_stride + (size_t)w.h * D;
     }
-    SFFN_DEV void begin_row(const atc::Work &w, RowInfo &r, int tok, int head, bool valid, float, float l) const {
-        r.inv = 1.f / l;
-        r.dst = static_cast<uint16_t *>(a.out) +
-                (valid ? ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D : 0);
-    }
-    SFFN_DEV void store(const atc::Work &, const RowInfo &r, int q, const uint32_t (&o)[32]) const {
-        uint4 *dst = reinterpret_cast<uint4 *>(r.dst + q * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t p[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                p[e] = atc::pack_bf16(__uint_as_float(o[i * 8 + 2 * e]) * r.inv, __uint_as_float(o[i * 8 + 2 * e + 1]) * r.inv);
-            dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
-        }
+    SFFN_DEV bool partial(const atc::Work &) const { return false; }
+    SFFN_DEV unsigned char *begin_row(const atc::Work &w, int tok, int head, bool valid, float, float l,
+                                      float &inv) const {
+        inv = 1.f / l;
+        if (!valid) return nullptr;
+        return reinterpret_cast<unsigned char *>(static_cast<uint16_t *>(a.out) +
+                                                 ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D);
     }
 };
 

@@ -34,6 +34,9 @@ namespace atc {
 
 constexpr int kThreads = 320;
 constexpr int kKeys = 128;                   // keys of a tile
+constexpr int kItems = 3;                    // items that the loading warp has described, at most
+constexpr uint32_t kHoldNs = 10000000;       // the hardware may hold a waiting warp for 10 ms,
+constexpr int kMaxTries = 200;               // and a wait gives up after 200 of them (2 s)
 constexpr float kLazyLog2 = 8.f;             // the running maximum moves when passed by 2^8
 
 template <int D, int STAGES>
@@ -43,11 +46,13 @@ struct Cfg {
     static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
     static constexpr int kStages = STAGES;                      // K and V tiles of the ring
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
-    static constexpr int kSmem = (2 + kStages) * kTile + 1024 /*alignment*/;
+    static constexpr int kOut = 2048;                           // a softmax warp's: 128 bytes of 16 output rows
+    static constexpr int kSmem = (2 + kStages) * kTile + 8 * kOut + 1024 /*alignment*/;
 };
 
-// One item, the same for every warp.
+// One item.  The loading warp finds the items and describes them in a small ring.
 struct Work {
+    int more;           // 0: no further item
     int q_row;          // first token (row of q and out)
     int nt;             // tokens
     int h;              // key head
@@ -87,6 +92,13 @@ SFFN_DEV uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Maximum of three (NaNs are passed over, as in fmaxf).
+SFFN_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 SFFN_DEV uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t *>(&p);
@@ -99,19 +111,22 @@ SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x008
 SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // P: the policy (prompts or tree).  It gives
-//   bool next(Work &, Walk &)  the CTA's items in turn, the same in every warp; each warp
-//                          keeps its item and its place in shared memory (the softmax
-//                          warps need their registers for a row's 128 scores)
-//   load_q / load_kv       the producer's loads
-//   visible words, value rows, the epilogue's destination (see attn_prompt.cu / attn_tree.cu)
+//   start                  before the first item (every warp calls it)
+//   bool next(Work &)      the CTA's items in turn (the loading warp alone)
+//   load_kv                the producer's loads of a K or V tile
+//   row_info, visible      a row's own data; which keys of a masked tile it sees, as four words
+//   value_row              a key's value row in memory (null: the row does not see the key)
+//   begin_row, partial     where a row's output goes; whether as fp32 partial result
 template <int D, int STAGES, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                             float scale, int G, int32_t *err, unsigned char *smem_raw) {
     using C = Cfg<D, STAGES>;
     const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + 2 * C::kTile;
-    unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile;
+    unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile,
+                  *sm_out = sm_kv + C::kStages * C::kTile;
     constexpr int NS = C::kStages;
-    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone;
+    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone,
+        i_full[kItems], i_empty[kItems];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
 
@@ -127,6 +142,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             mbar_init(&o_full[t], 1);
         }
         mbar_init(&mdone, 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&i_full[i], 1);
+            mbar_init(&i_empty[i], 9);  // the issuing warp and the eight softmax warps
+        }
         s_abort = 0;
         s_bad = 0;
         mbar_fence_init();
@@ -151,39 +170,50 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     // results are not valid then), and every later wait passes at once: all loops still end,
     // and a wait that is over costs one look and one branch, which counts between two products.
     auto wait_slow = [&](uint64_t *bar, uint32_t parity) {
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar, parity) && !s_abort)
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+        for (int tries = 0; !mbar_try_wait_for(bar, parity, kHoldNs) && !s_abort; ++tries)
+            if (tries == kMaxTries) {
                 s_abort = 1;
                 record_error(err, SFFN_ERR_TIMEOUT);
             }
     };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_try_wait(bar, parity)) wait_slow(bar, parity);
+        if (!mbar_try_wait_for(bar, parity, kHoldNs)) wait_slow(bar, parity);
         __syncwarp();
     };
 
     griddep_wait();
     const int TB = 128 / G;
-    __shared__ Work s_work[kThreads / 32];
-    __shared__ typename P::Walk s_walk[kThreads / 32];
-    Work &w = s_work[warp];
-    typename P::Walk &walk = s_walk[warp];
-    policy.start(walk);
+    __shared__ Work s_work[kItems];
+    policy.start();
     griddep_launch_dependents();
-    // the next item; the warp's lanes agree on it before and after
-    auto next = [&]() -> bool {
+    int item = 0;  // items taken so far
+    // The other warps' next item, and its return.
+    auto take = [&]() -> const Work & {
+        const int i = item % kItems;
+        wait(&i_full[i], (uint32_t)((item / kItems) & 1));
+        return s_work[i];
+    };
+    auto give_back = [&]() {
         __syncwarp();
-        const bool more = policy.next(w, walk);
-        __syncwarp();
-        return more;
+        if (lane == 0) mbar_arrive(&i_empty[item % kItems]);
+        ++item;
     };
 
     if (warp == 0) {
         // ---------------- loads ----------------
         int it = 0, qn[2] = {0, 0};
         const uint64_t keep = tc::l2_evict_last_policy();
-        while (next()) {
+        for (;; ++item) {
+            Work &w = s_work[item % kItems];
+            wait(&i_empty[item % kItems], (uint32_t)(((item / kItems) & 1) ^ 1));
+            const bool more = policy.next(w) && !s_abort;
+            __syncwarp();
+            if (lane == 0) {
+                w.more = more;
+                mbar_arrive(&i_full[item % kItems]);
+            }
+            __syncwarp();
+            if (!more) break;
             const int n0 = w.n[0], n1 = w.n[1], nmax = max(n0, n1);
             for (int j = 0; j < nmax; ++j) {
                 for (int part = 0; part < 2; ++part) {
@@ -240,7 +270,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
         // The ring's tiles are given back by the softmax warps, which see S_t(j) arrive after their last
         // reader: no tcgen05.commit but the one per score product.
-        while (next()) {
+        for (;; give_back()) {
+            const Work &w = take();
+            if (!w.more) break;
             // uniform by construction; the reductions tell the compiler so
             const int n[2] = {__reduce_max_sync(0xffffffffu, w.n[0]), __reduce_max_sync(0xffffffffu, w.n[1])};
             const int nmax = max(n[0], n[1]);
@@ -292,7 +324,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
         int sn = 0, on = 0, base = 0;
-        while (next()) {
+        bool seen = true;  // this warp has seen every earlier fill of the ring, as far as it matters for V_0
+        for (;; give_back()) {
+            const Work &w = take();
+            if (!w.more) break;
             const int n = w.n[t], nmax = max(w.n[0], w.n[1]);
             const int item_tok = t * TB + tok;          // token of the item
             const bool valid = tok < TB && item_tok < w.nt;
@@ -302,26 +337,42 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             for (int j = 0; j < n; ++j) {
                 const bool masked = j >= w.mask_from[t];
                 if (masked) {
-                    // non-finite values of this tile: zero (and noted, if their keys exist)
+                    // Non-finite values of this tile: zero (and noted, if their keys exist).  The wait
+                    // for V tells its fill from the slot's one before only if that one has been
+                    // seen: S_t(j - 1) and O_t say so, but not for tiles that these rows skipped.
+                    if (j == 0 && !seen) wait(&s_full[t], (uint32_t)(sn & 1));
                     const int iv = base + 2 * j + 1, vs = iv % NS;
                     wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
                     uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
                     const int kb = w.k0 + j * kKeys;
-                    for (int i = tid - 64 - t * 128; i < C::kTile / 16; i += 128) {
-                        uint4 x = v[i];
-                        const uint32_t b0 = nonfinite_bits(x.x), b1 = nonfinite_bits(x.y), b2 = nonfinite_bits(x.z),
-                                       b3 = nonfinite_bits(x.w);
-                        if (b0 | b1 | b2 | b3) {
-                            if (kb + ((i >> 3) & 127) < w.exist) {
-                                s_bad = 1;
-                                __threadfence_block();
+#pragma unroll 1
+                    for (int i0 = quad * 32 + lane; i0 < C::kTile / 16; i0 += 512) {
+                        uint4 x[4];
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) x[u] = v[i0 + u * 128];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            any |= nonfinite_bits(x[u].x) | nonfinite_bits(x[u].y) | nonfinite_bits(x[u].z) |
+                                   nonfinite_bits(x[u].w);
+                        if (any) {
+#pragma unroll 1
+                            for (int i = i0; i < i0 + 512; i += 128) {
+                                uint4 y = v[i];
+                                const uint32_t b0 = nonfinite_bits(y.x), b1 = nonfinite_bits(y.y),
+                                               b2 = nonfinite_bits(y.z), b3 = nonfinite_bits(y.w);
+                                if (!(b0 | b1 | b2 | b3)) continue;
+                                if (kb + ((i >> 3) & 127) < w.exist) {
+                                    s_bad = 1;
+                                    __threadfence_block();
+                                }
+                                // (bit >> 15) * 0xffff: the whole half
+                                y.x &= ~((b0 >> 15) * 0xffffu);
+                                y.y &= ~((b1 >> 15) * 0xffffu);
+                                y.z &= ~((b2 >> 15) * 0xffffu);
+                                y.w &= ~((b3 >> 15) * 0xffffu);
+                                v[i] = y;
                             }
-                            // (bit >> 15) * 0xffff: the whole half
-                            x.x &= ~((b0 >> 15) * 0xffffu);
-                            x.y &= ~((b1 >> 15) * 0xffffu);
-                            x.z &= ~((b2 >> 15) * 0xffffu);
-                            x.w &= ~((b3 >> 15) * 0xffffu);
-                            v[i] = x;
                         }
                     }
                     fence_proxy_async_smem();
@@ -347,18 +398,21 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     policy.visible(w, ri, j, vis);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
+                        if (__any_sync(0xffffffffu, vis[q] != 0xffffffffu)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            s[q][i] = (vis[q] >> i) & 1u ? s[q][i] : 0xff800000u;  // -inf
+                            for (int i = 0; i < 32; ++i)
+                                s[q][i] = (vis[q] >> i) & 1u ? s[q][i] : 0xff800000u;  // -inf
+                        }
                 }
                 float mx[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    mx[q] = __uint_as_float(s[q][0]);
+                    mx[q] = fmaxf(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]));
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                    for (int i = 2; i < 32; i += 2)
+                        mx[q] = max3(mx[q], __uint_as_float(s[q][i]), __uint_as_float(s[q][i + 1]));
                 }
-                const float mnew = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const float mnew = max3(m, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool up = (mnew - m) * c > kLazyLog2;
                 if (__any_sync(0xffffffffu, up)) {
                     const float alpha = up ? ex2((m - mnew) * c) : 1.f;
@@ -410,14 +464,44 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 if (releases && lane == 0 && quad == 0) mbar_arrive(&kv_empty[(base + 2 * n - 1) % NS]);
                 tc::fence_after_sync();
                 const bool bad = s_bad != 0;
-                policy.begin_row(w, ri, item_tok, head, valid, m, l);
+                // this lane's row of the output (null: not a row), and a factor
+                float inv;
+                unsigned char *dst = policy.begin_row(w, item_tok, head, valid, m, l, inv);
+                const bool f32 = policy.partial(w);
+                unsigned char *stage = sm_out + (warp - 2) * C::kOut;
+                // 128 bytes of 16 rows at a time through shared memory, 16-byte chunks swizzled by the
+                // row: a store then covers four rows' lines instead of 16 bytes of 32 rows
+                auto flush = [&](const uint32_t (&x)[32], int seg) {
+#pragma unroll
+                    for (int hr = 0; hr < 2; ++hr) {
+                        if ((lane >> 4) == hr) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4 *>(stage + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
+                                    make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 4 + (lane >> 3), ch = lane & 7;
+                            unsigned char *d = reinterpret_cast<unsigned char *>(
+                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), hr * 16 + r));
+                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
+                            if (d) *reinterpret_cast<uint4 *>(d + (size_t)seg * 128 + ch * 16) = v;
+                        }
+                        __syncwarp();
+                    }
+                };
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(to + q * 32, o);
-                    tc::tmem_wait_ld();
-                    if (valid) {
-                        if (bad) {
+                for (int q2 = 0; q2 < D / 64; ++q2) {
+                    uint32_t pk[32];  // 64 columns as bf16
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int q = q2 * 2 + h;
+                        uint32_t o[32];
+                        tc::tmem_ld32(to + q * 32, o);
+                        tc::tmem_wait_ld();
+                        if (bad && valid) {
                             // the masked tiles' non-finite values that this row sees
                             const int from = w.k0 + min(w.mask_from[0], w.mask_from[1]) * kKeys;
                             for (int key = from; key < w.k1; ++key) {
@@ -437,12 +521,20 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                                 }
                             }
                         }
-                        policy.store(w, ri, q, o);
+                        if (f32) {
+                            flush(o, q);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pk[h * 16 + i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        }
                     }
+                    if (!f32) flush(pk, q2);
                 }
                 tc::fence_before_sync();  // O_t has been read: the next item's product may overwrite it
             }
             base += 2 * nmax;
+            seen = n >= nmax - 1;
         }
     }
     tc::fence_before_sync();

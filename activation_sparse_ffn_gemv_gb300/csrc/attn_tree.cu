@@ -96,16 +96,11 @@ template <int D>
 struct TreePolicy {
     const TreeArgs &a;
     long long *pre;         // units before each sequence (shared memory)
-    long long u1;           // end of this CTA's units
+    long long u, u1;        // this CTA's next unit, and the end of its units
     int G, TB, box;         // box: cache rows of one copy (a page's, 64 at most)
 
-    struct Walk {
-        long long u;
-    };
     struct RowInfo {
         uint64_t mask;
-        float inv;
-        void *dst;
     };
 
     long long *scratch;
@@ -113,15 +108,14 @@ struct TreePolicy {
     SFFN_DEV TreePolicy(const TreeArgs &args, long long *prefix, long long *scan)
         : a(args), pre(prefix), G(args.group), TB(128 / args.group), box(min(64, 1 << args.page_shift)), scratch(scan) {}
 
-    SFFN_DEV void start(Walk &k) {
+    SFFN_DEV void start() {
         tree_prefix(a, pre, scratch, blockIdx.x == 0);
         const long long total = pre[a.n_seq];
         const int W = tree_ctas(total, gridDim.x), b = blockIdx.x;
-        k.u = b < W ? tree_cut(total, b, W) : 0;
+        u = b < W ? tree_cut(total, b, W) : 0;
         u1 = b < W ? tree_cut(total, b + 1, W) : 0;
     }
-    SFFN_DEV bool next(atc::Work &w, Walk &k) const {
-        const long long u = k.u;
+    SFFN_DEV bool next(atc::Work &w) {
         if (u >= u1) return false;
         const int s = tree_find(pre, a.n_seq, u);
         const TreeSeq q = tree_seq(a, s, false);
@@ -131,8 +125,7 @@ struct TreePolicy {
         const int tile = item / a.n_kv_heads, tk0 = tile * a.tile_tokens;
         const int k0 = un0 * kTreeUnit, k1 = min(q.ctx + q.n, un1 * kTreeUnit);
         const int n = (k1 - k0 + atc::kKeys - 1) / atc::kKeys;
-        __syncwarp();
-        k.u = u + (un1 - un0);
+        u += un1 - un0;
         w.h = item - tile * a.n_kv_heads;
         w.q_row = q.t0 + tk0;
         w.nt = min(a.tile_tokens, q.n - tk0);
@@ -171,7 +164,7 @@ struct TreePolicy {
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
         const int i = w.tok0 + tok;
         const uint64_t m = a.tree_mask ? a.tree_mask[w.q_row + tok] : (i == 63 ? ~0ull : (1ull << (i + 1)) - 1ull);
-        return RowInfo{m, 0.f, nullptr};
+        return RowInfo{m};
     }
     SFFN_DEV void visible(const atc::Work &w, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
         const int kb = w.k0 + j * atc::kKeys;
@@ -191,36 +184,18 @@ struct TreePolicy {
         if (row >= ((long long)a.n_pages * a.n_kv_heads) << a.page_shift) return nullptr;
         return static_cast<const uint16_t *>(a.cv) + (size_t)row * D;
     }
-    SFFN_DEV void begin_row(const atc::Work &w, RowInfo &r, int tok, int head, bool valid, float m, float l) const {
-        if (!valid) return;
-        if (w.whole) {
-            r.inv = l == 0.f ? 0.f : 1.f / l;
-            r.dst = static_cast<uint16_t *>(a.out) +
-                    ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D;
-        } else {
-            float *slot = a.part + tree_slot_floats(a.rows_max, D) * (size_t)w.slot;
-            const int row = tok * G + head;
-            r.dst = slot + (size_t)row * D;
-            *reinterpret_cast<float2 *>(slot + (size_t)a.rows_max * D + 2 * row) = make_float2(m * a.scale, l);
-        }
-    }
-    SFFN_DEV void store(const atc::Work &w, const RowInfo &r, int q, const uint32_t (&o)[32]) const {
-        if (w.whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(r.dst) + q * 32);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t p[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    p[e] = atc::pack_bf16(__uint_as_float(o[i * 8 + 2 * e]) * r.inv,
-                                          __uint_as_float(o[i * 8 + 2 * e + 1]) * r.inv);
-                dst[i] = make_uint4(p[0], p[1], p[2], p[3]);
-            }
-        } else {
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<float *>(r.dst) + q * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        }
+    SFFN_DEV bool partial(const atc::Work &w) const { return !w.whole; }
+    SFFN_DEV unsigned char *begin_row(const atc::Work &w, int tok, int head, bool valid, float m, float l,
+                                      float &inv) const {
+        inv = l == 0.f ? 0.f : 1.f / l;
+        if (!valid) return nullptr;
+        if (w.whole)
+            return reinterpret_cast<unsigned char *>(static_cast<uint16_t *>(a.out) +
+                                                     ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D);
+        float *slot = a.part + tree_slot_floats(a.rows_max, D) * (size_t)w.slot;
+        const int row = tok * G + head;
+        *reinterpret_cast<float2 *>(slot + (size_t)a.rows_max * D + 2 * row) = make_float2(m * a.scale, l);
+        return reinterpret_cast<unsigned char *>(slot + (size_t)row * D);
     }
 };
 

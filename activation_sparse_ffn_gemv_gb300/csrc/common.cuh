@@ -78,15 +78,16 @@ SFFN_DEV bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// Whether the phase is complete, without waiting.
-SFFN_DEV bool mbar_test(uint64_t *bar, uint32_t parity) {
+// The same with a hint of how long (in ns) the hardware may hold the thread before the try fails:
+// a warp that is held does not poll, and leaves the issue slots to its neighbours.
+SFFN_DEV bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
         : "memory");
     return ok != 0;
 }
