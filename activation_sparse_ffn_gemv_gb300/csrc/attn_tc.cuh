@@ -46,7 +46,7 @@ struct Cfg {
     static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
     static constexpr int kStages = STAGES;                      // K and V tiles of the ring
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
-    static constexpr int kOut = 2048;                           // a softmax warp's: 128 bytes of 16 output rows
+    static constexpr int kOut = 2048;                           // a softmax warp's: 64 bytes of its 32 output rows
     static constexpr int kSmem = (2 + kStages) * kTile + 8 * kOut + 1024 /*alignment*/;
 };
 
@@ -325,7 +325,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
         int sn = 0, on = 0, base = 0;
         bool seen = true;  // this warp has seen every earlier fill of the ring, as far as it matters for V_0
-        for (;; give_back()) {
+        for (;;) {
             const Work &w = take();
             if (!w.more) break;
             const int n = w.n[t], nmax = max(w.n[0], w.n[1]);
@@ -382,10 +382,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 if (lane == 0 && quad == 0) {
                     // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
                     // before it are, once the later row tile's products are through
-                    if (j + 1 == n) mbar_arrive(&q_empty[t]);
+                    if (j + 1 == n) mbar_arrive_relaxed(&q_empty[t]);
                     if (releases) {
-                        mbar_arrive(&kv_empty[(base + 2 * j) % NS]);
-                        if (j > 0) mbar_arrive(&kv_empty[(base + 2 * j - 1) % NS]);
+                        mbar_arrive_relaxed(&kv_empty[(base + 2 * j) % NS]);
+                        if (j > 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * j - 1) % NS]);
                     }
                 }
                 tc::fence_after_sync();
@@ -461,7 +461,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (n > 0) {
                 wait(&o_full[t], (uint32_t)(on & 1));
                 ++on;
-                if (releases && lane == 0 && quad == 0) mbar_arrive(&kv_empty[(base + 2 * n - 1) % NS]);
+                if (releases && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) % NS]);
                 tc::fence_after_sync();
                 const bool bad = s_bad != 0;
                 // this lane's row of the output (null: not a row), and a factor
@@ -469,69 +469,77 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 unsigned char *dst = policy.begin_row(w, item_tok, head, valid, m, l, inv);
                 const bool f32 = policy.partial(w);
                 unsigned char *stage = sm_out + (warp - 2) * C::kOut;
-                // 128 bytes of 16 rows at a time through shared memory, 16-byte chunks swizzled by the
-                // row: a store then covers four rows' lines instead of 16 bytes of 32 rows
-                auto flush = [&](const uint32_t (&x)[32], int seg) {
-#pragma unroll
-                    for (int hr = 0; hr < 2; ++hr) {
-                        if ((lane >> 4) == hr) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4 *>(stage + (lane & 15) * 128 + ((i ^ (lane & 7)) << 4)) =
-                                    make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                        }
-                        __syncwarp();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 4 + (lane >> 3), ch = lane & 7;
-                            unsigned char *d = reinterpret_cast<unsigned char *>(
-                                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), hr * 16 + r));
-                            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((ch ^ (r & 7)) << 4));
-                            if (d) *reinterpret_cast<uint4 *>(d + (size_t)seg * 128 + ch * 16) = v;
-                        }
-                        __syncwarp();
-                    }
-                };
+                if (__any_sync(0xffffffffu, bad && valid)) {
+                    // the masked tiles' non-finite values that this row sees
+                    const int from = w.k0 + min(w.mask_from[0], w.mask_from[1]) * kKeys;
 #pragma unroll 1
-                for (int q2 = 0; q2 < D / 64; ++q2) {
-                    uint32_t pk[32];  // 64 columns as bf16
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int q = q2 * 2 + h;
-                        uint32_t o[32];
-                        tc::tmem_ld32(to + q * 32, o);
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(to + q * 16, o);
                         tc::tmem_wait_ld();
-                        if (bad && valid) {
-                            // the masked tiles' non-finite values that this row sees
-                            const int from = w.k0 + min(w.mask_from[0], w.mask_from[1]) * kKeys;
-                            for (int key = from; key < w.k1; ++key) {
-                                const uint4 *vr = reinterpret_cast<const uint4 *>(policy.value_row(w, ri, key));
-                                if (!vr) continue;
+                        for (int key = from; valid && key < w.k1; ++key) {
+                            const uint4 *vr = reinterpret_cast<const uint4 *>(policy.value_row(w, ri, key));
+                            if (!vr) continue;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    const uint4 x = vr[q * 4 + i];
-                                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                            for (int i = 0; i < 2; ++i) {
+                                const uint4 x = vr[q * 2 + i];
+                                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const uint32_t nb = nonfinite_bits(xs[e]);
-                                        uint32_t &lo = o[i * 8 + e * 2], &hi = o[i * 8 + e * 2 + 1];
-                                        if (nb & 0x8000u) lo = __float_as_uint(__uint_as_float(lo) + bf16lo(xs[e]));
-                                        if (nb & 0x80000000u) hi = __float_as_uint(__uint_as_float(hi) + bf16hi(xs[e]));
-                                    }
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t nb = nonfinite_bits(xs[e]);
+                                    uint32_t &lo = o[i * 8 + e * 2], &hi = o[i * 8 + e * 2 + 1];
+                                    if (nb & 0x8000u) lo = __float_as_uint(__uint_as_float(lo) + bf16lo(xs[e]));
+                                    if (nb & 0x80000000u) hi = __float_as_uint(__uint_as_float(hi) + bf16hi(xs[e]));
                                 }
                             }
                         }
-                        if (f32) {
-                            flush(o, q);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                pk[h * 16 + i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-                        }
+                        __syncwarp();
+                        tc::tmem_st16(to + q * 16, o);
                     }
-                    if (!f32) flush(pk, q2);
+                    tc::tmem_wait_st();
+                }
+                give_back();  // before the stores, which the release would wait for
+                // 64 bytes of every row at a time through shared memory, the 16-byte chunks swizzled by
+                // the row: a store then covers 64 bytes of eight rows instead of 16 of 32
+                auto flush = [&](const uint32_t (&x)[16], int seg) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = i * 8 + (lane >> 2), ch = lane & 3;
+                        unsigned char *d = reinterpret_cast<unsigned char *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
+                        if (d) *reinterpret_cast<uint4 *>(d + (size_t)seg * 64 + ch * 16) = v;
+                    }
+                };
+                if (f32) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t o[16];
+                        tc::tmem_ld16(to + q * 16, o);
+                        tc::tmem_wait_ld();
+                        flush(o, q);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t o[32], pk[16];
+                        tc::tmem_ld32(to + q * 32, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+                        flush(pk, q);
+                    }
                 }
                 tc::fence_before_sync();  // O_t has been read: the next item's product may overwrite it
+            } else {
+                give_back();
             }
             base += 2 * nmax;
             seen = n >= nmax - 1;

@@ -67,6 +67,10 @@ SFFN_DEV void mbar_arrive_expect_tx(uint64_t *bar, uint32_t bytes) {
 SFFN_DEV void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// An arrival that orders no memory access of this thread (it does not wait for its stores).
+SFFN_DEV void mbar_arrive_relaxed(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 SFFN_DEV bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
