@@ -19,7 +19,7 @@ namespace sffn {
 namespace {
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 4 : 8>;  // 208 KB and 176 KB of shared memory
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false>;  // 208 KB and 176 KB of shared memory
 
 template <int D>
 struct PromptPolicy {
@@ -101,18 +101,22 @@ struct PromptPolicy {
         w.k0 = 0;
         w.k1 = k1;
         w.exist = n;
-        w.n[0] = (min(i0 + TB, n) + atc::kKeys - 1) / atc::kKeys;
-        w.n[1] = nt > TB ? (k1 + atc::kKeys - 1) / atc::kKeys : 0;
+        w.tiles = (k1 + atc::kKeys - 1) / atc::kKeys;
+        w.split = nt <= TB;
+        w.n[0] = w.split ? (w.tiles + 1) / 2 : (min(i0 + TB, n) + atc::kKeys - 1) / atc::kKeys;
+        w.n[1] = w.split ? w.tiles / 2 : w.tiles;
         w.mask_from[0] = (i0 + 1) / atc::kKeys;
-        w.mask_from[1] = (i0 + TB + 1) / atc::kKeys;
+        w.mask_from[1] = (i0 + (w.split ? 0 : TB) + 1) / atc::kKeys;
         return true;
     }
-    SFFN_DEV void load_kv(const atc::Work &w, int j, const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int lane,
-                          uint64_t pol) const {
+    // Row of a key tile's first key.
+    SFFN_DEV int place(const atc::Work &w, int j, int) const { return w.base + j * atc::kKeys; }
+    SFFN_DEV void load_kv(const atc::Work &w, int, int row, const CUtensorMap *map, unsigned char *dst, uint64_t *bar,
+                          int lane, uint64_t pol) const {
         if (lane != 0) return;
         mbar_arrive_expect_tx(bar, Cfg<D>::kTile);
         for (int c = 0; c < Cfg<D>::kHalves; ++c)
-            tc::tma_load_3d(dst + c * Cfg<D>::kBlock, map, c * 64, w.h, w.base + j * atc::kKeys, bar, pol);
+            tc::tma_load_3d(dst + c * Cfg<D>::kBlock, map, c * 64, w.h, row, bar, pol);
     }
 
     struct RowInfo {
@@ -144,7 +148,7 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
                   const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
     extern __shared__ unsigned char smem_raw[];
     PromptPolicy<D> policy(a);
-    atc::attention_cta<D, Cfg<D>::kStages>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
+    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
 }
 
 template <int D>

@@ -17,7 +17,10 @@
 //   warps 2-5   softmax of tile 0: a thread owns a row; S_t from TMEM, weights P_t (bf16)
 //   warps 6-9   softmax of tile 1  back to TMEM over S_t, where the second product reads
 //               them as its A operand; at the end O_t / sum to global memory
-// While one tile's softmax runs, the tensor cores work on the other tile.
+// While one tile's softmax runs, the tensor cores work on the other tile.  An item of a single row
+// tile (few new tokens, a prompt's last ones) has its key tiles dealt to the two pipelines
+// instead; at the end the first one joins both results, reading the other's accumulator
+// from TMEM (the same rows are the same lanes).
 //
 // A weight of zero times an infinite or NaN value would be NaN, so in a tile with
 // masked keys the softmax warps look through V in shared memory before the second
@@ -39,12 +42,21 @@ constexpr uint32_t kHoldNs = 10000000;       // the hardware may hold a waiting 
 constexpr int kMaxTries = 200;               // and a wait gives up after 200 of them (2 s)
 constexpr float kLazyLog2 = 8.f;             // the running maximum moves when passed by 2^8
 
-template <int D, int STAGES>
+// GROUPED: layout of the K and V tiles in shared memory.  false: column block by column block
+// (a TMA box is 128 rows of one block).  true: by groups of 8 rows, each with its column blocks in
+// turn, so that any multiple of 8 rows with all its columns is one box (a page).
+template <int D, int STAGES, bool GROUPED>
 struct Cfg {
     static constexpr int kHalves = D / 64;                      // 64-element (128-byte) column blocks
     static constexpr int kBlock = 128 * 128;                    // bytes of a column block: 128 rows x 128 bytes
     static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
     static constexpr int kStages = STAGES;                      // K and V tiles of the ring
+    static_assert((STAGES & (STAGES - 1)) == 0, "ring indexes are masked");
+    static constexpr bool kGrouped = GROUPED;
+    static constexpr int kRows8 = GROUPED ? kHalves * 1024 : 1024;  // bytes from 8 rows to the next 8
+    static constexpr int kColBlock = GROUPED ? 1024 : kBlock;       // bytes from a column block to the next
+    // Row of a K or V tile that its i-th 16-byte chunk belongs to.
+    SFFN_DEV static int row_of(int i) { return GROUPED ? (i / (64 * kHalves)) * 8 + ((i >> 3) & 7) : (i >> 3) & 127; }
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
     static constexpr int kOut = 2048;                           // a softmax warp's: 64 bytes of its 32 output rows
     static constexpr int kSmem = (2 + kStages) * kTile + 8 * kOut + 1024 /*alignment*/;
@@ -56,8 +68,10 @@ struct Work {
     int q_row;          // first token (row of q and out)
     int nt;             // tokens
     int h;              // key head
-    int n[2];           // key tiles of each row tile
-    int mask_from[2];   // first of them with masked keys
+    int split;          // one row tile: the two pipelines take its even and its odd key tiles
+    int tiles;          // key tiles
+    int n[2];           // those of each pipeline
+    int mask_from[2];   // first key tile with masked keys
     int k0, k1;         // keys [k0, k1) (logical positions)
     int exist;          // keys below this one exist
     int i0;             // prompt: position of the first token
@@ -117,18 +131,18 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 //   row_info, visible      a row's own data; which keys of a masked tile it sees, as four words
 //   value_row              a key's value row in memory (null: the row does not see the key)
 //   begin_row, partial     where a row's output goes; whether as fp32 partial result
-template <int D, int STAGES, typename P>
+template <typename C, int D, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                             float scale, int G, int32_t *err, unsigned char *smem_raw) {
-    using C = Cfg<D, STAGES>;
     const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + 2 * C::kTile;
     unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile,
                   *sm_out = sm_kv + C::kStages * C::kTile;
     constexpr int NS = C::kStages;
     __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone,
-        i_full[kItems], i_empty[kItems];
+        i_full[kItems], i_empty[kItems], x_full, x_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
+    __shared__ float2 s_x[128];  // maximum and sum of the second pipeline's rows (split items)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -142,6 +156,8 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             mbar_init(&o_full[t], 1);
         }
         mbar_init(&mdone, 1);
+        mbar_init(&x_full, 4);
+        mbar_init(&x_empty, 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&i_full[i], 1);
             mbar_init(&i_empty[i], 9);  // the issuing warp and the eight softmax warps
@@ -214,25 +230,28 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             }
             __syncwarp();
             if (!more) break;
-            const int n0 = w.n[0], n1 = w.n[1], nmax = max(n0, n1);
-            for (int j = 0; j < nmax; ++j) {
+            const int tiles = w.tiles;
+            int place = policy.place(w, 0, lane);
+            for (int j = 0; j < tiles; ++j) {
+                const int nxt = j + 1 < tiles ? policy.place(w, j + 1, lane) : 0;  // a tile ahead
                 for (int part = 0; part < 2; ++part) {
-                    // the item's queries: tile 0 before the first K, tile 1 after it
-                    if (j == 0 && (part ? n1 : n0) > 0) {
+                    // the item's queries: the first tile's before the first K, the second's after it
+                    if (j == 0 && w.n[part] > 0) {
                         wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1));
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
                             for (int c = 0; c < C::kHalves; ++c)
                                 tc::tma_load_3d(sm_q + part * C::kTile + c * C::kBlock, &map_q, c * 64, w.h * G,
-                                                w.q_row + part * TB, &q_full[part], keep);
+                                                w.q_row + (w.split ? 0 : part * TB), &q_full[part], keep);
                         }
                         ++qn[part];
                     }
                     const int s = it % NS;
                     wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1));
-                    policy.load_kv(w, j, part ? &map_v : &map_k, sm_kv + s * C::kTile, &kv_full[s], lane, keep);
+                    policy.load_kv(w, j, place, part ? &map_v : &map_k, sm_kv + s * C::kTile, &kv_full[s], lane, keep);
                     ++it;
                 }
+                place = nxt;
             }
         }
         if (s_abort && lane == 0) {  // let the copies in flight land before the CTA can exit
@@ -245,21 +264,21 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         constexpr uint32_t idesc_s = tc::idesc_bf16_f32(128, 128, false);
         constexpr uint32_t idesc_o = tc::idesc_bf16_f32(128, D, true);
         // The whole warp runs this code, uniformly; one lane issues each instruction.
-        const uint64_t hi = tc::smem_desc_sw128(0, 16, 1024), hi_v = tc::smem_desc_sw128(0, C::kBlock, 1024);
+        const uint64_t hi_q = tc::smem_desc_sw128(0, 16, 1024), hi_k = tc::smem_desc_sw128(0, 16, C::kRows8),
+                       hi_v = tc::smem_desc_sw128(0, C::kColBlock, C::kRows8);
         auto scores = [&](int t, uint32_t tile) {  // S_t = Q_t K^T
-            const uint64_t a = hi | ((q_addr + t * C::kTile) >> 4), b = hi | (tile >> 4);
+            const uint64_t a = hi_q | ((q_addr + t * C::kTile) >> 4), b = hi_k | (tile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4;
-                tc::mma_bf16_warp(tmem + t * 128, a + off, b + off, idesc_s, kk != 0);
-            }
+            for (int kk = 0; kk < D / 16; ++kk)
+                tc::mma_bf16_warp(tmem + t * 128, a + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4),
+                                  b + (((kk >> 2) * C::kColBlock + (kk & 3) * 32) >> 4), idesc_s, kk != 0);
             tc::mma_commit_warp(&s_full[t]);
         };
         auto values = [&](int t, int half, uint32_t tile, bool acc) {  // O_t (+)= P_t V over half of the keys
             const uint64_t b = hi_v | (tile >> 4);
 #pragma unroll
             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                tc::mma_bf16_ts_warp(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8, b + kk * (2048 >> 4), idesc_o,
+                tc::mma_bf16_ts_warp(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8, b + kk * (2 * C::kRows8 >> 4), idesc_o,
                                      acc || kk != 0);
         };
         int slot = 0;                                        // ring position and its parity
@@ -268,47 +287,94 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (++slot == NS) slot = 0, par ^= 1;
         };
         auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
-        // The ring's tiles are given back by the softmax warps, which see S_t(j) arrive after their last
-        // reader: no tcgen05.commit but the one per score product.
-        for (;; give_back()) {
-            const Work &w = take();
-            if (!w.more) break;
-            // uniform by construction; the reductions tell the compiler so
-            const int n[2] = {__reduce_max_sync(0xffffffffu, w.n[0]), __reduce_max_sync(0xffffffffu, w.n[1])};
-            const int nmax = max(n[0], n[1]);
+        auto first_scores = [&](int t) {
+            wait(&q_full[t], q_par[t]);
+            q_par[t] ^= 1;
+            tc::fence_after_sync();
+            scores(t, tile_of(slot));
+        };
+        auto weigh = [&](int t, uint32_t v, bool acc) {  // O_t (+)= P_t V, as the weights come
+            wait(&p_ready[0][t], p_par[t]);
+            tc::fence_after_sync();
+            values(t, 0, v, acc);
+            wait(&p_ready[1][t], p_par[t]);
+            p_par[t] ^= 1;
+            tc::fence_after_sync();
+            values(t, 1, v, true);
+        };
+        // Two row tiles over the same key tiles.
+        auto both = [&](const int n0, const int n1) {
+            const int n[2] = {n0, n1};
             wait(&kv_full[slot], par);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (n[t] > 0) {
-                    wait(&q_full[t], q_par[t]);
-                    q_par[t] ^= 1;
-                    tc::fence_after_sync();
-                    scores(t, tile_of(slot));
-                }
-            }
+            for (int t = 0; t < 2; ++t) first_scores(t);
             step();
-            for (int j = 0; j < nmax; ++j) {
+            for (int j = 0; j < n1; ++j) {
                 const int vs = slot;
                 wait(&kv_full[vs], par);
                 step();
-                const bool more = j + 1 < nmax;
+                const bool more = j + 1 < n1;
                 if (more) wait(&kv_full[slot], par);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < n[t]) {
-                        wait(&p_ready[0][t], p_par[t]);
-                        tc::fence_after_sync();
-                        values(t, 0, tile_of(vs), j > 0);
-                        wait(&p_ready[1][t], p_par[t]);
-                        p_par[t] ^= 1;
-                        tc::fence_after_sync();
-                        values(t, 1, tile_of(vs), true);
+                        weigh(t, tile_of(vs), j > 0);
                         if (j + 1 == n[t]) tc::mma_commit_warp(&o_full[t]);
                     }
                     if (j + 1 < n[t]) scores(t, tile_of(slot));
                 }
                 if (more) step();
             }
+        };
+        // One row tile: pipeline t takes every other key tile.
+        auto dealt = [&](const int tiles) {
+            wait(&kv_full[slot], par);
+            first_scores(0);
+            step();
+            // V of tile i lies at the position of step i; K of tile i + 1 follows it
+            int v_slot = slot;
+            uint32_t v_par = par;
+            step();
+            if (tiles > 1) {
+                wait(&kv_full[slot], par);
+                first_scores(1);
+                step();
+            }
+            for (int i = 0; i < tiles; i += 2) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (i + t < tiles) {
+                        wait(&kv_full[v_slot], v_par);
+                        weigh(t, tile_of(v_slot), i > 0);
+                        // given back at once: S_t(i + 2) would say so too, but only after the next K's load
+                        tc::mma_commit_warp(&kv_empty[v_slot]);
+                        // on to the next tile's V; position `slot` is that of tile i + t + 1's V
+                        v_slot = slot;
+                        v_par = par;
+                        if (i + t + 1 < tiles) step();
+                        if (i + t + 2 < tiles) {
+                            wait(&kv_full[slot], par);
+                            tc::fence_after_sync();
+                            scores(t, tile_of(slot));
+                            step();
+                        } else {
+                            tc::mma_commit_warp(&o_full[t]);
+                        }
+                    }
+                }
+            }
+        };
+        // The ring's tiles are given back by the softmax warps, which see S_t(j) arrive after their last
+        // reader, with no more commits here (V of a dealt tile excepted).
+        for (;; give_back()) {
+            const Work &w = take();
+            if (!w.more) break;
+            // uniform by construction; the reductions tell the compiler so
+            const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
+            if (__reduce_max_sync(0xffffffffu, w.split))
+                dealt(n0 + n1);
+            else
+                both(n0, n1);
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
@@ -323,79 +389,88 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + t * 128;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
-        int sn = 0, on = 0, base = 0;
+        int sn = 0, on = 0, xn = 0, base = 0;
         bool seen = true;  // this warp has seen every earlier fill of the ring, as far as it matters for V_0
         for (;;) {
             const Work &w = take();
             if (!w.more) break;
-            const int n = w.n[t], nmax = max(w.n[0], w.n[1]);
-            const int item_tok = t * TB + tok;          // token of the item
+            const int n = w.n[t], dealt = w.split, tiles = w.tiles;
+            const int item_tok = (dealt ? 0 : t * TB) + tok;  // token of the item
             const bool valid = tok < TB && item_tok < w.nt;
             typename P::RowInfo ri = policy.row_info(w, valid ? item_tok : 0);
-            const bool releases = t == (w.n[1] > 0 ? 1 : 0);
+            // of two row tiles' pipelines the second is the last reader of a key tile
+            const bool releases = dealt || t == (w.n[1] > 0 ? 1 : 0);
+            if (dealt) seen = false;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
-                const bool masked = j >= w.mask_from[t];
-                if (masked) {
-                    // Non-finite values of this tile: zero (and noted, if their keys exist).  The wait
-                    // for V tells its fill from the slot's one before only if that one has been
-                    // seen: S_t(j - 1) and O_t say so, but not for tiles that these rows skipped.
-                    if (j == 0 && !seen) wait(&s_full[t], (uint32_t)(sn & 1));
-                    const int iv = base + 2 * j + 1, vs = iv % NS;
-                    wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
-                    uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
-                    const int kb = w.k0 + j * kKeys;
+                const int kt = dealt ? 2 * j + t : j, k_at = base + 2 * kt;  // key tile, ring index of its K
+                const bool masked = kt >= w.mask_from[t];
+                // The look through V comes before S_t(j) (it costs nothing there), except where the slot's
+                // fill before V has not been seen by then (a wait tells only successive fills apart)
+                // or is given back with S_t(j).
+                const bool late = dealt || (j == 0 && !seen);
 #pragma unroll 1
-                    for (int i0 = quad * 32 + lane; i0 < C::kTile / 16; i0 += 512) {
-                        uint4 x[4];
-                        uint32_t any = 0;
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) x[u] = v[i0 + u * 128];
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            any |= nonfinite_bits(x[u].x) | nonfinite_bits(x[u].y) | nonfinite_bits(x[u].z) |
-                                   nonfinite_bits(x[u].w);
-                        if (any) {
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (masked && pass == (late ? 1 : 0)) {
+                        // Non-finite values of this tile: zero (and noted, if their keys exist)
+                        const int iv = k_at + 1, vs = iv & (NS - 1);
+                        wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
+                        uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
+                        const int kb = w.k0 + kt * kKeys;
 #pragma unroll 1
-                            for (int i = i0; i < i0 + 512; i += 128) {
-                                uint4 y = v[i];
-                                const uint32_t b0 = nonfinite_bits(y.x), b1 = nonfinite_bits(y.y),
-                                               b2 = nonfinite_bits(y.z), b3 = nonfinite_bits(y.w);
-                                if (!(b0 | b1 | b2 | b3)) continue;
-                                if (kb + ((i >> 3) & 127) < w.exist) {
-                                    s_bad = 1;
-                                    __threadfence_block();
+                        for (int i0 = quad * 32 + lane; i0 < C::kTile / 16; i0 += 512) {
+                            uint4 x[4];
+                            uint32_t any = 0;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) x[u] = v[i0 + u * 128];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                any |= nonfinite_bits(x[u].x) | nonfinite_bits(x[u].y) | nonfinite_bits(x[u].z) |
+                                       nonfinite_bits(x[u].w);
+                            if (any) {
+#pragma unroll 1
+                                for (int i = i0; i < i0 + 512; i += 128) {
+                                    uint4 y = v[i];
+                                    const uint32_t b0 = nonfinite_bits(y.x), b1 = nonfinite_bits(y.y),
+                                                   b2 = nonfinite_bits(y.z), b3 = nonfinite_bits(y.w);
+                                    if (!(b0 | b1 | b2 | b3)) continue;
+                                    if (kb + C::row_of(i) < w.exist) {
+                                        s_bad = 1;
+                                        __threadfence_block();
+                                    }
+                                    // (bit >> 15) * 0xffff: the whole half
+                                    y.x &= ~((b0 >> 15) * 0xffffu);
+                                    y.y &= ~((b1 >> 15) * 0xffffu);
+                                    y.z &= ~((b2 >> 15) * 0xffffu);
+                                    y.w &= ~((b3 >> 15) * 0xffffu);
+                                    v[i] = y;
                                 }
-                                // (bit >> 15) * 0xffff: the whole half
-                                y.x &= ~((b0 >> 15) * 0xffffu);
-                                y.y &= ~((b1 >> 15) * 0xffffu);
-                                y.z &= ~((b2 >> 15) * 0xffffu);
-                                y.w &= ~((b3 >> 15) * 0xffffu);
-                                v[i] = y;
                             }
                         }
+                        fence_proxy_async_smem();
                     }
-                    fence_proxy_async_smem();
-                }
-                wait(&s_full[t], (uint32_t)(sn & 1));
-                ++sn;
-                if (lane == 0 && quad == 0) {
-                    // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
-                    // before it are, once the later row tile's products are through
-                    if (j + 1 == n) mbar_arrive_relaxed(&q_empty[t]);
-                    if (releases) {
-                        mbar_arrive_relaxed(&kv_empty[(base + 2 * j) % NS]);
-                        if (j > 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * j - 1) % NS]);
+                    if (pass == 0) {
+                        wait(&s_full[t], (uint32_t)(sn & 1));
+                        ++sn;
+                        if (lane == 0 && quad == 0) {
+                            // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
+                            // before it are, once the later row tile's products are through
+                            if (j + 1 == n) mbar_arrive_relaxed(&q_empty[t]);
+                            if (releases) {
+                                mbar_arrive_relaxed(&kv_empty[k_at & (NS - 1)]);
+                                if (j > 0 && !dealt) mbar_arrive_relaxed(&kv_empty[(k_at - 1) & (NS - 1)]);
+                            }
+                        }
+                        tc::fence_after_sync();
                     }
                 }
-                tc::fence_after_sync();
                 uint32_t s[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::tmem_ld32(ts + q * 32, s[q]);
                 tc::tmem_wait_ld();
                 if (masked) {
                     uint32_t vis[4];
-                    policy.visible(w, ri, j, vis);
+                    policy.visible(w, ri, kt, vis);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         if (__any_sync(0xffffffffu, vis[q] != 0xffffffffu)) {
@@ -461,12 +536,53 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (n > 0) {
                 wait(&o_full[t], (uint32_t)(on & 1));
                 ++on;
-                if (releases && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) % NS]);
+                if (releases && !dealt && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) & (NS - 1)]);
                 tc::fence_after_sync();
+            }
+            float f0 = 1.f, f1 = 0.f;  // factors of O_0 and O_1 in a joint result
+            const bool join = dealt && w.n[1] > 0;
+            if (join) {
+                if (t == 1) {  // hand over; O_1 stays as it is until it has been read
+                    s_x[row] = make_float2(m, l);
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_full);
+                    wait(&x_empty, (uint32_t)(xn & 1));
+                } else {
+                    wait(&x_full, (uint32_t)(xn & 1));
+                    tc::fence_after_sync();
+                    const float2 o = s_x[row];
+                    const float mj = fmaxf(m, o.x), ref = mj == -INFINITY ? 0.f : mj;
+                    f0 = ex2((m - ref) * c);
+                    f1 = ex2((o.x - ref) * c);
+                    l = l * f0 + o.y * f1;
+                    m = mj;
+                }
+                ++xn;
+            }
+            if (n > 0 && !(join && t == 1)) {
                 const bool bad = s_bad != 0;
                 // this lane's row of the output (null: not a row), and a factor
                 float inv;
                 unsigned char *dst = policy.begin_row(w, item_tok, head, valid, m, l, inv);
+                if (join) {
+                    // O_0 <- f0 O_0 + f1 O_1
+#pragma unroll 1
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t x[16], y[16];
+                        tc::tmem_ld16(to + q * 16, x);
+                        tc::tmem_ld16(to + D + q * 16, y);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = __float_as_uint(__uint_as_float(x[i]) * f0 + __uint_as_float(y[i]) * f1);
+                        tc::tmem_st16(to + q * 16, x);
+                    }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_empty);
+                }
                 const bool f32 = policy.partial(w);
                 unsigned char *stage = sm_out + (warp - 2) * C::kOut;
                 if (__any_sync(0xffffffffu, bad && valid)) {
@@ -541,8 +657,8 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             } else {
                 give_back();
             }
-            base += 2 * nmax;
-            seen = n >= nmax - 1;
+            base += 2 * tiles;
+            seen = !dealt && n >= tiles - 1;
         }
     }
     tc::fence_before_sync();

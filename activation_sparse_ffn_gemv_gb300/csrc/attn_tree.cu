@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
 // ---------------------------------------------------------------------------
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 4 : 8>;
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, true>;
 
 template <int D>
 struct TreePolicy {
@@ -131,8 +131,10 @@ struct TreePolicy {
         w.nt = min(a.tile_tokens, q.n - tk0);
         w.k0 = k0;
         w.k1 = w.exist = k1;
-        w.n[0] = n;
-        w.n[1] = w.nt > TB ? n : 0;
+        w.tiles = n;
+        w.split = w.nt <= TB;
+        w.n[0] = w.split ? (n + 1) / 2 : n;
+        w.n[1] = w.split ? n / 2 : n;
         w.mask_from[0] = w.mask_from[1] = max(0, min(q.ctx, k1) - k0) / atc::kKeys;
         w.ctx = q.ctx;
         w.seq = s;
@@ -141,25 +143,33 @@ struct TreePolicy {
         w.slot = 2 * blockIdx.x + (un0 > 0 ? 0 : 1);
         return true;
     }
-    // Row of the cache (head h's) that holds key `key`; past the end if its page is not one.
-    SFFN_DEV long long cache_row(const atc::Work &w, int key) const {
-        const int pg = a.page_table[(size_t)w.seq * a.table_width + (key >> a.page_shift)];
+    SFFN_DEV int page_of(const atc::Work &w, int key) const {
+        return a.page_table[(size_t)w.seq * a.table_width + (key >> a.page_shift)];
+    }
+    // Row of the cache (head h's) that holds key `key`, on page pg; past the end if that is not one.
+    SFFN_DEV long long cache_row(const atc::Work &w, int key, int pg) const {
         if (pg < 0 || pg >= a.n_pages) {
             record_error(a.err, SFFN_ERR_DEVICE);
             return ((long long)a.n_pages * a.n_kv_heads) << a.page_shift;
         }
         return (((long long)pg * a.n_kv_heads + w.h) << a.page_shift) + (key & ((1 << a.page_shift) - 1));
     }
-    SFFN_DEV void load_kv(const atc::Work &w, int j, const CUtensorMap *map, unsigned char *dst, uint64_t *bar, int lane,
-                          uint64_t pol) const {
+    // Page of this lane's part of key tile j, a box of `box` rows (16 boxes at most); looked up a
+    // tile ahead of its use.
+    SFFN_DEV int place(const atc::Work &w, int j, int lane) const {
+        const int off = j * atc::kKeys + lane * box;
+        return lane * box < atc::kKeys && off < w.k1 - w.k0 ? page_of(w, w.k0 + off) : 0;
+    }
+    SFFN_DEV void load_kv(const atc::Work &w, int j, int pg, const CUtensorMap *map, unsigned char *dst, uint64_t *bar,
+                          int lane, uint64_t pol) const {
         constexpr int H = Cfg<D>::kHalves;
-        const int kb = w.k0 + j * atc::kKeys, left = min(atc::kKeys, w.k1 - kb);
-        const int boxes = (left + box - 1) / box, b = lane / H, c = lane % H;  // boxes <= 16
-        int row = 0;
-        if (b < boxes) row = (int)cache_row(w, kb + b * box);
+        const int kb = w.k0 + j * atc::kKeys, left = min(atc::kKeys, w.k1 - kb), boxes = (left + box - 1) / box;
         if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * H));
         __syncwarp();
-        if (b < boxes) tc::tma_load_2d(dst + c * Cfg<D>::kBlock + b * box * 128, map, c * 64, row, bar, pol);
+        if (lane < boxes) {
+            const int row = (int)cache_row(w, kb + lane * box, pg);
+            tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, row >> 3, bar, pol);
+        }
     }
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
         const int i = w.tok0 + tok;
@@ -180,7 +190,7 @@ struct TreePolicy {
     }
     SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &r, int key) const {
         if (key >= w.ctx && !((r.mask >> (key - w.ctx)) & 1)) return nullptr;
-        const long long row = cache_row(w, key);
+        const long long row = cache_row(w, key, page_of(w, key));
         if (row >= ((long long)a.n_pages * a.n_kv_heads) << a.page_shift) return nullptr;
         return static_cast<const uint16_t *>(a.cv) + (size_t)row * D;
     }
@@ -208,8 +218,7 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ long long scratch[33];
     TreePolicy<D> policy(a, reinterpret_cast<long long *>(smem_raw), scratch);
-    atc::attention_cta<D, Cfg<D>::kStages>(policy, map_q, map_k, map_v, a.scale, a.group, a.err,
-                                           smem_raw + kPrefixBytes);
+    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw + kPrefixBytes);
 }
 
 // Joins the pieces of cut items: for each row, M = max of the pieces' maxima,
@@ -292,10 +301,12 @@ sffn_status launch_tree_bf16(const TreeArgs &a, int grid, cudaStream_t s) {
     const int G = a.group, TB = 128 / G, ps = 1 << a.page_shift;
     CUtensorMap mq, mk, mv;
     const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, sq[2] = {D * 2, (uint64_t)a.q_stride * 2};
-    const uint64_t dk[2] = {D, (uint64_t)a.n_pages * a.n_kv_heads * ps}, sk[1] = {D * 2};
-    const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[2] = {64, (uint32_t)(ps < 64 ? ps : 64)};
-    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 2, dk, sk, bk) ||
-        !make_map_bf16(&mv, a.cv, 2, dk, sk, bk))
+    // the cache as [8-row group][column block][row][64]: a box is a page's rows (64 at most), all columns
+    const uint64_t dk[4] = {64, 8, D / 64, (uint64_t)a.n_pages * a.n_kv_heads * ps / 8},
+                   sk[3] = {D * 2, 128, D * 16};
+    const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[4] = {64, 8, D / 64, (uint32_t)(ps < 64 ? ps : 64) / 8};
+    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 4, dk, sk, bk) ||
+        !make_map_bf16(&mv, a.cv, 4, dk, sk, bk))
         return SFFN_ERR_UNSUPPORTED;
     constexpr int smem = Cfg<D>::kSmem + (int)kPrefixBytes;
     cudaError_t e = set_max_smem((const void *)k_tree_tc<D>, smem);

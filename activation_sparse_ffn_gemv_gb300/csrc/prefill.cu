@@ -536,8 +536,8 @@ bool make_map_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *d
                    const uint32_t *box) {
     PFN_encodeTiled enc = get_encode();
     if (!enc) return false;
-    const cuuint32_t es[3] = {1, 1, 1};
-    cuuint64_t d[3], st[2];
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    cuuint64_t d[4], st[3];
     for (int i = 0; i < rank; ++i) d[i] = dims[i];
     for (int i = 0; i + 1 < rank; ++i) st[i] = strides[i];
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), d, st, box, es,

@@ -29,6 +29,16 @@ SFFN_DEV void tma_load_3d(void *smem_dst, const CUtensorMap *map, int x, int y, 
         : "memory");
 }
 
+// 4-D tile load.
+SFFN_DEV void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y, int z, int u, uint64_t *bar,
+                          uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(smem_dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+
 SFFN_DEV void prefetch_tensormap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -180,7 +190,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
 
 }  // namespace tc
 
-// Host: 128-byte swizzled tensor map of a bf16 tensor of `rank` (2 or 3) dimensions, innermost
+// Host: 128-byte swizzled tensor map of a bf16 tensor of `rank` (2 to 4) dimensions, innermost
 // first; strides in bytes from the second dimension on; out-of-range elements read as zero.
 // False when the driver refuses it.
 bool make_map_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
