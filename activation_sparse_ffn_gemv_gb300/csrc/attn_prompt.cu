@@ -19,7 +19,7 @@ namespace sffn {
 namespace {
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false>;  // 208 KB and 176 KB of shared memory
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false, false>;  // 208 KB and 176 KB of shared memory
 
 template <int D>
 struct PromptPolicy {

@@ -45,13 +45,15 @@ constexpr float kLazyLog2 = 8.f;             // the running maximum moves when p
 // GROUPED: layout of the K and V tiles in shared memory.  false: column block by column block
 // (a TMA box is 128 rows of one block).  true: by groups of 8 rows, each with its column blocks in
 // turn, so that any multiple of 8 rows with all its columns is one box (a page).
-template <int D, int STAGES, bool GROUPED>
+// ONE: every item has one row tile (both pipelines read the same Q_0; the memory goes to the ring).
+template <int D, int STAGES, bool GROUPED, bool ONE>
 struct Cfg {
     static constexpr int kHalves = D / 64;                      // 64-element (128-byte) column blocks
     static constexpr int kBlock = 128 * 128;                    // bytes of a column block: 128 rows x 128 bytes
     static constexpr int kTile = kHalves * kBlock;              // Q, K or V tile
     static constexpr int kStages = STAGES;                      // K and V tiles of the ring
-    static_assert((STAGES & (STAGES - 1)) == 0, "ring indexes are masked");
+    static constexpr bool kOne = ONE;
+    static constexpr int kQ = ONE ? 1 : 2;
     static constexpr bool kGrouped = GROUPED;
     static constexpr int kRows8 = GROUPED ? kHalves * 1024 : 1024;  // bytes from 8 rows to the next 8
     static constexpr int kColBlock = GROUPED ? 1024 : kBlock;       // bytes from a column block to the next
@@ -59,7 +61,7 @@ struct Cfg {
     SFFN_DEV static int row_of(int i) { return GROUPED ? (i / (64 * kHalves)) * 8 + ((i >> 3) & 7) : (i >> 3) & 127; }
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
     static constexpr int kOut = 2048;                           // a softmax warp's: 64 bytes of its 32 output rows
-    static constexpr int kSmem = (2 + kStages) * kTile + 8 * kOut + 1024 /*alignment*/;
+    static constexpr int kSmem = (kQ + kStages) * kTile + (ONE ? 4 : 8) * kOut + 1024 /*alignment*/;
 };
 
 // One item.  The loading warp finds the items and describes them in a small ring.
@@ -134,8 +136,8 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 template <typename C, int D, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
                             float scale, int G, int32_t *err, unsigned char *smem_raw) {
-    const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + 2 * C::kTile;
-    unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + 2 * C::kTile,
+    const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + C::kQ * C::kTile;
+    unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + C::kQ * C::kTile,
                   *sm_out = sm_kv + C::kStages * C::kTile;
     constexpr int NS = C::kStages;
     __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone,
@@ -236,7 +238,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 const int nxt = j + 1 < tiles ? policy.place(w, j + 1, lane) : 0;  // a tile ahead
                 for (int part = 0; part < 2; ++part) {
                     // the item's queries: the first tile's before the first K, the second's after it
-                    if (j == 0 && w.n[part] > 0) {
+                    if (j == 0 && w.n[part] > 0 && part < C::kQ) {
                         wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1));
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
@@ -267,7 +269,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint64_t hi_q = tc::smem_desc_sw128(0, 16, 1024), hi_k = tc::smem_desc_sw128(0, 16, C::kRows8),
                        hi_v = tc::smem_desc_sw128(0, C::kColBlock, C::kRows8);
         auto scores = [&](int t, uint32_t tile) {  // S_t = Q_t K^T
-            const uint64_t a = hi_q | ((q_addr + t * C::kTile) >> 4), b = hi_k | (tile >> 4);
+            const uint64_t a = hi_q | ((q_addr + (C::kOne ? 0 : t) * C::kTile) >> 4), b = hi_k | (tile >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
                 tc::mma_bf16_warp(tmem + t * 128, a + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4),
@@ -288,8 +290,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         };
         auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
         auto first_scores = [&](int t) {
-            wait(&q_full[t], q_par[t]);
-            q_par[t] ^= 1;
+            if (t < C::kQ) {
+                wait(&q_full[t], q_par[t]);
+                q_par[t] ^= 1;
+            }
             tc::fence_after_sync();
             scores(t, tile_of(slot));
         };
@@ -340,6 +344,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 first_scores(1);
                 step();
             }
+            if (C::kOne && tiles <= 2) tc::mma_commit_warp(&q_empty[0]);
             for (int i = 0; i < tiles; i += 2) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -357,6 +362,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                             tc::fence_after_sync();
                             scores(t, tile_of(slot));
                             step();
+                            if (C::kOne && i + t + 3 == tiles) tc::mma_commit_warp(&q_empty[0]);
                         } else {
                             tc::mma_commit_warp(&o_full[t]);
                         }
@@ -371,10 +377,14 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (!w.more) break;
             // uniform by construction; the reductions tell the compiler so
             const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
-            if (__reduce_max_sync(0xffffffffu, w.split))
+            if constexpr (C::kOne) {
                 dealt(n0 + n1);
-            else
-                both(n0, n1);
+            } else {
+                if (__reduce_max_sync(0xffffffffu, w.split))
+                    dealt(n0 + n1);
+                else
+                    both(n0, n1);
+            }
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
@@ -394,7 +404,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         for (;;) {
             const Work &w = take();
             if (!w.more) break;
-            const int n = w.n[t], dealt = w.split, tiles = w.tiles;
+            const int n = w.n[t], dealt = C::kOne ? 1 : w.split, tiles = w.tiles;
             const int item_tok = (dealt ? 0 : t * TB) + tok;  // token of the item
             const bool valid = tok < TB && item_tok < w.nt;
             typename P::RowInfo ri = policy.row_info(w, valid ? item_tok : 0);
@@ -413,7 +423,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 for (int pass = 0; pass < 2; ++pass) {
                     if (masked && pass == (late ? 1 : 0)) {
                         // Non-finite values of this tile: zero (and noted, if their keys exist)
-                        const int iv = k_at + 1, vs = iv & (NS - 1);
+                        const int iv = k_at + 1, vs = iv % NS;
                         wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
                         uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
                         const int kb = w.k0 + kt * kKeys;
@@ -455,10 +465,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         if (lane == 0 && quad == 0) {
                             // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
                             // before it are, once the later row tile's products are through
-                            if (j + 1 == n) mbar_arrive_relaxed(&q_empty[t]);
+                            if (!C::kOne && j + 1 == n) mbar_arrive_relaxed(&q_empty[t]);
                             if (releases) {
-                                mbar_arrive_relaxed(&kv_empty[k_at & (NS - 1)]);
-                                if (j > 0 && !dealt) mbar_arrive_relaxed(&kv_empty[(k_at - 1) & (NS - 1)]);
+                                mbar_arrive_relaxed(&kv_empty[k_at % NS]);
+                                if (j > 0 && !dealt) mbar_arrive_relaxed(&kv_empty[(k_at - 1) % NS]);
                             }
                         }
                         tc::fence_after_sync();
@@ -536,7 +546,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (n > 0) {
                 wait(&o_full[t], (uint32_t)(on & 1));
                 ++on;
-                if (releases && !dealt && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) & (NS - 1)]);
+                if (releases && !dealt && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) % NS]);
                 tc::fence_after_sync();
             }
             float f0 = 1.f, f1 = 0.f;  // factors of O_0 and O_1 in a joint result
@@ -584,7 +594,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     if (lane == 0) mbar_arrive(&x_empty);
                 }
                 const bool f32 = policy.partial(w);
-                unsigned char *stage = sm_out + (warp - 2) * C::kOut;
+                unsigned char *stage = sm_out + (C::kOne ? quad : warp - 2) * C::kOut;
                 if (__any_sync(0xffffffffu, bad && valid)) {
                     // the masked tiles' non-finite values that this row sees
                     const int from = w.k0 + min(w.mask_from[0], w.mask_from[1]) * kKeys;

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
 // ---------------------------------------------------------------------------
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, true>;
+using Cfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
 
 template <int D>
 struct TreePolicy {
@@ -132,9 +132,9 @@ struct TreePolicy {
         w.k0 = k0;
         w.k1 = w.exist = k1;
         w.tiles = n;
-        w.split = w.nt <= TB;
-        w.n[0] = w.split ? (n + 1) / 2 : n;
-        w.n[1] = w.split ? n / 2 : n;
+        w.split = 1;
+        w.n[0] = (n + 1) / 2;
+        w.n[1] = n / 2;
         w.mask_from[0] = w.mask_from[1] = max(0, min(q.ctx, k1) - k0) / atc::kKeys;
         w.ctx = q.ctx;
         w.seq = s;
@@ -321,7 +321,7 @@ TreePlan make_tree_plan(int dtype, int T, int n_heads, int n_kv_heads, int head_
     TreePlan p = {};
     const int G = n_heads / n_kv_heads;
     p.grid = device_sm_count();
-    p.tile_tokens = dtype == SFFN_BF16 ? 2 * (128 / G) : rows::kRows / G;
+    p.tile_tokens = (dtype == SFFN_BF16 ? 128 : rows::kRows) / G;
     int tokens = T < kTreeMaxTokens ? T : kTreeMaxTokens;
     if (tokens > p.tile_tokens) tokens = p.tile_tokens;
     p.rows_max = tokens * G;
