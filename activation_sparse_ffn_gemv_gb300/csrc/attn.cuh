@@ -11,22 +11,27 @@ namespace sffn {
 // How sffn_attn_tree's work is split
 //
 // A sequence's new tokens are cut into row tiles of `tile_tokens` tokens (times
-// the G query heads of a key head: one row each).  An item is a (sequence, row
-// tile, key head); it reads ceil(positions / 64) units of 64 cached positions.  All
-// items' units form one line, sequence by sequence; CTA w of W takes the units
-// [w total / W, (w + 1) total / W) of it, whatever the lengths.  An item that lies in
-// one CTA's range is finished there; the pieces of a cut item are written as
-// partial results (unnormalised output, running maximum and sum) and joined by
+// the G query heads of a key head: one row each).  An item is a (sequence, key head,
+// row tile); it reads ceil(positions / 64) units of 64 cached positions.  On one line, item
+// after item, each takes its units and kTreeItemCost more in front of them for what an
+// item costs by itself; CTA w of W takes [w total / W, (w + 1) total / W) of the line, whatever
+// the lengths.  (A batch of 48 sequences, some of them a few positions long: 132 us
+// without the extra cost, because one CTA got all the short items of a sequence group.)  Row tiles of
+// one key head are neighbours, so that they read its keys at about the same time.  An
+// item whose units lie in one CTA's range is finished there; the pieces of a cut item are
+// written as partial results (unnormalised output, running maximum and sum) and joined by
 // k_tree_join in the order of the CTAs.  The cut depends on the lengths alone.
 // ---------------------------------------------------------------------------
 
 constexpr int kTreeUnit = 64;
+constexpr int kTreeItemCost = 4;
 constexpr int kTreeMaxTokens = 64;
 constexpr int kTreeMaxCtx = 0x7fff0000;  // positions stay below 2^31 with room for a tile
 
 struct TreeSeq {
     int t0, n, ctx;   // first new token, new tokens, committed positions
     int tiles, units; // row tiles, units of each item
+    SFFN_DEV int span() const { return units + kTreeItemCost; }  // an item's length on the line
 };
 
 // A sequence's numbers, checked; one that breaks the contract has no rows.
@@ -49,7 +54,7 @@ SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
     return q;
 }
 
-// pre[s] = units before sequence s, pre[n_seq] = all (shared memory, every thread of
+// pre[s] = length of the line before sequence s, pre[n_seq] = all of it (shared memory, every thread of
 // the CTA takes part; scratch: >= 33 long longs).
 SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch, bool record) {
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = nt >> 5;
@@ -59,7 +64,7 @@ SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch,
         long long v = 0;
         if (s < a.n_seq) {
             const TreeSeq q = tree_seq(a, s, record);
-            v = (long long)q.tiles * a.n_kv_heads * q.units;
+            v = (long long)q.tiles * a.n_kv_heads * q.span();
         }
         long long incl = v;
 #pragma unroll
@@ -82,7 +87,7 @@ SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch,
     __syncthreads();
 }
 
-// Last sequence s with pre[s] <= u (u < pre[n_seq]): the one that unit u belongs to.
+// Last sequence s with pre[s] <= u (u < pre[n_seq]): the one that place u of the line belongs to.
 SFFN_DEV int tree_find(const long long *pre, int n_seq, long long u) {
     int lo = 0, hi = n_seq;  // pre[lo] <= u < pre[hi]
     while (hi - lo > 1) {
@@ -92,13 +97,33 @@ SFFN_DEV int tree_find(const long long *pre, int n_seq, long long u) {
     return lo;
 }
 
-// CTAs that take part (none of them with an empty range: each slot that the join
-// reads has been written).
+// CTAs that take part: none has an empty range.
 SFFN_HOST_DEV int tree_ctas(long long total, int grid) { return total < grid ? (int)total : grid; }
 
-// First unit of CTA w, and the CTA that unit u falls to.
+// First place of CTA w, and the CTA that place u falls to.
 SFFN_HOST_DEV long long tree_cut(long long total, int w, int W) { return total * w / W; }
 SFFN_HOST_DEV int tree_owner(long long total, long long u, int W) { return (int)(((u + 1) * W - 1) / total); }
+
+// The piece of an item at place u of the line, in a range that ends at u1.
+struct TreePiece {
+    int s, h, tile;  // sequence, key head, row tile
+    int un0, un1;    // units; none if the range ends before the first
+    long long next;  // where the range goes on
+};
+SFFN_DEV TreePiece tree_piece(const TreeArgs &a, const long long *pre, long long u, long long u1, TreeSeq &q) {
+    TreePiece p;
+    p.s = tree_find(pre, a.n_seq, u);
+    q = tree_seq(a, p.s, false);
+    const long long local = u - pre[p.s];
+    const int item = (int)(local / q.span()), at = (int)(local - (long long)item * q.span());
+    p.h = item / q.tiles;
+    p.tile = item - p.h * q.tiles;
+    const int end = (int)min((long long)q.span(), at + (u1 - u));
+    p.un0 = max(0, at - kTreeItemCost);
+    p.un1 = max(0, end - kTreeItemCost);
+    p.next = u + (end - at);
+    return p;
+}
 
 // Partial result slots: a CTA's range cuts at most one item at its front (slot 2 w)
 // and one at its end (slot 2 w + 1).  A slot holds rows_max rows of D floats, then

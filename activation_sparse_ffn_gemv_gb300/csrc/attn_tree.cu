@@ -27,13 +27,12 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
     const long long u1 = tree_cut(total, w + 1, W);
     const int G = a.group, ps = 1 << a.page_shift;
     for (long long u = tree_cut(total, w, W); u < u1;) {
-        const int s = tree_find(pre, a.n_seq, u);
-        const TreeSeq q = tree_seq(a, s, false);
-        const long long local = u - pre[s];
-        const int item = (int)(local / q.units), un0 = (int)(local - (long long)item * q.units);
-        const int un1 = (int)min((long long)q.units, un0 + (u1 - u));
-        const int tile = item / a.n_kv_heads, h = item - tile * a.n_kv_heads;
-        const int tk0 = tile * a.tile_tokens, nt = min(a.tile_tokens, q.n - tk0);
+        TreeSeq q;
+        const TreePiece pc = tree_piece(a, pre, u, u1, q);
+        u = pc.next;
+        if (pc.un0 >= pc.un1) continue;
+        const int s = pc.s, h = pc.h, un0 = pc.un0, un1 = pc.un1;
+        const int tk0 = pc.tile * a.tile_tokens, nt = min(a.tile_tokens, q.n - tk0);
         const int32_t *table = a.page_table + (size_t)s * a.table_width;
         const long long keys = (long long)q.ctx + q.n;
         const long long k0 = (long long)un0 * kTreeUnit, k1 = min(keys, (long long)un1 * kTreeUnit);
@@ -81,7 +80,6 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
                 }
             }
         }
-        u += un1 - un0;
     }
 }
 
@@ -116,17 +114,17 @@ struct TreePolicy {
         u1 = b < W ? tree_cut(total, b + 1, W) : 0;
     }
     SFFN_DEV bool next(atc::Work &w) {
-        if (u >= u1) return false;
-        const int s = tree_find(pre, a.n_seq, u);
-        const TreeSeq q = tree_seq(a, s, false);
-        const long long local = u - pre[s];
-        const int item = (int)(local / q.units), un0 = (int)(local - (long long)item * q.units);
-        const int un1 = (int)min((long long)q.units, un0 + (u1 - u));
-        const int tile = item / a.n_kv_heads, tk0 = tile * a.tile_tokens;
+        TreeSeq q;
+        TreePiece pc;
+        do {
+            if (u >= u1) return false;
+            pc = tree_piece(a, pre, u, u1, q);
+            u = pc.next;
+        } while (pc.un0 >= pc.un1);
+        const int un0 = pc.un0, un1 = pc.un1, s = pc.s, tk0 = pc.tile * a.tile_tokens;
         const int k0 = un0 * kTreeUnit, k1 = min(q.ctx + q.n, un1 * kTreeUnit);
         const int n = (k1 - k0 + atc::kKeys - 1) / atc::kKeys;
-        u += un1 - un0;
-        w.h = item - tile * a.n_kv_heads;
+        w.h = pc.h;
         w.q_row = q.t0 + tk0;
         w.nt = min(a.tile_tokens, q.n - tk0);
         w.k0 = k0;
@@ -224,56 +222,77 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
 // Joins the pieces of cut items: for each row, M = max of the pieces' maxima,
 // out = sum(exp(m_i - M) o_i) / sum(exp(m_i - M) l_i), the pieces in the order of
 // their CTAs.  One warp a row (token, query head).
-constexpr int kJoinWarps = 8;
+// Where a row's pieces are depends on the call's inputs alone, so that is found before the wait
+// for the pieces' kernel (which lets this one start once it has itself waited for the inputs;
+// 128 threads of 40 registers find room beside it); after the wait come one load of all maxima and
+// sums and then the outputs, independent of one another.
+constexpr int kJoinWarps = 4;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_tree_join(const TreeArgs a, int grid) {
+__global__ void __launch_bounds__(32 * kJoinWarps, 12) k_tree_join(const TreeArgs a, int grid) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     long long *pre = reinterpret_cast<long long *>(smem_raw);
     __shared__ long long scratch[33];
-    griddep_wait();
-    griddep_launch_dependents();
     tree_prefix(a, pre, scratch, false);
     const long long total = pre[a.n_seq];
     const int W = tree_ctas(total, grid);
     const int lane = threadIdx.x & 31;
     const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (row >= (long long)a.T * a.n_heads) return;
-    const int t = (int)(row / a.n_heads), hq = (int)(row - (long long)t * a.n_heads);
-    // the sequence of token t: the last one that starts at or before it
-    int lo = 0, hi = a.n_seq;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_tokens[mid] <= t) lo = mid; else hi = mid;
+    int w0 = 0, w1 = 0, r = 0;  // CTAs of the first and the last piece, row within the slots
+    if (row < (long long)a.T * a.n_heads) {
+        const int t = (int)(row / a.n_heads), hq = (int)(row - (long long)t * a.n_heads);
+        // the sequence of token t: the last one that starts at or before it
+        int lo = 0, hi = a.n_seq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (a.cu_tokens[mid] <= t) lo = mid; else hi = mid;
+        }
+        const TreeSeq q = tree_seq(a, lo, false);
+        if (t >= q.t0 && t < q.t0 + q.n) {
+            const int G = a.group, h = hq / G, tile = (t - q.t0) / a.tile_tokens;
+            r = (t - q.t0 - tile * a.tile_tokens) * G + hq - h * G;
+            const long long i0 = pre[lo] + ((long long)h * q.tiles + tile) * q.span();
+            w0 = tree_owner(total, i0 + kTreeItemCost, W);
+            w1 = tree_owner(total, i0 + q.span() - 1, W);
+        }
     }
-    const TreeSeq q = tree_seq(a, lo, false);
-    if (t < q.t0 || t >= q.t0 + q.n) return;
-    const int G = a.group, h = hq / G, tile = (t - q.t0) / a.tile_tokens;
-    const int r = (t - q.t0 - tile * a.tile_tokens) * G + hq - h * G;
-    const long long i0 = pre[lo] + ((long long)tile * a.n_kv_heads + h) * q.units, i1 = i0 + q.units;
-    const int w0 = tree_owner(total, i0, W), w1 = tree_owner(total, i1 - 1, W);
-    if (w0 == w1) return;  // finished by its one CTA
+    griddep_wait();
+    griddep_launch_dependents();
+    if (w0 == w1) return;  // finished by its one CTA, or not a row
     const size_t sf = tree_slot_floats(a.rows_max, D);
     auto slot = [&](int w) { return a.part + sf * (size_t)(2 * w + (w == w0 ? 1 : 0)); };
-    float M = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) M = fmaxf(M, slot(w)[(size_t)a.rows_max * D + 2 * r]);
-    M = warp_max(M);
-    const float ref = M == -INFINITY ? 0.f : M;
-    float o[D / 32], l = 0.f;
+    constexpr int C = D / 32;  // columns of a lane
+    float o[C], l = 0.f, M = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
-    for (int w = w0; w <= w1; ++w) {
-        const float *p = slot(w), *ml = p + (size_t)a.rows_max * D + 2 * r;
-        const float m = ml[0], f = expf(m - ref);
-        if (m == -INFINITY && ml[1] == 0.f) continue;  // a piece without a key that this row sees
-        l += f * ml[1];
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+    for (int wb = w0; wb <= w1; wb += 32) {  // 32 pieces at a time
+        const int n = min(32, w1 - wb + 1);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(slot(wb + lane) + (size_t)a.rows_max * D + 2 * r));
+        const float Mn = fmaxf(M, warp_max(ml.x)), ref = Mn == -INFINITY ? 0.f : Mn;
+        // a piece without a key that this row sees has no weight
+        const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : expf(ml.x - ref), keep = expf(M - ref);
+        l = l * keep + warp_sum(f * ml.y);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] += f * p[(size_t)r * D + lane * (D / 32) + i];
+        for (int i = 0; i < C; ++i) o[i] *= keep;
+        M = Mn;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float *p = slot(wb + k) + (size_t)r * D + lane * C;
+            if constexpr (C == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+                o[0] += fk * x.x, o[1] += fk * x.y, o[2] += fk * x.z, o[3] += fk * x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+                o[0] += fk * x.x, o[1] += fk * x.y;
+            }
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    T *dst = static_cast<T *>(a.out) + (size_t)row * D + lane * (D / 32);
+    T *dst = static_cast<T *>(a.out) + (size_t)row * D + lane * C;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < C; ++i) {
         if constexpr (sizeof(T) == 4) dst[i] = o[i] * inv;
         else dst[i] = __float2bfloat16_rn(o[i] * inv);
     }

@@ -71,7 +71,7 @@ SFFN_DEV void load8(const float *p, float (&f)[8]) {
 }
 
 template <typename T, int D, int U>
-__global__ void __launch_bounds__(32 * kRopeWarps) k_qk_norm_rope(const RopeArgs a) {
+__global__ void __launch_bounds__(32 * kRopeWarps, 6) k_qk_norm_rope(const RopeArgs a) {
     constexpr int LPH = D / 8;       // lanes of a row
     constexpr int RPW = 32 / LPH;    // rows of a warp at a time
     griddep_wait();
@@ -80,117 +80,133 @@ __global__ void __launch_bounds__(32 * kRopeWarps) k_qk_norm_rope(const RopeArgs
     const int hkv = a.hkv, hqk = a.hq + hkv;
     const int rows = hqk + (a.ck ? hkv : 0);  // rows of a token: q, k, and v for the cache
     const int chunks = (rows + RPW * U - 1) / (RPW * U);
-    const long long item = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
-    if (item >= (long long)a.T * chunks) return;
-    const int t = (int)(item / chunks), c = (int)(item - (long long)t * chunks);
-    int p = 0;
-    if (a.rot) {
-        p = a.positions[t];
-        if (p < 0 || p >= a.max_pos) {
+    // below 2^31: at most 2^20 tokens of 1536 chunks
+    const unsigned items = (unsigned)a.T * (unsigned)chunks, stride = gridDim.x * kRopeWarps;
+    unsigned item = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+
+    // Rows, position and slot of an item; the next item's are on their way while this one is worked
+    // on (in an in-place call too: no warp writes another's rows).
+    struct In {
+        Row8<T> x[U];
+        int t, c, p, slot;
+    };
+    auto fetch = [&](unsigned it, In &in) {
+        const int t = (int)(it / (unsigned)chunks), c = (int)(it - (unsigned)t * (unsigned)chunks);
+        in.t = t;
+        in.c = c;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = (c * U + u) * RPW + grp;
+            const T *src = nullptr;
+            if (r < a.hq)
+                src = static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)r * D;
+            else if (r < hqk)
+                src = static_cast<const T *>(a.k) + (size_t)t * a.k_stride + (size_t)(r - a.hq) * D;
+            else if (r < rows)
+                src = static_cast<const T *>(a.v) + (size_t)t * a.v_stride + (size_t)(r - hqk) * D;
+            if (src)
+                in.x[u].load(src + l * 8);
+            else
+                in.x[u].zero();
+        }
+        in.p = a.rot ? a.positions[t] : 0;
+        in.slot = a.ck ? a.slots[t] : -1;
+    };
+    In in;
+    if (item < items) fetch(item, in);
+    for (; item < items; item += stride) {
+        Row8<T> x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = in.x[u];
+        const int t = in.t, c = in.c, p = in.p, slot = in.slot;
+        if (item + stride < items) fetch(item + stride, in);
+        if (a.rot && (p < 0 || p >= a.max_pos)) {
             if (lane == 0) record_error(a.err, SFFN_ERR_DEVICE);
-            return;
+            continue;
         }
-    }
-
-    Row8<T> x[U];
+        // this lane's cosines and sines (of 8 pairs with half-split, of 4 with interleaved pairs)
+        float cs[8], sn[8];
+        const bool turns = l * 8 < a.rot;
+        const bool low = l * 16 < a.rot;  // half-split: this lane holds the pairs' first elements
+        const int half = a.rot / 2;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int r = (c * U + u) * RPW + grp;
-        const T *src = nullptr;
-        if (r < a.hq)
-            src = static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)r * D;
-        else if (r < hqk)
-            src = static_cast<const T *>(a.k) + (size_t)t * a.k_stride + (size_t)(r - a.hq) * D;
-        else if (r < rows)
-            src = static_cast<const T *>(a.v) + (size_t)t * a.v_stride + (size_t)(r - hqk) * D;
-        if (src)
-            x[u].load(src + l * 8);
-        else
-            x[u].zero();
-    }
-    // this lane's cosines and sines (of 8 pairs with half-split, of 4 with interleaved pairs)
-    float cs[8], sn[8];
-    const bool turns = l * 8 < a.rot;
-    const bool low = l * 16 < a.rot;  // half-split: this lane holds the pairs' first elements
-    const int half = a.rot / 2;
+        for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
+        if (turns) {
+            const float *row = a.table + (size_t)p * a.rot;
+            if (a.style == SFFN_ROPE_HALF) {
+                const int i0 = low ? l * 8 : l * 8 - half;
+                load8(row + i0, cs);
+                load8(row + half + i0, sn);
+                if (low) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = 1.f, sn[i] = 0.f;
-    if (turns) {
-        const float *row = a.table + (size_t)p * a.rot;
-        if (a.style == SFFN_ROPE_HALF) {
-            const int i0 = low ? l * 8 : l * 8 - half;
-            load8(row + i0, cs);
-            load8(row + half + i0, sn);
-            if (low) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // first element: a cos - b sin
-            }
-        } else {
-            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + l * 4));
-            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + l * 4));
-            cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
-            sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
-        }
-    }
-    // lane of the pair's other half (half-split); itself when nothing turns
-    const int partner = !turns ? lane : (low ? lane + a.rot / 16 : lane - a.rot / 16);
-
-    // where the token's cache rows go
-    long long crow = -1;  // row index of head 0 at this token's slot
-    if (a.ck) {
-        const int slot = a.slots[t];
-        const int pg = slot >> a.page_shift;
-        if (slot >= 0 && pg < a.n_pages)
-            crow = (((long long)pg * hkv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
-        else if (slot != -1 && lane == 0)
-            record_error(a.err, SFFN_ERR_DEVICE);
-    }
-
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int r = (c * U + u) * RPW + grp;
-        float f[8];
-        x[u].get(f);
-        const void *w = r < a.hq ? a.q_weight : a.k_weight;
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (w && r < hqk) {
-            Row8<T> wr;
-            wr.load(static_cast<const T *>(w) + l * 8);
-            float wf[8];
-            wr.get(wf);
-            const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * wf[i];
-        }
-        float y[8];
-        if (a.style == SFFN_ROPE_HALF) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float o = __shfl_sync(0xffffffffu, f[i], partner);
-                y[i] = turns ? f[i] * cs[i] + o * sn[i] : f[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float e0 = f[2 * i], e1 = f[2 * i + 1];
-                y[2 * i] = turns ? e0 * cs[i] - e1 * sn[i] : e0;
-                y[2 * i + 1] = turns ? e1 * cs[i] + e0 * sn[i] : e1;
+                    for (int i = 0; i < 8; ++i) sn[i] = -sn[i];  // first element: a cos - b sin
+                }
+            } else {
+                const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + l * 4));
+                const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + half + l * 4));
+                cs[0] = c4.x, cs[1] = c4.y, cs[2] = c4.z, cs[3] = c4.w;
+                sn[0] = s4.x, sn[1] = s4.y, sn[2] = s4.z, sn[3] = s4.w;
             }
         }
-        if (r < hqk) x[u].set(y);  // a value row goes on as it came
-        if (r < a.hq) {
-            x[u].store(static_cast<T *>(a.q_out) + ((size_t)t * a.hq + r) * D + l * 8);
-        } else if (r < rows) {
-            const bool is_k = r < hqk;
-            const int h = is_k ? r - a.hq : r - hqk;
-            if (is_k && a.k_out) x[u].store(static_cast<T *>(a.k_out) + ((size_t)t * hkv + h) * D + l * 8);
-            if (crow >= 0)
-                x[u].store(static_cast<T *>(is_k ? a.ck : a.cv) + (size_t)(crow + ((long long)h << a.page_shift)) * D +
-                           l * 8);
+        // lane of the pair's other half (half-split); itself when nothing turns
+        const int partner = !turns ? lane : (low ? lane + a.rot / 16 : lane - a.rot / 16);
+
+        // where the token's cache rows go
+        long long crow = -1;  // row index of head 0 at this token's slot
+        if (a.ck) {
+            const int pg = slot >> a.page_shift;
+            if (slot >= 0 && pg < a.n_pages)
+                crow = (((long long)pg * hkv) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+            else if (slot != -1 && lane == 0)
+                record_error(a.err, SFFN_ERR_DEVICE);
+        }
+
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = (c * U + u) * RPW + grp;
+            float f[8];
+            x[u].get(f);
+            const void *w = r < a.hq ? a.q_weight : a.k_weight;
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss += f[i] * f[i];
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (w && r < hqk) {
+                Row8<T> wr;
+                wr.load(static_cast<const T *>(w) + l * 8);
+                float wf[8];
+                wr.get(wf);
+                const float inv = 1.f / sqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = f[i] * inv * wf[i];
+            }
+            float y[8];
+            if (a.style == SFFN_ROPE_HALF) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float o = __shfl_sync(0xffffffffu, f[i], partner);
+                    y[i] = turns ? f[i] * cs[i] + o * sn[i] : f[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e0 = f[2 * i], e1 = f[2 * i + 1];
+                    y[2 * i] = turns ? e0 * cs[i] - e1 * sn[i] : e0;
+                    y[2 * i + 1] = turns ? e1 * cs[i] + e0 * sn[i] : e1;
+                }
+            }
+            if (r < hqk) x[u].set(y);  // a value row goes on as it came
+            if (r < a.hq) {
+                x[u].store(static_cast<T *>(a.q_out) + ((size_t)t * a.hq + r) * D + l * 8);
+            } else if (r < rows) {
+                const bool is_k = r < hqk;
+                const int h = is_k ? r - a.hq : r - hqk;
+                if (is_k && a.k_out) x[u].store(static_cast<T *>(a.k_out) + ((size_t)t * hkv + h) * D + l * 8);
+                if (crow >= 0)
+                    x[u].store(static_cast<T *>(is_k ? a.ck : a.cv) + (size_t)(crow + ((long long)h << a.page_shift)) * D +
+                               l * 8);
+            }
         }
     }
 }
@@ -200,16 +216,19 @@ cudaError_t launch_rope(const RopeArgs &a, cudaStream_t s) {
     constexpr int per = (32 / (D / 8)) * U;
     const int rows = a.hq + a.hkv + (a.ck ? a.hkv : 0);
     const long long items = (long long)a.T * ((rows + per - 1) / per);
-    const long long grid = (items + kRopeWarps - 1) / kRopeWarps;
+    long long grid = (items + kRopeWarps - 1) / kRopeWarps;
+    const long long resident = 6LL * device_sm_count();
+    if (grid > resident) grid = resident;
     return launch_k(k_qk_norm_rope<T, D, U>, dim3((unsigned)grid), dim3(32 * kRopeWarps), 0, s, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_rope_u(const RopeArgs &a, cudaStream_t s) {
-    // Four rows a lane once that still leaves every SM several warps; one row below
+    // Several rows a lane (64 bytes) once that still leaves every SM several warps; one row below
     // (the smallest calls: more warps, each with one load to wait for).
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
     const long long rows = (long long)a.T * (a.hq + 2 * a.hkv);
-    return rows >= 64LL * device_sm_count() ? launch_rope<T, D, 4>(a, s) : launch_rope<T, D, 1>(a, s);
+    return rows >= 64LL * device_sm_count() ? launch_rope<T, D, U>(a, s) : launch_rope<T, D, 1>(a, s);
 }
 
 }  // namespace
