@@ -464,16 +464,36 @@ def _need(ok: bool, status: int, where: str):
         raise SffnError(status, where)
 
 
-def _rows(t: torch.Tensor, where: str) -> int:
+def _rows(t: torch.Tensor, shape, where: str) -> int:
     """Token stride of a [T, heads, head_dim] tensor or view; its heads must be contiguous."""
-    _need(t.dim() == 3 and t.is_cuda and (t.shape[0] == 0 or (t.stride(2) == 1 and t.stride(1) == t.shape[2])),
-          ERR_INVALID_ARG, where)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if len(shape) != 3 or not t.is_cuda:
+        raise SffnError(ERR_INVALID_ARG, where)
+    T, H, D = shape
+    if T == 0:
+        return H * D
+    st, sh, sd = t.stride()
+    if sd != 1 or (sh != D and H > 1):
+        raise SffnError(ERR_INVALID_ARG, where)
+    return st if T > 1 else H * D
 
 
 def _vec(t, n: int, dtype, where: str):
-    """A contiguous device array of n (or more) elements of one type, or None."""
-    _need(t is None or (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= n), ERR_INVALID_ARG, where)
+    """Address of a contiguous device array of n (or more) elements of one type, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_cuda or not t.is_contiguous():
+        raise SffnError(ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+# address of the current stream of the current device, without the objects around it where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch_stream(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return _stream(stream)
 
 
 class KVCache:
@@ -487,9 +507,10 @@ class KVCache:
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
         self.c = KVCacheStruct(_TDTYPE[k.dtype], self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
                                _ptr(k), _ptr(v))
+        self.c_ref = C.pointer(self.c)
 
     def ref(self):
-        return C.byref(self.c)
+        return self.c_ref
 
 
 def attn_workspace_size(which: int, T: int, n_seq: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -519,35 +540,34 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v, table, positions, q_weight
     projection are fine); with a cache, k and v rows go to their slots.  table [max_pos, rot_dim]
     (see rope_table; None: no rotation).  Returns (q_out, k_out); k_out is None when the
     keys go to the cache only (a cache and no k_out given)."""
-    T, hq, D = q.shape
-    hkv = k.shape[1]
     where = "sffn_qk_norm_rope"
-    qs, ks = _rows(q, where), _rows(k, where)
-    vs = 0 if v is None else _rows(v, where)
-    dt = q.dtype
-    _need(dt in _TDTYPE and k.dtype == dt and (v is None or v.dtype == dt), ERR_INVALID_ARG, where)
-    _need(k.shape[0] == T and k.shape[2] == D and (v is None or v.shape == k.shape), ERR_SHAPE, where)
-    _vec(q_weight, D, dt, where)
-    _vec(k_weight, D, dt, where)
-    _vec(positions, T, torch.int32, where)
-    _vec(slots, T, torch.int32, where)
+    qshape, kshape, dt = q.shape, k.shape, q.dtype
+    qs, ks, vs = _rows(q, qshape, where), _rows(k, kshape, where), 0
+    T, hq, D = qshape
+    hkv = kshape[1]
+    _need(dt in _TDTYPE and k.dtype is dt, ERR_INVALID_ARG, where)
+    _need(kshape[0] == T and kshape[2] == D, ERR_SHAPE, where)
+    if v is not None:
+        vs = _rows(v, v.shape, where)
+        _need(v.dtype is dt, ERR_INVALID_ARG, where)
+        _need(v.shape == kshape, ERR_SHAPE, where)
     max_pos = rot = 0
     if table is not None:
-        _need(table.dim() == 2 and table.dtype == torch.float32 and table.is_contiguous() and table.is_cuda,
-              ERR_INVALID_ARG, where)
+        _need(table.dim() == 2, ERR_INVALID_ARG, where)
         max_pos, rot = table.shape
     if q_out is None:
         q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
     if k_out is None and cache is None:
         k_out = torch.empty((T, hkv, D), dtype=dt, device=q.device)
-    _vec(q_out, T * hq * D, dt, where)
-    _vec(k_out, T * hkv * D, dt, where)
     if workspace is None:
         workspace = alloc_attn_workspace(WS_QK_NORM_ROPE, T, 1, hq, hkv, D, q.device)
-    st = lib().sffn_qk_norm_rope(_TDTYPE[dt], _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, hq, hkv, D, _ptr(q_weight),
-                                 _ptr(k_weight), float(eps), _ptr(table), rot, max_pos, int(style), _ptr(positions),
-                                 _ptr(q_out), _ptr(k_out), None if cache is None else cache.ref(), _ptr(slots),
-                                 _ptr(workspace), workspace.numel(), _stream(stream))
+    st = lib().sffn_qk_norm_rope(_TDTYPE[dt], q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, T, hq, hkv, D,
+                                 _vec(q_weight, D, dt, where), _vec(k_weight, D, dt, where), eps,
+                                 _vec(table, 0, torch.float32, where), rot, max_pos, style,
+                                 _vec(positions, T, torch.int32, where), _vec(q_out, T * hq * D, dt, where),
+                                 _vec(k_out, T * hkv * D, dt, where), None if cache is None else cache.c_ref,
+                                 _vec(slots, T, torch.int32, where), workspace.data_ptr(), workspace.numel(),
+                                 _launch_stream(stream))
     _check(st, where)
     return q_out, k_out
 
@@ -557,21 +577,22 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     """Causal attention over packed prompts: q [T, n_heads, D], k and v [T, n_kv_heads, D] bf16
     (views of a fused projection are fine), cu_seqlens int32 [n_seq + 1].  Returns out [T, n_heads, D]."""
     where = "sffn_attn_prompt"
-    T, hq, D = q.shape
-    hkv = k.shape[1]
-    qs, ks, vs = _rows(q, where), _rows(k, where), _rows(v, where)
-    _need(q.dtype == k.dtype == v.dtype == torch.bfloat16, ERR_UNSUPPORTED, where)
-    _need(k.shape == v.shape and k.shape[0] == T and k.shape[2] == D, ERR_SHAPE, where)
-    _vec(cu_seqlens, 2, torch.int32, where)
+    qshape, kshape, vshape = q.shape, k.shape, v.shape
+    qs, ks, vs = _rows(q, qshape, where), _rows(k, kshape, where), _rows(v, vshape, where)
+    T, hq, D = qshape
+    hkv = kshape[1]
+    bf16 = torch.bfloat16
+    _need(q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16, ERR_UNSUPPORTED, where)
+    _need(kshape == vshape and kshape[0] == T and kshape[2] == D, ERR_SHAPE, where)
+    cu = _vec(cu_seqlens, 2, torch.int32, where)
     n_seq = cu_seqlens.numel() - 1
     if out is None:
-        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    _vec(out, T * hq * D, q.dtype, where)
+        out = torch.empty((T, hq, D), dtype=bf16, device=q.device)
     if workspace is None:
         workspace = alloc_attn_workspace(WS_ATTN_PROMPT, T, n_seq, hq, hkv, D, q.device)
-    st = lib().sffn_attn_prompt(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, T, hq, hkv, D, _ptr(cu_seqlens), n_seq,
-                                float(D ** -0.5 if scale is None else scale), _ptr(out), _ptr(workspace),
-                                workspace.numel(), _stream(stream))
+    st = lib().sffn_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, hq, hkv, D, cu, n_seq,
+                                D ** -0.5 if scale is None else scale, _vec(out, T * hq * D, bf16, where),
+                                workspace.data_ptr(), workspace.numel(), _launch_stream(stream))
     _check(st, where)
     return out
 
@@ -583,22 +604,21 @@ def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len
     q [T, n_heads, D], page_table int32 [n_seq, width], ctx_lens int32 [n_seq], cu_tokens int32
     [n_seq + 1].  Returns out [T, n_heads, D]."""
     where = "sffn_attn_tree"
-    T, hq, D = q.shape
-    qs = _rows(q, where)
-    _need(q.dtype == cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
-    _need(page_table.dim() == 2 and page_table.is_contiguous() and page_table.dtype == torch.int32
-          and page_table.is_cuda, ERR_INVALID_ARG, where)
+    qshape, dt = q.shape, q.dtype
+    qs = _rows(q, qshape, where)
+    T, hq, D = qshape
+    _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
+    _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
     n_seq, width = page_table.shape
-    _vec(ctx_lens, n_seq, torch.int32, where)
-    _vec(cu_tokens, n_seq + 1, torch.int32, where)
-    _vec(tree_mask, T, torch.int64, where)
     if out is None:
-        out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    _vec(out, T * hq * D, q.dtype, where)
+        out = torch.empty((T, hq, D), dtype=dt, device=q.device)
     if workspace is None:
         workspace = alloc_attn_workspace(WS_ATTN_TREE, T, n_seq, hq, cache.n_kv_heads, D, q.device)
-    st = lib().sffn_attn_tree(_ptr(q), qs, T, hq, cache.ref(), _ptr(page_table), width, _ptr(ctx_lens),
-                              _ptr(cu_tokens), n_seq, _ptr(tree_mask), float(D ** -0.5 if scale is None else scale),
-                              _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+    i32 = torch.int32
+    st = lib().sffn_attn_tree(q.data_ptr(), qs, T, hq, cache.c_ref, _vec(page_table, 0, i32, where), width,
+                              _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
+                              _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
+                              _vec(out, T * hq * D, dt, where), workspace.data_ptr(), workspace.numel(),
+                              _launch_stream(stream))
     _check(st, where)
     return out
