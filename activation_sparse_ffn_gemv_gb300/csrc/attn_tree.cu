@@ -10,7 +10,7 @@ namespace sffn {
 
 namespace {
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     rows::Smem<D> &sm = *reinterpret_cast<rows::Smem<D> *>(smem_raw);
@@ -31,45 +31,43 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_tree_rows(const TreeArgs 
         const TreePiece pc = tree_piece(a, pre, u, u1, q);
         u = pc.next;
         if (pc.un0 >= pc.un1) continue;
-        const int s = pc.s, h = pc.h, un0 = pc.un0, un1 = pc.un1;
         const int tk0 = pc.tile * a.tile_tokens, nt = min(a.tile_tokens, q.n - tk0);
-        const int32_t *table = a.page_table + (size_t)s * a.table_width;
-        const long long keys = (long long)q.ctx + q.n;
-        const long long k0 = (long long)un0 * kTreeUnit, k1 = min(keys, (long long)un1 * kTreeUnit);
+        const int32_t *table = a.page_table + (size_t)pc.s * a.table_width;
+        const int k0 = pc.un0 * kTreeUnit, k1 = min(q.ctx + q.n, pc.un1 * kTreeUnit);
         __syncthreads();
         if (tid < nt)
             mask[tid] = a.tree_mask ? a.tree_mask[q.t0 + tk0 + tid]
                                     : (tk0 + tid == 63 ? ~0ull : (1ull << (tk0 + tid + 1)) - 1ull);
         rows::Acc<D> acc;
-        rows::attend<T, D>(
-            sm, acc, nt * G, k0, k1, a.scale,
+        rows::attend<D>(
+            sm, acc, nt * G, k0, k1, min(q.ctx, k1), a.scale,
             [&](int r) {
-                return static_cast<const T *>(a.q) + (size_t)(q.t0 + tk0 + r / G) * a.q_stride +
-                       (size_t)(h * G + r % G) * D;
+                return static_cast<const float *>(a.q) + (size_t)(q.t0 + tk0 + r / G) * a.q_stride +
+                       (size_t)(pc.h * G + r % G) * D;
             },
-            [&](long long j, int which) -> const T * {
+            [&](int j, int which) -> const float * {
                 const int pg = table[j >> a.page_shift];
                 if (pg < 0 || pg >= a.n_pages) {
                     record_error(a.err, SFFN_ERR_DEVICE);
                     return nullptr;
                 }
-                return static_cast<const T *>(which ? a.cv : a.ck) +
-                       ((((size_t)pg * a.n_kv_heads + h) << a.page_shift) + (size_t)(j & (ps - 1))) * D;
+                return static_cast<const float *>(which ? a.cv : a.ck) +
+                       ((((size_t)pg * a.n_kv_heads + pc.h) << a.page_shift) + (size_t)(j & (ps - 1))) * D;
             },
-            [&](int r, long long j) { return j < q.ctx || ((mask[r / G] >> (j - q.ctx)) & 1); });
-        const bool whole = un0 == 0 && un1 == q.units;
-        float *slot = a.part + tree_slot_floats(a.rows_max, D) * (size_t)(2 * w + (un0 > 0 ? 0 : 1));
-        const int c = (tid % rows::Acc<D>::CT) * 4, g = tid / rows::Acc<D>::CT;
+            [&](int r, int j) { return (mask[r / G] >> (j - q.ctx)) & 1; });
+        const bool whole = pc.un0 == 0 && pc.un1 == q.units;
+        float *slot = a.part + tree_slot_floats(a.rows_max, D) * (size_t)(2 * w + (pc.un0 > 0 ? 0 : 1));
+        const int c = (tid % rows::Acc<D>::CT) * 4, g = (tid / rows::Acc<D>::CT) * rows::Acc<D>::RPT;
 #pragma unroll
         for (int i = 0; i < rows::Acc<D>::RPT; ++i) {
-            const int r = g + i * rows::Acc<D>::RG;
+            const int r = g + i;
             if (r < nt * G) {
-                float4 o = acc.o[i];
+                const float4 o = acc.o[i];
                 if (whole) {
                     const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
-                    T *dst = static_cast<T *>(a.out) +
-                             ((size_t)(q.t0 + tk0 + r / G) * a.n_heads + (size_t)(h * G + r % G)) * D + c;
-                    rows::store4<T>(dst, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                    float *dst = static_cast<float *>(a.out) +
+                                 ((size_t)(q.t0 + tk0 + r / G) * a.n_heads + (size_t)(pc.h * G + r % G)) * D + c;
+                    *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                 } else {
                     *reinterpret_cast<float4 *>(slot + (size_t)r * D + c) = o;
                     if (c == 0) {
@@ -307,9 +305,9 @@ cudaError_t launch_join(const TreeArgs &a, int grid, cudaStream_t s) {
 
 template <int D>
 sffn_status launch_tree_f32(const TreeArgs &a, int grid, cudaStream_t s) {
-    cudaError_t e = set_max_smem((const void *)k_tree_rows<float, D>, (int)(sizeof(rows::Smem<D>) + kPrefixBytes));
+    cudaError_t e = set_max_smem((const void *)k_tree_rows<D>, (int)(sizeof(rows::Smem<D>) + kPrefixBytes));
     if (e == cudaSuccess)
-        e = launch_k(k_tree_rows<float, D>, dim3(grid), dim3(rows::kThreads),
+        e = launch_k(k_tree_rows<D>, dim3(grid), dim3(rows::kThreads),
                      sizeof(rows::Smem<D>) + (size_t)(a.n_seq + 1) * sizeof(long long), s, a);
     if (e == cudaSuccess) e = launch_join<float, D>(a, grid, s);
     return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
