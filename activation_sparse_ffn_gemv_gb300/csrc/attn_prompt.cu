@@ -23,6 +23,7 @@ using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false, false>;  // 208 KB and 176 KB o
 
 template <int D>
 struct PromptPolicy {
+    static constexpr bool kReread = true;
     const PromptArgs &a;
     int G, TB;
     // The walk's place: blocks [nxt, top] of the `cnt` sequences that have them; `before` pairs
@@ -102,11 +103,10 @@ struct PromptPolicy {
         w.k1 = k1;
         w.exist = n;
         w.tiles = (k1 + atc::kKeys - 1) / atc::kKeys;
-        w.split = nt <= TB;
-        w.n[0] = w.split ? (w.tiles + 1) / 2 : (min(i0 + TB, n) + atc::kKeys - 1) / atc::kKeys;
-        w.n[1] = w.split ? w.tiles / 2 : w.tiles;
+        w.n[0] = (min(i0 + TB, n) + atc::kKeys - 1) / atc::kKeys;
+        w.n[1] = nt > TB ? w.tiles : 0;
         w.mask_from[0] = (i0 + 1) / atc::kKeys;
-        w.mask_from[1] = (i0 + (w.split ? 0 : TB) + 1) / atc::kKeys;
+        w.mask_from[1] = (i0 + TB + 1) / atc::kKeys;
         return true;
     }
     // Row of a key tile's first key.

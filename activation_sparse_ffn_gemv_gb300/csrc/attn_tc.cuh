@@ -17,10 +17,10 @@
 //   warps 2-5   softmax of tile 0: a thread owns a row; S_t from TMEM, weights P_t (bf16)
 //   warps 6-9   softmax of tile 1  back to TMEM over S_t, where the second product reads
 //               them as its A operand; at the end O_t / sum to global memory
-// While one tile's softmax runs, the tensor cores work on the other tile.  An item of a single row
-// tile (few new tokens, a prompt's last ones) has its key tiles dealt to the two pipelines
-// instead; at the end the first one joins both results, reading the other's accumulator
-// from TMEM (the same rows are the same lanes).
+// While one tile's softmax runs, the tensor cores work on the other tile.  Where every item has
+// one row tile (ONE: few new tokens over a long cache) its key tiles are dealt to the two
+// pipelines instead, and at the end the first one joins both results, reading the
+// other's accumulator from TMEM (the same rows are the same lanes).
 //
 // A weight of zero times an infinite or NaN value would be NaN, so in a tile with
 // masked keys the softmax warps look through V in shared memory before the second
@@ -70,7 +70,6 @@ struct Work {
     int q_row;          // first token (row of q and out)
     int nt;             // tokens
     int h;              // key head
-    int split;          // one row tile: the two pipelines take its even and its odd key tiles
     int tiles;          // key tiles
     int n[2];           // those of each pipeline
     int mask_from[2];   // first key tile with masked keys
@@ -128,6 +127,7 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 
 // P: the policy (prompts or tree).  It gives
 //   start                  before the first item (every warp calls it)
+//   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
 //   load_kv                the producer's loads of a K or V tile
 //   row_info, visible      a row's own data; which keys of a masked tile it sees, as four words
@@ -140,7 +140,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + C::kQ * C::kTile,
                   *sm_out = sm_kv + C::kStages * C::kTile;
     constexpr int NS = C::kStages;
-    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_full[2], mdone,
+    __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], mdone,
         i_full[kItems], i_empty[kItems], x_full, x_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
@@ -153,8 +153,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             mbar_init(&q_full[t], 1);
             mbar_init(&q_empty[t], 1);
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_ready[0][t], 4);  // [half of the tile's keys][row tile]
-            mbar_init(&p_ready[1][t], 4);
+            mbar_init(&p_ready[t], 4);
             mbar_init(&o_full[t], 1);
         }
         mbar_init(&mdone, 1);
@@ -220,7 +219,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     if (warp == 0) {
         // ---------------- loads ----------------
         int it = 0, qn[2] = {0, 0};
-        const uint64_t keep = tc::l2_evict_last_policy();
+        const uint64_t keep = P::kReread ? tc::l2_evict_last_policy() : l2_evict_first_policy();
         for (;; ++item) {
             Work &w = s_work[item % kItems];
             wait(&i_empty[item % kItems], (uint32_t)(((item / kItems) & 1) ^ 1));
@@ -244,7 +243,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                             mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
                             for (int c = 0; c < C::kHalves; ++c)
                                 tc::tma_load_3d(sm_q + part * C::kTile + c * C::kBlock, &map_q, c * 64, w.h * G,
-                                                w.q_row + (w.split ? 0 : part * TB), &q_full[part], keep);
+                                                w.q_row + part * TB, &q_full[part], keep);
                         }
                         ++qn[part];
                     }
@@ -276,10 +275,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                                   b + (((kk >> 2) * C::kColBlock + (kk & 3) * 32) >> 4), idesc_s, kk != 0);
             tc::mma_commit_warp(&s_full[t]);
         };
-        auto values = [&](int t, int half, uint32_t tile, bool acc) {  // O_t (+)= P_t V over half of the keys
+        auto values = [&](int t, uint32_t tile, bool acc) {  // O_t (+)= P_t V
             const uint64_t b = hi_v | (tile >> 4);
 #pragma unroll
-            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
+            for (int kk = 0; kk < kKeys / 16; ++kk)
                 tc::mma_bf16_ts_warp(tmem + C::kColO + t * D, tmem + t * 128 + kk * 8, b + kk * (2 * C::kRows8 >> 4), idesc_o,
                                      acc || kk != 0);
         };
@@ -297,27 +296,25 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             tc::fence_after_sync();
             scores(t, tile_of(slot));
         };
-        auto weigh = [&](int t, uint32_t v, bool acc) {  // O_t (+)= P_t V, as the weights come
-            wait(&p_ready[0][t], p_par[t]);
-            tc::fence_after_sync();
-            values(t, 0, v, acc);
-            wait(&p_ready[1][t], p_par[t]);
+        auto weigh = [&](int t, uint32_t v, bool acc) {  // once the weights are there
+            wait(&p_ready[t], p_par[t]);
             p_par[t] ^= 1;
             tc::fence_after_sync();
-            values(t, 1, v, true);
+            values(t, v, acc);
         };
-        // Two row tiles over the same key tiles.
+        // Two row tiles (or the first alone) over the same key tiles.
         auto both = [&](const int n0, const int n1) {
-            const int n[2] = {n0, n1};
+            const int n[2] = {n0, n1}, nmax = max(n0, n1);
             wait(&kv_full[slot], par);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) first_scores(t);
+            for (int t = 0; t < 2; ++t)
+                if (n[t] > 0) first_scores(t);
             step();
-            for (int j = 0; j < n1; ++j) {
+            for (int j = 0; j < nmax; ++j) {
                 const int vs = slot;
                 wait(&kv_full[vs], par);
                 step();
-                const bool more = j + 1 < n1;
+                const bool more = j + 1 < nmax;
                 if (more) wait(&kv_full[slot], par);
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
@@ -377,14 +374,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (!w.more) break;
             // uniform by construction; the reductions tell the compiler so
             const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
-            if constexpr (C::kOne) {
+            if constexpr (C::kOne)
                 dealt(n0 + n1);
-            } else {
-                if (__reduce_max_sync(0xffffffffu, w.split))
-                    dealt(n0 + n1);
-                else
-                    both(n0, n1);
-            }
+            else
+                both(n0, n1);
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
@@ -404,13 +397,13 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         for (;;) {
             const Work &w = take();
             if (!w.more) break;
-            const int n = w.n[t], dealt = C::kOne ? 1 : w.split, tiles = w.tiles;
+            const int n = w.n[t], tiles = w.tiles;
+            constexpr bool dealt = C::kOne;
             const int item_tok = (dealt ? 0 : t * TB) + tok;  // token of the item
             const bool valid = tok < TB && item_tok < w.nt;
             typename P::RowInfo ri = policy.row_info(w, valid ? item_tok : 0);
             // of two row tiles' pipelines the second is the last reader of a key tile
             const bool releases = dealt || t == (w.n[1] > 0 ? 1 : 0);
-            if (dealt) seen = false;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
                 const int kt = dealt ? 2 * j + t : j, k_at = base + 2 * kt;  // key tile, ring index of its K
@@ -532,13 +525,13 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         p[i] = pack_bf16(e0, e1);
                     }
                     tc::tmem_st16(ts + q * 16, p);
-                    if (q & 1) {  // the weights of 64 keys are there: their product may start
-                        tc::tmem_wait_st();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_ready[q >> 1][t]);
-                    }
                 }
+                // (handing over the first 64 keys' weights early cost the issuing warp a second look at
+                // a barrier and gained nothing: 190 against 187 us for 8192 tokens of 16 heads)
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[t]);
                 float l0, l1;
                 split(add2(sum[0], sum[1]), l0, l1);
                 l += l0 + l1;

@@ -90,6 +90,7 @@ using Cfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
 
 template <int D>
 struct TreePolicy {
+    static constexpr bool kReread = false;
     const TreeArgs &a;
     long long *pre;         // units before each sequence (shared memory)
     long long u, u1;        // this CTA's next unit, and the end of its units
@@ -128,7 +129,6 @@ struct TreePolicy {
         w.k0 = k0;
         w.k1 = w.exist = k1;
         w.tiles = n;
-        w.split = 1;
         w.n[0] = (n + 1) / 2;
         w.n[1] = n / 2;
         w.mask_from[0] = w.mask_from[1] = max(0, min(q.ctx, k1) - k0) / atc::kKeys;
@@ -219,44 +219,18 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
 
 // Joins the pieces of cut items: for each row, M = max of the pieces' maxima,
 // out = sum(exp(m_i - M) o_i) / sum(exp(m_i - M) l_i), the pieces in the order of
-// their CTAs.  One warp a row (token, query head).
-// Where a row's pieces are depends on the call's inputs alone, so that is found before the wait
-// for the pieces' kernel (which lets this one start once it has itself waited for the inputs;
-// 128 threads of 40 registers find room beside it); after the wait come one load of all maxima and
-// sums and then the outputs, independent of one another.
+// their CTAs.
+// There are `parts` blocks for each place between two CTAs' ranges; those of all the places that cut
+// an item share its rows, a warp a row at a time (an item cut often has many
+// pieces to read and as many more blocks).  What a block has to do depends on the call's inputs
+// alone and is found before the wait for the pieces' kernel (which lets this one start once it has itself waited for the inputs; 128 threads of 40
+// registers find room beside it); after the wait come one load of all maxima and sums and
+// then the outputs, independent of one another.
 constexpr int kJoinWarps = 4;
+constexpr int kJoinRows = 8;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps, 12) k_tree_join(const TreeArgs a, int grid) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    long long *pre = reinterpret_cast<long long *>(smem_raw);
-    __shared__ long long scratch[33];
-    tree_prefix(a, pre, scratch, false);
-    const long long total = pre[a.n_seq];
-    const int W = tree_ctas(total, grid);
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    int w0 = 0, w1 = 0, r = 0;  // CTAs of the first and the last piece, row within the slots
-    if (row < (long long)a.T * a.n_heads) {
-        const int t = (int)(row / a.n_heads), hq = (int)(row - (long long)t * a.n_heads);
-        // the sequence of token t: the last one that starts at or before it
-        int lo = 0, hi = a.n_seq;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (a.cu_tokens[mid] <= t) lo = mid; else hi = mid;
-        }
-        const TreeSeq q = tree_seq(a, lo, false);
-        if (t >= q.t0 && t < q.t0 + q.n) {
-            const int G = a.group, h = hq / G, tile = (t - q.t0) / a.tile_tokens;
-            r = (t - q.t0 - tile * a.tile_tokens) * G + hq - h * G;
-            const long long i0 = pre[lo] + ((long long)h * q.tiles + tile) * q.span();
-            w0 = tree_owner(total, i0 + kTreeItemCost, W);
-            w1 = tree_owner(total, i0 + q.span() - 1, W);
-        }
-    }
-    griddep_wait();
-    griddep_launch_dependents();
-    if (w0 == w1) return;  // finished by its one CTA, or not a row
+SFFN_DEV void join_row(const TreeArgs &a, long long row, int w0, int w1, int r, int lane) {
     const size_t sf = tree_slot_floats(a.rows_max, D);
     auto slot = [&](int w) { return a.part + sf * (size_t)(2 * w + (w == w0 ? 1 : 0)); };
     constexpr int C = D / 32;  // columns of a lane
@@ -297,10 +271,45 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 12) k_tree_join(const TreeArg
 }
 
 template <typename T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps, 12) k_tree_join(const TreeArgs a, int grid, int parts) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    long long *pre = reinterpret_cast<long long *>(smem_raw);
+    __shared__ long long scratch[33];
+    tree_prefix(a, pre, scratch, false);
+    const long long total = pre[a.n_seq];
+    const int W = tree_ctas(total, grid), lane = threadIdx.x & 31;
+    const int w = 1 + blockIdx.x / parts, part = blockIdx.x % parts;
+    int w0 = 0, w1 = 0, nr = 0, tok = 0, head = 0;  // the item's CTAs, rows, first token and query head
+    if (w < W) {
+        const long long u = tree_cut(total, w, W);
+        const int s = tree_find(pre, a.n_seq, u);
+        const TreeSeq q = tree_seq(a, s, false);
+        const long long local = u - pre[s];
+        const int item = (int)(local / q.span());
+        const long long i0 = pre[s] + (long long)item * q.span();
+        const int h = item / q.tiles, tk0 = (item - h * q.tiles) * a.tile_tokens;
+        w0 = tree_owner(total, i0 + kTreeItemCost, W);
+        w1 = tree_owner(total, i0 + q.span() - 1, W);
+        nr = min(a.tile_tokens, q.n - tk0) * a.group;
+        tok = q.t0 + tk0;
+        head = h * a.group;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    if (w0 >= w || w > w1) return;  // no item is cut here
+    const int blocks = (w1 - w0) * parts, b = (w - w0 - 1) * parts + part;
+    for (int r = b * kJoinWarps + (threadIdx.x >> 5); r < nr; r += blocks * kJoinWarps)
+        join_row<T, D>(a, (long long)(tok + r / a.group) * a.n_heads + head + r % a.group, w0, w1, r, lane);
+}
+
+template <typename T, int D>
 cudaError_t launch_join(const TreeArgs &a, int grid, cudaStream_t s) {
-    const long long rows = (long long)a.T * a.n_heads;
-    return launch_k(k_tree_join<T, D>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), dim3(32 * kJoinWarps),
-                    (size_t)(a.n_seq + 1) * sizeof(long long), s, a, grid);
+    if (grid < 2) return cudaSuccess;  // one CTA: nothing is cut
+    // two rows a warp where an item is cut once, as long as one wave of blocks takes them all
+    int parts = (a.rows_max + kJoinRows - 1) / kJoinRows;
+    if (parts > 12) parts = 12;
+    return launch_k(k_tree_join<T, D>, dim3((unsigned)((grid - 1) * parts)), dim3(32 * kJoinWarps),
+                    (size_t)(a.n_seq + 1) * sizeof(long long), s, a, grid, parts);
 }
 
 template <int D>
