@@ -19,7 +19,7 @@ namespace sffn {
 namespace {
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false, false>;  // 208 KB and 176 KB of shared memory
+using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false, false>;  // 224 KB and 192 KB of shared memory
 
 template <int D>
 struct PromptPolicy {
@@ -145,29 +145,29 @@ struct PromptPolicy {
 template <int D>
 __global__ void __launch_bounds__(atc::kThreads, 1)
     k_attn_prompt(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                  const __grid_constant__ CUtensorMap map_v, const PromptArgs a) {
+                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o, const PromptArgs a) {
     extern __shared__ unsigned char smem_raw[];
     PromptPolicy<D> policy(a);
-    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw);
+    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, map_o, a.scale, a.group, a.err, smem_raw);
 }
 
 template <int D>
 sffn_status launch_prompt(const PromptArgs &a, cudaStream_t s) {
     const int G = a.group, TB = 128 / G;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, dk[3] = {D, (uint64_t)a.n_kv_heads, (uint64_t)a.T};
     const uint64_t sq[2] = {D * 2, (uint64_t)a.q_stride * 2}, sk[2] = {D * 2, (uint64_t)a.k_stride * 2},
-                   sv[2] = {D * 2, (uint64_t)a.v_stride * 2};
+                   sv[2] = {D * 2, (uint64_t)a.v_stride * 2}, so[2] = {D * 2, (uint64_t)a.n_heads * D * 2};
     const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[3] = {64, 1, atc::kKeys};
     if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.k, 3, dk, sk, bk) ||
-        !make_map_bf16(&mv, a.v, 3, dk, sv, bk))
+        !make_map_bf16(&mv, a.v, 3, dk, sv, bk) || !make_map_bf16(&mo, a.out, 3, dq, so, bq))
         return SFFN_ERR_UNSUPPORTED;
     // at most one partial block per sequence
     const long long items = ((long long)a.T / (2 * TB) + a.n_seq) * a.n_kv_heads;
     const int grid = (int)(items < device_sm_count() ? items : device_sm_count());
     cudaError_t e = set_max_smem((const void *)k_attn_prompt<D>, Cfg<D>::kSmem);
     if (e == cudaSuccess)
-        e = launch_k(k_attn_prompt<D>, dim3(grid), dim3(atc::kThreads), Cfg<D>::kSmem, s, mq, mk, mv, a);
+        e = launch_k(k_attn_prompt<D>, dim3(grid), dim3(atc::kThreads), Cfg<D>::kSmem, s, mq, mk, mv, mo, a);
     return e == cudaSuccess ? SFFN_OK : SFFN_ERR_CUDA;
 }
 

@@ -60,7 +60,7 @@ struct Cfg {
     // Row of a K or V tile that its i-th 16-byte chunk belongs to.
     SFFN_DEV static int row_of(int i) { return GROUPED ? (i / (64 * kHalves)) * 8 + ((i >> 3) & 7) : (i >> 3) & 127; }
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
-    static constexpr int kOut = 2048;                           // a softmax warp's: 64 bytes of its 32 output rows
+    static constexpr int kOut = ONE ? 2048 : 4096;              // a softmax warp's: 64 (128) bytes of its 32 output rows
     static constexpr int kSmem = (kQ + kStages) * kTile + (ONE ? 4 : 8) * kOut + 1024 /*alignment*/;
 };
 
@@ -135,7 +135,7 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 //   begin_row, partial     where a row's output goes; whether as fp32 partial result
 template <typename C, int D, typename P>
 SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorMap &map_k, const CUtensorMap &map_v,
-                            float scale, int G, int32_t *err, unsigned char *smem_raw) {
+                            const CUtensorMap &map_o, float scale, int G, int32_t *err, unsigned char *smem_raw) {
     const uint32_t raw_addr = smem_u32(smem_raw), q_addr = (raw_addr + 1023u) & ~1023u, kv_addr = q_addr + C::kQ * C::kTile;
     unsigned char *sm_q = smem_raw + (q_addr - raw_addr), *sm_kv = sm_q + C::kQ * C::kTile,
                   *sm_out = sm_kv + C::kStages * C::kTile;
@@ -617,7 +617,47 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     }
                     tc::tmem_wait_st();
                 }
+                const int o_h = w.h * G, o_row = w.q_row + t * TB;
+                const bool full = !C::kOne && w.nt >= (t + 1) * TB;
                 give_back();  // before the stores, which the release would wait for
+                if constexpr (!C::kOne) {
+                    // A whole row tile leaves by TMA, 64 columns at a time: the warps go on while it is
+                    // written (their own stores took 4000 cycles an item, stalling the loads after them).
+                    unsigned char *buf = sm_out + t * 4 * C::kOut;
+                    const bool issues = quad == 0 && lane == 0;
+                    if (full) {
+#pragma unroll 1
+                        for (int q2 = 0; q2 < D / 64; ++q2) {
+                            if (issues) tc::bulk_wait_read();
+                            named_barrier_sync(1 + t, 128);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                uint32_t o[32];
+                                tc::tmem_ld32(to + q2 * 64 + h * 32, o);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    uint32_t p[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        p[e] = pack_bf16(__uint_as_float(o[i * 8 + 2 * e]) * inv,
+                                                         __uint_as_float(o[i * 8 + 2 * e + 1]) * inv);
+                                    *reinterpret_cast<uint4 *>(buf + row * 128 + (((h * 4 + i) ^ (row & 7)) << 4)) =
+                                        make_uint4(p[0], p[1], p[2], p[3]);
+                                }
+                            }
+                            fence_proxy_async_smem();
+                            named_barrier_sync(1 + t, 128);
+                            if (issues) {
+                                tc::tma_store_3d(&map_o, q2 * 64, o_h, o_row, buf);
+                                tc::bulk_commit();
+                            }
+                        }
+                    } else {
+                        if (issues) tc::bulk_wait_read();
+                        named_barrier_sync(1 + t, 128);
+                    }
+                }
                 // 64 bytes of every row at a time through shared memory, the 16-byte chunks swizzled by
                 // the row: a store then covers 64 bytes of eight rows instead of 16 of 32
                 auto flush = [&](const uint32_t (&x)[16], int seg) {
@@ -636,7 +676,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         if (d) *reinterpret_cast<uint4 *>(d + (size_t)seg * 64 + ch * 16) = v;
                     }
                 };
-                if (f32) {
+                if (full) {
+                    // on its way
+                } else if (f32) {
 #pragma unroll 1
                     for (int q = 0; q < D / 16; ++q) {
                         uint32_t o[16];
@@ -663,6 +705,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             base += 2 * tiles;
             seen = !dealt && n >= tiles - 1;
         }
+        if (!C::kOne && quad == 0 && lane == 0) tc::bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();

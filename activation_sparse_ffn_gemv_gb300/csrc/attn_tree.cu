@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
     extern __shared__ __align__(16) unsigned char smem_raw[];
     __shared__ long long scratch[33];
     TreePolicy<D> policy(a, reinterpret_cast<long long *>(smem_raw), scratch);
-    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, a.scale, a.group, a.err, smem_raw + kPrefixBytes);
+    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, map_q, a.scale, a.group, a.err, smem_raw + kPrefixBytes);
 }
 
 // Joins the pieces of cut items: for each row, M = max of the pieces' maxima,

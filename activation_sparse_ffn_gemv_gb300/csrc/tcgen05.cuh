@@ -39,6 +39,18 @@ SFFN_DEV void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y, 
         : "memory");
 }
 
+// 3-D tile store from shared memory (the box's start inside the tensor), in the thread's current
+// bulk group; bulk_commit closes the group, bulk_wait_read waits until the closed groups have been
+// read out of shared memory, bulk_wait until they are complete.
+SFFN_DEV void tma_store_3d(const CUtensorMap *map, int x, int y, int z, const void *smem_src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(smem_u32(smem_src))
+                 : "memory");
+}
+SFFN_DEV void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+SFFN_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+SFFN_DEV void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 SFFN_DEV void prefetch_tensormap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
