@@ -6,7 +6,8 @@
 // 16 keys), the product with the values (thread: four columns, D / 16 rows; the weights lie
 // key by key, so a thread reads four rows' at once).  The next keys' rows are copied
 // meanwhile (cp.async, two buffers).  Bound: shared-memory reads of the two products,
-// about 5 a 16 multiply-adds; one read of the cache at 8 tokens of 8 grouped heads.
+// about 5 a 16 multiply-adds.  Measured: 4 sequences of up to 4000 positions, 1 to 8 tokens, 16/2
+// heads of 64, 28 us with the join (latency: a CTA has one or two tiles).
 #pragma once
 
 #include "attn.cuh"
