@@ -651,3 +651,24 @@ def test_tree_workspace_refusals_and_binding_checks(S):
         S.attn_prompt(z.bfloat16(), z.bfloat16(), z.bfloat16(), torch.tensor([0, 3]).cuda())  # 64-bit offsets
     with pytest.raises(S.SffnError):
         S.attn_tree(z, p.cache, p.table.cuda(), p.cu[:1].cuda(), p.cu.cuda())
+
+
+@pytest.mark.gpu
+def test_empty_calls_and_the_most_sequences(S):
+    """No tokens at all; as many sequences as a call takes, most of them without new tokens."""
+    e = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert S.attn_prompt(e, k, k, zero).shape == (0, 4, 64)
+    q, kk = S.qk_norm_rope(e, k, None, S.rope_table(4, 64), zero[:0])
+    assert q.shape == (0, 4, 64) and kk.shape == (0, 2, 64)
+    p = Paged(S, [20], [2], 4, 2, 64, 16, "bf16", 1)
+    assert S.attn_tree(e, p.cache, p.table.cuda(), zero[:1], zero).shape == (0, 4, 64)
+    n = [0, 0, 1, 0] * 256
+    p = Paged(S, [(7 * i) % 90 for i in range(1024)], n, 4, 2, 64, 16, "bf16", 2)
+    p.check(p.call(S))
+    lens = [0, 3, 1, 0, 20] * 60
+    qkv, cu = prompt_inputs(lens, 4, 2, 64, 21)
+    dev = qkv.cuda()
+    out = S.attn_prompt(dev[:, :4], dev[:, 4:6], dev[:, 6:], cu.cuda())
+    check_attention(out.cpu(), *ref_prompt(qkv, lens, 4, 2, 64), 64, 20, True)
