@@ -9,14 +9,14 @@
 //
 // Rows.  The G query heads of a key head read the same keys, so a row is a (token,
 // query head) pair and a 128-row tile holds TB = 128 / G tokens (one TMA box of TB
-// tokens x G heads x 64 elements lays them out as rows).  An item has two such tiles.
+// tokens x G heads x 64 elements lays them out as rows).  An item has two such tiles (or one).
 //
 // One CTA per SM, ten warps, no CTA-wide barrier between items:
 //   warp 0      loads: queries, then the ring of 128-key K and V tiles
 //   warp 1      issues the tcgen05.mma: S_t = Q_t K^T into TMEM (fp32), later O_t += P_t V
-//   warps 2-5   softmax of tile 0: a thread owns a row; S_t from TMEM, weights P_t (bf16)
-//   warps 6-9   softmax of tile 1  back to TMEM over S_t, where the second product reads
-//               them as its A operand; at the end O_t / sum to global memory
+//   warps 2-5   softmax of tile 0 (6-9: of tile 1): a thread owns a row; S_t from TMEM, weights
+//               P_t (bf16) back to TMEM over S_t, where the second product reads them as its
+//               A operand; at the end O_t / sum to global memory
 // While one tile's softmax runs, the tensor cores work on the other tile.  Where every item has
 // one row tile (ONE: few new tokens over a long cache) its key tiles are dealt to the two
 // pipelines instead, and at the end the first one joins both results, reading the
@@ -25,8 +25,8 @@
 // A weight of zero times an infinite or NaN value would be NaN, so in a tile with
 // masked keys the softmax warps look through V in shared memory before the second
 // product: non-finite elements become zero, and where they belong to existing keys the
-// rows that do see them get them added at the end (fix_row).  Rows that do not see
-// them come out bit for bit as without them.
+// rows that do see them get them added at the end.  Rows that do not see them come out bit
+// for bit as without them.
 #pragma once
 
 #include "attn.cuh"
@@ -129,7 +129,7 @@ SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u 
 //   start                  before the first item (every warp calls it)
 //   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
-//   load_kv                the producer's loads of a K or V tile
+//   place, load_kv         where a key tile lies, looked up a tile ahead; the load of its K or V
 //   row_info, visible      a row's own data; which keys of a masked tile it sees, as four words
 //   value_row              a key's value row in memory (null: the row does not see the key)
 //   begin_row, partial     where a row's output goes; whether as fp32 partial result
@@ -144,7 +144,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         i_full[kItems], i_empty[kItems], x_full, x_empty;
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
-    __shared__ float2 s_x[128];  // maximum and sum of the second pipeline's rows (split items)
+    __shared__ float2 s_x[128];  // maximum and sum of the second pipeline's rows (keys dealt to both)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
