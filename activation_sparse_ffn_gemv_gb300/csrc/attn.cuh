@@ -15,8 +15,9 @@ namespace sffn {
 // row tile); it reads ceil(positions / 64) units of 64 cached positions.  On one line, item
 // after item, each takes its units and kTreeItemCost more in front of them for what an
 // item costs by itself; CTA w of W takes [w total / W, (w + 1) total / W) of the line, whatever
-// the lengths.  (A batch of 48 sequences, some of them a few positions long: 132 us
-// without the extra cost, because one CTA got all the short items of a sequence group.)  Row tiles of
+// the lengths.  (48 sequences of one token, some a few positions long: 132 us without the extra
+// cost, because one CTA got all the short items of a sequence group, 92 with 2 units, 66 with 4, 65.5
+// with 5, 67 with 7; 32 with large draft trees 144, 130, 124.6 and 124.4.)  Row tiles of
 // one key head are neighbours, so that they read its keys at about the same time.  An
 // item whose units lie in one CTA's range is finished there; the pieces of a cut item are
 // written as partial results (unnormalised output, running maximum and sum) and joined by
@@ -24,7 +25,7 @@ namespace sffn {
 // ---------------------------------------------------------------------------
 
 constexpr int kTreeUnit = 64;
-constexpr int kTreeItemCost = 4;
+constexpr int kTreeItemCost = 5;
 constexpr int kTreeMaxTokens = 64;
 constexpr int kTreeMaxCtx = 0x7fff0000;  // positions stay below 2^31 with room for a tile
 

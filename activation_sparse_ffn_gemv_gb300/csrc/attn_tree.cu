@@ -5,7 +5,7 @@
 // all the query heads that share them.  Measured: 8 tokens over 65531 positions, 64/8 heads of
 // 128, 54 us (4.9 TB/s, 0.72 of the measured copy rate, about 12 us of it start, join and
 // tail); 48 ragged sequences of one token, 32/8 heads, 66 us (4.6 TB/s); one token over 300
-// positions 12 us.
+// positions 13 us.
 #include "attn_rows.cuh"
 #include "attn_tc.cuh"
 
