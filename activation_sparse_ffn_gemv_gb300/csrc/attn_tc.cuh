@@ -393,7 +393,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
         int sn = 0, on = 0, xn = 0, base = 0;
-        bool seen = true;  // this warp has seen every earlier fill of the ring, as far as it matters for V_0
+        // Whether this warp knows that the fill before V_0 in its ring slot (V of the next to last key tile before this
+        // item, or an older one) has landed: it does after the product with that tile or a later one.
+        bool seen = true;
         for (;;) {
             const Work &w = take();
             if (!w.more) break;
@@ -703,7 +705,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 give_back();
             }
             base += 2 * tiles;
-            seen = !dealt && n >= tiles - 1;
+            seen = !dealt && n > 0 && n >= tiles - 1;  // (an item without work for this group tells it nothing)
         }
         if (!C::kOne && quad == 0 && lane == 0) tc::bulk_wait();
     }
