@@ -38,8 +38,8 @@ namespace atc {
 constexpr int kThreads = 320;
 constexpr int kKeys = 128;                   // keys of a tile
 constexpr int kItems = 3;                    // items that the loading warp has described, at most
-constexpr uint32_t kHoldNs = 10000000;       // the hardware may hold a waiting warp for 10 ms,
-constexpr int kMaxTries = 200;               // and a wait gives up after 200 of them (2 s)
+constexpr uint32_t kHoldNs = 10000000;       // the hardware may hold a waiting warp for 10 ms at a time,
+constexpr uint64_t kGiveUpNs = 2000000000;   // and a wait gives up after 2 s
 constexpr float kLazyLog2 = 8.f;             // the running maximum moves when passed by 2^8
 
 // GROUPED: layout of the K and V tiles in shared memory.  false: column block by column block
@@ -141,7 +141,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                   *sm_out = sm_kv + C::kStages * C::kTile;
     constexpr int NS = C::kStages;
     __shared__ uint64_t kv_full[NS], kv_empty[NS], q_full[2], q_empty[2], s_full[2], p_ready[2], o_full[2], mdone,
-        i_full[kItems], i_empty[kItems], x_full, x_empty;
+        i_full[kItems], i_empty[kItems], x_full, x_empty, g_met[2];
     __shared__ uint32_t tmem_slot;
     __shared__ volatile int s_abort, s_bad;
     __shared__ float2 s_x[128];  // maximum and sum of the second pipeline's rows (keys dealt to both)
@@ -155,6 +155,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             mbar_init(&s_full[t], 1);
             mbar_init(&p_ready[t], 4);
             mbar_init(&o_full[t], 1);
+            mbar_init(&g_met[t], 4);
         }
         mbar_init(&mdone, 1);
         mbar_init(&x_full, 4);
@@ -183,19 +184,22 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         record_error(err, SFFN_ERR_DEVICE);
     }
 
-    // Bounded wait.  A wait that gives up records the error and goes on as if its phase had come (the
-    // results are not valid then), and every later wait passes at once: all loops still end,
-    // and a wait that is over costs one look and one branch, which counts between two products.
+    // Bounded wait of a whole warp: true once the phase has come.  One that runs out records the error and
+    // gives up, and so does every other wait of the CTA whose phase has not come by then.  A warp that gets
+    // false leaves its loops at once: nothing is loaded, issued or stored on behalf of a phase that never
+    // came.  The answer is the same in every lane.
     auto wait_slow = [&](uint64_t *bar, uint32_t parity) {
-        for (int tries = 0; !mbar_try_wait_for(bar, parity, kHoldNs) && !s_abort; ++tries)
-            if (tries == kMaxTries) {
-                s_abort = 1;
-                record_error(err, SFFN_ERR_TIMEOUT);
-            }
+        const uint64_t t0 = globaltimer_ns();
+        while (!__any_sync(0xffffffffu, s_abort || globaltimer_ns() - t0 > kGiveUpNs))
+            if (__all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kHoldNs))) return true;
+        if (lane == 0) {
+            s_abort = 1;
+            record_error(err, SFFN_ERR_TIMEOUT);
+        }
+        return false;
     };
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        if (!mbar_try_wait_for(bar, parity, kHoldNs)) wait_slow(bar, parity);
-        __syncwarp();
+        return __all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kHoldNs)) || wait_slow(bar, parity);
     };
 
     griddep_wait();
@@ -204,11 +208,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
     policy.start();
     griddep_launch_dependents();
     int item = 0;  // items taken so far
-    // The other warps' next item, and its return.
-    auto take = [&]() -> const Work & {
+    // The other warps' next item (null: none, or a wait gave up), and its return.
+    auto take = [&]() -> const Work * {
         const int i = item % kItems;
-        wait(&i_full[i], (uint32_t)((item / kItems) & 1));
-        return s_work[i];
+        return wait(&i_full[i], (uint32_t)((item / kItems) & 1)) && s_work[i].more ? &s_work[i] : nullptr;
     };
     auto give_back = [&]() {
         __syncwarp();
@@ -220,17 +223,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         // ---------------- loads ----------------
         int it = 0, qn[2] = {0, 0};
         const uint64_t keep = P::kReread ? tc::l2_evict_last_policy() : l2_evict_first_policy();
-        for (;; ++item) {
-            Work &w = s_work[item % kItems];
-            wait(&i_empty[item % kItems], (uint32_t)(((item / kItems) & 1) ^ 1));
-            const bool more = policy.next(w) && !s_abort;
-            __syncwarp();
-            if (lane == 0) {
-                w.more = more;
-                mbar_arrive(&i_full[item % kItems]);
-            }
-            __syncwarp();
-            if (!more) break;
+        auto load = [&](const Work &w) {  // an item's tiles; false: gave up
             const int tiles = w.tiles;
             int place = policy.place(w, 0, lane);
             for (int j = 0; j < tiles; ++j) {
@@ -238,7 +231,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 for (int part = 0; part < 2; ++part) {
                     // the item's queries: the first tile's before the first K, the second's after it
                     if (j == 0 && w.n[part] > 0 && part < C::kQ) {
-                        wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1));
+                        if (!wait(&q_empty[part], (uint32_t)((qn[part] & 1) ^ 1))) return false;
                         if (lane == 0) {
                             mbar_arrive_expect_tx(&q_full[part], (uint32_t)(TB * G * 128 * C::kHalves));
                             for (int c = 0; c < C::kHalves; ++c)
@@ -248,14 +241,27 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         ++qn[part];
                     }
                     const int s = it % NS;
-                    wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1));
+                    if (!wait(&kv_empty[s], (uint32_t)(((it / NS) & 1) ^ 1))) return false;
                     policy.load_kv(w, j, place, part ? &map_v : &map_k, sm_kv + s * C::kTile, &kv_full[s], lane, keep);
                     ++it;
                 }
                 place = nxt;
             }
+            return true;
+        };
+        for (;; ++item) {
+            Work &w = s_work[item % kItems];
+            if (!wait(&i_empty[item % kItems], (uint32_t)(((item / kItems) & 1) ^ 1))) break;
+            const bool more = policy.next(w);
+            __syncwarp();
+            if (lane == 0) {
+                w.more = more;
+                mbar_arrive(&i_full[item % kItems]);
+            }
+            __syncwarp();
+            if (!more || !load(w)) break;
         }
-        if (s_abort && lane == 0) {  // let the copies in flight land before the CTA can exit
+        if (lane == 0) {  // no copy is in flight when the CTA exits, whoever gave up
             for (int j = max(0, it - NS); j < it; ++j) mbar_wait(&kv_full[j % NS], (uint32_t)((j / NS) & 1));
             for (int t = 0; t < 2; ++t)
                 if (qn[t]) mbar_wait(&q_full[t], (uint32_t)((qn[t] - 1) & 1));
@@ -288,57 +294,59 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             if (++slot == NS) slot = 0, par ^= 1;
         };
         auto tile_of = [&](int s) { return kv_addr + (uint32_t)s * C::kTile; };
+        // (each of these: false if a wait gave up)
         auto first_scores = [&](int t) {
             if (t < C::kQ) {
-                wait(&q_full[t], q_par[t]);
+                if (!wait(&q_full[t], q_par[t])) return false;
                 q_par[t] ^= 1;
             }
             tc::fence_after_sync();
             scores(t, tile_of(slot));
+            return true;
         };
         auto weigh = [&](int t, uint32_t v, bool acc) {  // once the weights are there
-            wait(&p_ready[t], p_par[t]);
+            if (!wait(&p_ready[t], p_par[t])) return false;
             p_par[t] ^= 1;
             tc::fence_after_sync();
             values(t, v, acc);
+            return true;
         };
         // Two row tiles (or the first alone) over the same key tiles.
         auto both = [&](const int n0, const int n1) {
             const int n[2] = {n0, n1}, nmax = max(n0, n1);
-            wait(&kv_full[slot], par);
+            if (!wait(&kv_full[slot], par)) return false;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                if (n[t] > 0) first_scores(t);
+                if (n[t] > 0 && !first_scores(t)) return false;
             step();
             for (int j = 0; j < nmax; ++j) {
                 const int vs = slot;
-                wait(&kv_full[vs], par);
+                if (!wait(&kv_full[vs], par)) return false;
                 step();
                 const bool more = j + 1 < nmax;
-                if (more) wait(&kv_full[slot], par);
+                if (more && !wait(&kv_full[slot], par)) return false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (j < n[t]) {
-                        weigh(t, tile_of(vs), j > 0);
+                        if (!weigh(t, tile_of(vs), j > 0)) return false;
                         if (j + 1 == n[t]) tc::mma_commit_warp(&o_full[t]);
                     }
                     if (j + 1 < n[t]) scores(t, tile_of(slot));
                 }
                 if (more) step();
             }
+            return true;
         };
         // One row tile: pipeline t takes every other key tile.
         auto dealt = [&](const int tiles) {
-            wait(&kv_full[slot], par);
-            first_scores(0);
+            if (!wait(&kv_full[slot], par) || !first_scores(0)) return false;
             step();
             // V of tile i lies at the position of step i; K of tile i + 1 follows it
             int v_slot = slot;
             uint32_t v_par = par;
             step();
             if (tiles > 1) {
-                wait(&kv_full[slot], par);
-                first_scores(1);
+                if (!wait(&kv_full[slot], par) || !first_scores(1)) return false;
                 step();
             }
             if (C::kOne && tiles <= 2) tc::mma_commit_warp(&q_empty[0]);
@@ -346,8 +354,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (i + t < tiles) {
-                        wait(&kv_full[v_slot], v_par);
-                        weigh(t, tile_of(v_slot), i > 0);
+                        if (!wait(&kv_full[v_slot], v_par) || !weigh(t, tile_of(v_slot), i > 0)) return false;
                         // given back at once: S_t(i + 2) would say so too, but only after the next K's load
                         tc::mma_commit_warp(&kv_empty[v_slot]);
                         // on to the next tile's V; position `slot` is that of tile i + t + 1's V
@@ -355,7 +362,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         v_par = par;
                         if (i + t + 1 < tiles) step();
                         if (i + t + 2 < tiles) {
-                            wait(&kv_full[slot], par);
+                            if (!wait(&kv_full[slot], par)) return false;
                             tc::fence_after_sync();
                             scores(t, tile_of(slot));
                             step();
@@ -366,18 +373,20 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     }
                 }
             }
+            return true;
         };
         // The ring's tiles are given back by the softmax warps, which see S_t(j) arrive after their last
         // reader, with no more commits here (V of a dealt tile excepted).
         for (;; give_back()) {
-            const Work &w = take();
-            if (!w.more) break;
+            const Work *w = take();
+            if (!w) break;
             // uniform by construction; the reductions tell the compiler so
-            const int n0 = __reduce_max_sync(0xffffffffu, w.n[0]), n1 = __reduce_max_sync(0xffffffffu, w.n[1]);
-            if constexpr (C::kOne)
-                dealt(n0 + n1);
-            else
-                both(n0, n1);
+            const int n0 = __reduce_max_sync(0xffffffffu, w->n[0]), n1 = __reduce_max_sync(0xffffffffu, w->n[1]);
+            if constexpr (C::kOne) {
+                if (!dealt(n0 + n1)) break;
+            } else {
+                if (!both(n0, n1)) break;
+            }
         }
         // every product of this CTA has completed before teardown
         if (lane == 0) {
@@ -392,13 +401,20 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         const uint32_t ts = tmem + ((uint32_t)(quad * 32) << 16) + t * 128;
         const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + C::kColO + t * D;
         const float c = scale * 1.44269504088896341f;  // the exponent in powers of two
-        int sn = 0, on = 0, xn = 0, base = 0;
+        int sn = 0, on = 0, xn = 0, gn = 0, base = 0;
+        // The four warps of the group meet (their writes to shared memory are seen after it); false: gave up.
+        auto meet = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&g_met[t]);
+            return wait(&g_met[t], (uint32_t)(gn++ & 1));
+        };
         // Whether this warp knows that the fill before V_0 in its ring slot (V of the next to last key tile before this
         // item, or an older one) has landed: it does after the product with that tile or a later one.
         bool seen = true;
         for (;;) {
-            const Work &w = take();
-            if (!w.more) break;
+            const Work *next = take();
+            if (!next) break;
+            const Work &w = *next;
             const int n = w.n[t], tiles = w.tiles;
             constexpr bool dealt = C::kOne;
             const int item_tok = (dealt ? 0 : t * TB) + tok;  // token of the item
@@ -419,7 +435,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     if (masked && pass == (late ? 1 : 0)) {
                         // Non-finite values of this tile: zero (and noted, if their keys exist)
                         const int iv = k_at + 1, vs = iv % NS;
-                        wait(&kv_full[vs], (uint32_t)((iv / NS) & 1));
+                        if (!wait(&kv_full[vs], (uint32_t)((iv / NS) & 1))) goto done;
                         uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
                         const int kb = w.k0 + kt * kKeys;
 #pragma unroll 1
@@ -455,7 +471,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         fence_proxy_async_smem();
                     }
                     if (pass == 0) {
-                        wait(&s_full[t], (uint32_t)(sn & 1));
+                        if (!wait(&s_full[t], (uint32_t)(sn & 1))) goto done;
                         ++sn;
                         if (lane == 0 && quad == 0) {
                             // S_t(j) is there: Q_t is free after the last tile; K of this tile and V of the one
@@ -539,7 +555,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 l += l0 + l1;
             }
             if (n > 0) {
-                wait(&o_full[t], (uint32_t)(on & 1));
+                if (!wait(&o_full[t], (uint32_t)(on & 1))) goto done;
                 ++on;
                 if (releases && !dealt && lane == 0 && quad == 0) mbar_arrive_relaxed(&kv_empty[(base + 2 * n - 1) % NS]);
                 tc::fence_after_sync();
@@ -552,9 +568,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     tc::fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&x_full);
-                    wait(&x_empty, (uint32_t)(xn & 1));
+                    if (!wait(&x_empty, (uint32_t)(xn & 1))) goto done;
                 } else {
-                    wait(&x_full, (uint32_t)(xn & 1));
+                    if (!wait(&x_full, (uint32_t)(xn & 1))) goto done;
                     tc::fence_after_sync();
                     const float2 o = s_x[row];
                     const float mj = fmaxf(m, o.x), ref = mj == -INFINITY ? 0.f : mj;
@@ -631,7 +647,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
 #pragma unroll 1
                         for (int q2 = 0; q2 < D / 64; ++q2) {
                             if (issues) tc::bulk_wait_read();
-                            named_barrier_sync(1 + t, 128);
+                            if (!meet()) goto done;
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 uint32_t o[32];
@@ -649,7 +665,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                                 }
                             }
                             fence_proxy_async_smem();
-                            named_barrier_sync(1 + t, 128);
+                            if (!meet()) goto done;
                             if (issues) {
                                 tc::tma_store_3d(&map_o, q2 * 64, o_h, o_row, buf);
                                 tc::bulk_commit();
@@ -657,7 +673,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         }
                     } else {
                         if (issues) tc::bulk_wait_read();
-                        named_barrier_sync(1 + t, 128);
+                        if (!meet()) goto done;
                     }
                 }
                 // 64 bytes of every row at a time through shared memory, the 16-byte chunks swizzled by
@@ -707,6 +723,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             base += 2 * tiles;
             seen = !dealt && n > 0 && n >= tiles - 1;  // (an item without work for this group tells it nothing)
         }
+    done:
         if (!C::kOne && quad == 0 && lane == 0) tc::bulk_wait();
     }
     tc::fence_before_sync();
