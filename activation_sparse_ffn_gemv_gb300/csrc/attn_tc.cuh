@@ -388,11 +388,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 if (!both(n0, n1)) break;
             }
         }
-        // every product of this CTA has completed before teardown
-        if (lane == 0) {
-            tc::mma_commit(&mdone);
-            mbar_wait(&mdone, 0);
-        }
+        // Every product of this CTA has completed before teardown.  A commit covers its own thread's products, so
+        // it is issued as they are, by the elected lane of the whole warp.
+        tc::mma_commit_warp(&mdone);
+        mbar_wait(&mdone, 0);
     } else {
         // ---------------- softmax of row tile t ----------------
         const int t = (warp - 2) >> 2, quad = warp & 3;
