@@ -6,7 +6,8 @@ from __future__ import annotations
 import pytest
 import torch
 
-from tests.test_attention import S, gen, check_attention  # noqa: F401  (S: the library)
+from tests import test_attention as A
+from tests.test_attention import S, check_attention, gen  # noqa: F401  (S: the library)
 
 
 def packed(lens, hq, hkv, D, seed, scale=1.5):
@@ -55,3 +56,123 @@ def test_prompt_short_rests_before_whole_blocks(S, n, lo, hi, hq, hkv, D):
     for _ in range(5):
         assert torch.equal(prompt_call(S, hurt, cu, hq, hkv), want)
         assert torch.equal(prompt_call(S, qkv, cu, hq, hkv), good)
+
+
+# 28/4 heads of 128: a block is 36 tokens, so a CTA of 152 gets three or four whole blocks
+RAGGED = [100, 383, 700, 257, 129, 640, 36, 512, 333, 501, 128, 611]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,hkv,D,copies", [(28, 4, 128, 1), (16, 16, 64, 4), (12, 12, 128, 4), (64, 8, 64, 2)])
+def test_prompt_several_whole_items_a_cta(S, hq, hkv, D, copies):
+    """The rings of one item going on into the next, whole row tiles written while the next item runs; then
+    with infinite values in the middle and at the end of each prompt."""
+    lens = RAGGED * copies
+    qkv, cu = packed(lens, hq, hkv, D, 17 + D)
+    good = prompt_call(S, qkv, cu, hq, hkv)
+    check_prompt_rows(good, qkv, lens, hq, hkv, D, list(range(0, sum(lens), 97)) + (cu[1:] - 1).tolist()[:12])
+    assert torch.equal(prompt_call(S, qkv, cu, hq, hkv), good)
+    hurt, want = qkv.clone(), good.clone()
+    G = hq // hkv
+    for i, n in enumerate(lens):
+        a = int(cu[i])
+        for t, h, col, x in ((n // 2, 0, 3, float("inf")), (n - 1, hkv - 1, 5, -float("inf"))):
+            hurt[a + t, hq + hkv + h, col] = x
+            want[a + t:a + n, h * G:(h + 1) * G, col] = x
+    assert torch.equal(prompt_call(S, hurt, cu, hq, hkv), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_scores_that_grow_along_the_keys(S, D):
+    """Every key tile passes the running maximum, in all items of a CTA: key j is (j / n) of a direction
+    that every query has, for scores up to about 60."""
+    lens, hq, hkv = [700, 650, 333, 1100], 16, 16
+    qkv, cu = packed(lens, hq, hkv, D, 23, 0.4)
+    for i, n in enumerate(lens):
+        a = int(cu[i])
+        qkv[a:a + n, :hq, :8] = 4.0
+        qkv[a:a + n, hq:hq + hkv, :8] = (torch.arange(n) / n * 60 * D ** 0.5 / 32)[:, None, None].bfloat16()
+    good = prompt_call(S, qkv, cu, hq, hkv)
+    check_prompt_rows(good, qkv, lens, hq, hkv, D, list(range(0, sum(lens), 61)))
+
+
+# ---------------------------------------------------------------------------
+# the paged cache
+# ---------------------------------------------------------------------------
+
+def check_tree_rows(p, got, tokens):
+    """Every head of the packed new tokens `tokens` against the definition in 64 bits."""
+    got, G = got.cpu(), p.hq // p.hkv
+    for t in tokens:
+        s = next(i for i in range(len(p.n)) if p.cu[i] <= t < p.cu[i + 1])
+        c, n = p.ctx[s], p.n[s]
+        sees = torch.ones(c + n, dtype=torch.bool)
+        sees[c:] = torch.tensor([(p.masks[t] >> j) & 1 for j in range(n)], dtype=torch.bool)
+        q = p.q[t].double().view(p.hkv, G, p.D)
+        k, v = (x[s][sees].double().permute(1, 0, 2) for x in (p.k, p.v))
+        w = torch.softmax(q @ k.transpose(1, 2) * p.D ** -0.5, -1)
+        cond = (q.abs() @ k.abs().transpose(1, 2)).amax(-1, keepdim=True) * p.D ** -0.5
+        check_attention(got[t].view(p.hkv, G, p.D), w @ v, w @ v.abs(), cond, p.D, c + n, p.dt == "bf16")
+
+
+# ctx, new tokens, hq, hkv, D, page, dtype, growing scores
+LONG = [
+    ([13000], [8], 64, 8, 64, 64, "bf16", False),
+    ([13000], [8], 64, 8, 128, 64, "bf16", False),
+    ([13003], [1], 8, 8, 128, 16, "bf16", True),
+    ([12997], [3], 16, 8, 64, 128, "bf16", True),
+    ([20000], [2], 4, 1, 128, 256, "bf16", True),       # one item in 152 pieces
+    ([20000], [2], 4, 1, 64, 256, "f32", False),
+    ([9000, 4001], [5, 2], 8, 8, 64, 64, "f32", True),
+    ([6000], [8], 16, 8, 128, 64, "f32", True),
+    # many items: several whole ones a CTA
+    ([300, 517, 64, 449, 0, 601, 333, 128] * 5, [64, 40, 33, 64, 64, 1, 50, 64] * 5, 32, 8, 128, 32, "bf16", False),
+    ([300, 517, 64, 449, 0, 601, 333, 128] * 5, [64, 40, 33, 64, 64, 1, 50, 64] * 5, 28, 4, 64, 16, "bf16", True),
+    ([300, 517, 64, 449, 0, 601] * 4, [20, 40, 1, 64, 30, 1] * 4, 16, 8, 64, 32, "f32", True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("ctx,n,hq,hkv,D,page,dt,grow", LONG)
+def test_tree_long_contexts_and_many_items(S, ctx, n, hq, hkv, D, page, dt, grow):
+    """Unused places of the pages hold NaN.  With `grow`, key j is (j / n) of a direction that every query has:
+    the running maximum moves at every tile."""
+    p = A.Paged(S, ctx, n, hq, hkv, D, page, dt, sum(ctx) + hq + D)
+    if grow:
+        p.q[:, :, :8] = 4.0
+        for s, (c, m) in enumerate(zip(ctx, n)):
+            up = (torch.arange(c + m) / (c + m) * 60 * D ** 0.5 / 32)[:, None, None].expand(-1, hkv, 8).to(p.ck.dtype)
+            p.k[s][:, :, :8] = up
+            j = torch.arange(c + m)
+            p.ck[p.table[s][j // page].long().cuda(), :, (j % page).cuda(), :8] = up.cuda()
+    ws = S.alloc_attn_workspace(S.WS_ATTN_TREE, sum(n), len(n), hq, hkv, D)
+    out = p.call(S, workspace=ws)
+    assert S.read_device_error(ws) == 0
+    T = sum(n)
+    check_tree_rows(p, out, sorted({t for t in range(0, T, max(1, T // 40))} | {T - 1}))
+    assert torch.equal(out, p.call(S, workspace=ws))
+
+
+# ---------------------------------------------------------------------------
+# norms and rotation of many rows: several rows a lane
+# ---------------------------------------------------------------------------
+
+MANY = [
+    # T, hq, hkv, D, dtype, interleaved, rot, page, cache, k_out
+    (300, 32, 2, 128, "bf16", False, 128, 64, True, True),
+    (333, 28, 4, 128, "bf16", True, 64, 16, True, False),
+    (301, 33, 3, 128, "bf16", True, 128, 32, True, True),
+    (700, 16, 2, 64, "bf16", True, 64, 16, True, False),
+    (310, 32, 2, 128, "f32", False, 64, 64, True, True),
+    (333, 31, 1, 128, "f32", True, 128, 16, True, False),
+    (640, 14, 2, 64, "f32", False, 64, 32, True, True),
+    (640, 16, 4, 64, "f32", True, 32, 16, False, True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,hq,hkv,D,dt,inter,rot,page,cached,k_out", MANY)
+def test_rope_of_many_rows(S, T, hq, hkv, D, dt, inter, rot, page, cached, k_out):
+    assert T * (hq + 2 * hkv) >= 64 * 152
+    A.test_qk_norm_rope(S, T, hq, hkv, D, dt, True, inter, rot, page, cached, k_out)
