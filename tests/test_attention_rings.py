@@ -97,6 +97,46 @@ def test_prompt_scores_that_grow_along_the_keys(S, D):
     check_prompt_rows(good, qkv, lens, hq, hkv, D, list(range(0, sum(lens), 61)))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,hq,hkv,D", [(3000, 4, 2, 64), (1700, 4, 4, 128)])
+def test_prompt_thousands_of_sequences(S, n, hq, hkv, D):
+    """Lengths from 0 to a few blocks in no order, a few long ones far apart: every row belongs to its sequence."""
+    lens = [(13 * i * i + 7 * i) % 90 if i % 5 else 0 for i in range(n)]
+    for i, m in ((3, 900), (n // 2, 2000), (n - 1, 1400), (n - 200, 515)):
+        lens[i] = m
+    qkv, cu = packed(lens, hq, hkv, D, n)
+    ws = S.alloc_attn_workspace(S.WS_ATTN_PROMPT, sum(lens), n, hq, hkv, D)
+    out = prompt_call(S, qkv, cu, hq, hkv, ws)
+    assert S.read_device_error(ws) == 0
+    last = [int(b) - 1 for a, b in zip(cu[:-1], cu[1:]) if b > a]
+    check_prompt_rows(out, qkv, lens, hq, hkv, D, last[::9] + last[-3:] + list(range(0, sum(lens), 331)))
+    assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.gpu
+def test_prompt_time_grows_with_the_sequences_not_with_their_square(S):
+    """Four times the prompts of 16 tokens take about four times as long; finding each item by a search
+    from the first sequence took fifteen times as long.  Half way between in ratio: eight."""
+    hq, hkv, D = 16, 8, 128
+
+    def best(n):
+        q = torch.randn(16 * n, hq, D, device="cuda").bfloat16()
+        k = torch.randn(16 * n, hkv, D, device="cuda").bfloat16()
+        cu = (torch.arange(n + 1, device="cuda") * 16).int()
+        ws, out = S.alloc_attn_workspace(S.WS_ATTN_PROMPT, 16 * n, n, hq, hkv, D), torch.empty_like(q)
+        times = []
+        for _ in range(6):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            S.attn_prompt(q, k, k, cu, out=out, workspace=ws)
+            e[1].record()
+            torch.cuda.synchronize()
+            times.append(e[0].elapsed_time(e[1]))
+        return min(times[1:])
+
+    assert best(16384) < 8 * best(4096)
+
+
 # ---------------------------------------------------------------------------
 # the paged cache
 # ---------------------------------------------------------------------------
