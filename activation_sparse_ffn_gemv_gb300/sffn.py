@@ -8,6 +8,7 @@ activation_sparse_ffn_gemv_gb300.build``) the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -496,6 +497,14 @@ def _launch_stream(stream):
     return _stream(stream)
 
 
+def _made_on(stream):
+    """Context in which the outputs and workspaces that a call makes itself belong to its launch stream: their
+    memory is free, filled and used again in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class KVCache:
     """A paged key/value cache: k and v [n_pages, n_kv_heads, page_size, head_dim], fp32
     or bf16, contiguous.  Keeps the tensors alive and the C struct."""
@@ -555,12 +564,13 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v, table, positions, q_weight
     if table is not None:
         _need(table.dim() == 2, ERR_INVALID_ARG, where)
         max_pos, rot = table.shape
-    if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
-    if k_out is None and cache is None:
-        k_out = torch.empty((T, hkv, D), dtype=dt, device=q.device)
-    if workspace is None:
-        workspace = alloc_attn_workspace(WS_QK_NORM_ROPE, T, 1, hq, hkv, D, q.device)
+    with _made_on(stream):
+        if q_out is None:
+            q_out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+        if k_out is None and cache is None:
+            k_out = torch.empty((T, hkv, D), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_QK_NORM_ROPE, T, 1, hq, hkv, D, q.device)
     st = lib().sffn_qk_norm_rope(_TDTYPE[dt], q.data_ptr(), qs, k.data_ptr(), ks, _ptr(v), vs, T, hq, hkv, D,
                                  _vec(q_weight, D, dt, where), _vec(k_weight, D, dt, where), eps,
                                  _vec(table, 0, torch.float32, where), rot, max_pos, style,
@@ -586,10 +596,11 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     _need(kshape == vshape and kshape[0] == T and kshape[2] == D, ERR_SHAPE, where)
     cu = _vec(cu_seqlens, 2, torch.int32, where)
     n_seq = cu_seqlens.numel() - 1
-    if out is None:
-        out = torch.empty((T, hq, D), dtype=bf16, device=q.device)
-    if workspace is None:
-        workspace = alloc_attn_workspace(WS_ATTN_PROMPT, T, n_seq, hq, hkv, D, q.device)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((T, hq, D), dtype=bf16, device=q.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_ATTN_PROMPT, T, n_seq, hq, hkv, D, q.device)
     st = lib().sffn_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, hq, hkv, D, cu, n_seq,
                                 D ** -0.5 if scale is None else scale, _vec(out, T * hq * D, bf16, where),
                                 workspace.data_ptr(), workspace.numel(), _launch_stream(stream))
@@ -610,10 +621,11 @@ def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len
     _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
     _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
     n_seq, width = page_table.shape
-    if out is None:
-        out = torch.empty((T, hq, D), dtype=dt, device=q.device)
-    if workspace is None:
-        workspace = alloc_attn_workspace(WS_ATTN_TREE, T, n_seq, hq, cache.n_kv_heads, D, q.device)
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_ATTN_TREE, T, n_seq, hq, cache.n_kv_heads, D, q.device)
     i32 = torch.int32
     st = lib().sffn_attn_tree(q.data_ptr(), qs, T, hq, cache.c_ref, _vec(page_table, 0, i32, where), width,
                               _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
