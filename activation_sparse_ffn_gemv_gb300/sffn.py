@@ -487,6 +487,13 @@ def _vec(t, n: int, dtype, where: str):
     return t.data_ptr()
 
 
+def _space(workspace, where: str):
+    """Address and bytes of a workspace: contiguous device memory of any type."""
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise SffnError(ERR_WORKSPACE, where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 # address of the current stream of the current device, without the objects around it where torch has that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -576,7 +583,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v, table, positions, q_weight
                                  _vec(table, 0, torch.float32, where), rot, max_pos, style,
                                  _vec(positions, T, torch.int32, where), _vec(q_out, T * hq * D, dt, where),
                                  _vec(k_out, T * hkv * D, dt, where), None if cache is None else cache.c_ref,
-                                 _vec(slots, T, torch.int32, where), workspace.data_ptr(), workspace.numel(),
+                                 _vec(slots, T, torch.int32, where), *_space(workspace, where),
                                  _launch_stream(stream))
     _check(st, where)
     return q_out, k_out
@@ -603,7 +610,7 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
             workspace = alloc_attn_workspace(WS_ATTN_PROMPT, T, n_seq, hq, hkv, D, q.device)
     st = lib().sffn_attn_prompt(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, hq, hkv, D, cu, n_seq,
                                 D ** -0.5 if scale is None else scale, _vec(out, T * hq * D, bf16, where),
-                                workspace.data_ptr(), workspace.numel(), _launch_stream(stream))
+                                *_space(workspace, where), _launch_stream(stream))
     _check(st, where)
     return out
 
@@ -630,7 +637,7 @@ def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len
     st = lib().sffn_attn_tree(q.data_ptr(), qs, T, hq, cache.c_ref, _vec(page_table, 0, i32, where), width,
                               _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
                               _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
-                              _vec(out, T * hq * D, dt, where), workspace.data_ptr(), workspace.numel(),
+                              _vec(out, T * hq * D, dt, where), *_space(workspace, where),
                               _launch_stream(stream))
     _check(st, where)
     return out

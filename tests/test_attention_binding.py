@@ -52,3 +52,29 @@ def test_what_a_call_makes_belongs_to_its_launch_stream(S, monkeypatch, as_int):
     assert stream_of(here) == side.cuda_stream
     assert stream_of(S.attn_prompt(dev[:, :8], dev[:, 8:10], dev[:, 10:], cud)) == torch.cuda.current_stream().cuda_stream
     torch.cuda.synchronize()
+
+
+def test_a_workspace_in_host_memory_is_refused(S):  # noqa: F811
+    with pytest.raises(S.SffnError) as e:
+        S._space(torch.zeros(256, dtype=torch.uint8), "here")
+    assert e.value.status == S.ERR_WORKSPACE
+
+
+@pytest.mark.gpu
+def test_workspaces_that_a_call_takes(S):  # noqa: F811
+    """Refused before anything is launched: host memory, every other element of an array.  Taken: an
+    array of another type whose bytes are enough, which is measured in bytes."""
+    p = Paged(S, [20], [2], 4, 2, 64, 16, "bf16", 1)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    k, cu = q[:, :2].contiguous(), torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    need = S.attn_workspace_size(S.WS_ATTN_TREE, 2, 1, 4, 2, 64)
+    pos = torch.arange(3, device="cuda").int()
+    for ws in (torch.zeros(need, dtype=torch.uint8), torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        for call in (lambda: p.call(S, workspace=ws), lambda: S.attn_prompt(q, k, k, cu, workspace=ws),
+                     lambda: S.qk_norm_rope(q, k, None, S.rope_table(4, 64), pos, workspace=ws)):
+            with pytest.raises(S.SffnError) as e:
+                call()
+            assert e.value.status == S.ERR_WORKSPACE
+    p.check(p.call(S, workspace=torch.zeros(need // 4, dtype=torch.int32, device="cuda")))
+    with pytest.raises(S.SffnError):
+        p.call(S, workspace=torch.zeros(need // 4 - 64, dtype=torch.int32, device="cuda"))
