@@ -582,7 +582,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, v, table, positions, q_weight
                                  _vec(q_weight, D, dt, where), _vec(k_weight, D, dt, where), eps,
                                  _vec(table, 0, torch.float32, where), rot, max_pos, style,
                                  _vec(positions, T, torch.int32, where), _vec(q_out, T * hq * D, dt, where),
-                                 _vec(k_out, T * hkv * D, dt, where), None if cache is None else cache.c_ref,
+                                 _vec(k_out, T * hkv * D, dt, where), None if cache is None else cache.ref(),
                                  _vec(slots, T, torch.int32, where), *_space(workspace, where),
                                  _launch_stream(stream))
     _check(st, where)
@@ -634,7 +634,7 @@ def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len
         if workspace is None:
             workspace = alloc_attn_workspace(WS_ATTN_TREE, T, n_seq, hq, cache.n_kv_heads, D, q.device)
     i32 = torch.int32
-    st = lib().sffn_attn_tree(q.data_ptr(), qs, T, hq, cache.c_ref, _vec(page_table, 0, i32, where), width,
+    st = lib().sffn_attn_tree(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where), width,
                               _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
                               _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
                               _vec(out, T * hq * D, dt, where), *_space(workspace, where),
