@@ -17,7 +17,9 @@ namespace sffn {
 // item costs by itself; CTA w of W takes [w total / W, (w + 1) total / W) of the line, whatever
 // the lengths.  (48 sequences of one token, some a few positions long: 132 us without the extra
 // cost, because one CTA got all the short items of a sequence group, 92 with 2 units, 66 with 4, 65.5
-// with 5, 67 with 7; 32 with large draft trees 144, 130, 124.6 and 124.4.)  Row tiles of
+// with 5, 67 with 7; 32 with large draft trees, kernel and join on the device, 144, 130, 124.6 and 124.4, which a call
+// from Python among others takes 132 for.  It also cuts a short call into more pieces: one token over 300
+// positions, 32 heads, 12.2 us with 4, 13 with 5.)  Row tiles of
 // one key head are neighbours, so that they read its keys at about the same time.  An
 // item whose units lie in one CTA's range is finished there; the pieces of a cut item are
 // written as partial results (unnormalised output, running maximum and sum) and joined by

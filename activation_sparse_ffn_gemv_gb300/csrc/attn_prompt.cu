@@ -2,9 +2,9 @@
 // contiguous keys.
 //
 // Bound: the tensor cores for long prompts (4 D operations a visible (query, key)
-// pair), latency for short ones.  Measured: one prompt of 16384, 64/8 heads of 128: 2.83 ms,
-// 1.55 PFLOP/s (0.82 of cuBLAS's measured burst); 13 ragged prompts of 9075 tokens, 28/4
-// heads: 82 us; prompts of 1 to 130 tokens: 9.4 us.
+// pair), latency for short ones.  Measured (a call among others, from Python): one prompt of 16384, 64/8
+// heads of 128: 2.87 ms, 1.53 PFLOP/s (0.81 of cuBLAS's measured burst); 13 ragged prompts of 9075 tokens, 28/4
+// heads: 84.5 us; prompts of 2048, 1777 and 1, 32 heads of 64: 55 us; prompts of 1 to 130 tokens: 9.9 us.
 //
 // Work.  An item is 2 TB tokens (TB = 128 / G) of one sequence with every query head
 // of one key head; it runs over the keys up to its last token.  The longest items go

@@ -7,7 +7,7 @@
 // key by key, so a thread reads four rows' at once).  The next keys' rows are copied
 // meanwhile (cp.async, two buffers).  Bound: shared-memory reads of the two products,
 // about 5 a 16 multiply-adds.  Measured: 4 sequences of up to 4000 positions, 1 to 8 tokens, 16/2
-// heads of 64, 26 us with the join (latency: a CTA has one or two tiles).
+// heads of 64, 27.5 us with the join (latency: a CTA has one or two tiles).
 #pragma once
 
 #include "attn.cuh"

@@ -83,6 +83,7 @@ struct Work {
     int slot;           // tree: partial result slot
 };
 
+// 2^x, good to about 2^-22 of it (a bf16 weight needs 2^-9); weights below 2^-126 are zero.
 SFFN_DEV float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -529,6 +530,10 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 const float mc = (m == -INFINITY ? 0.f : m) * c;  // nothing seen yet: every weight is 2^-inf = 0
                 const uint64_t c2 = f32x2(__float_as_uint(c), __float_as_uint(c)),
                                mc2 = f32x2(__float_as_uint(-mc), __float_as_uint(-mc));
+                // The weights are rounded to bf16 because the second product takes both operands in one type and V
+                // is bf16; the sum is of the unrounded ones.  A weight is off by 2^-8 of itself at most, which
+                // adds to the output about what the output's own rounding does: against 64 bits the norm of the
+                // error goes from 0.0016 of the output's to 0.0018 (short prompts), 0.0020 (long ones), 0.0023 (a long context).
                 uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {

@@ -2,10 +2,11 @@
 // cache (sm_103a).
 //
 // Bound: HBM, the cached keys and values, each read once for all the new tokens and
-// all the query heads that share them.  Measured: 8 tokens over 65531 positions, 64/8 heads of
-// 128, 54 us (4.9 TB/s, 0.72 of the measured copy rate, about 12 us of it start, join and
-// tail); 48 ragged sequences of one token, 32/8 heads, 66 us (4.6 TB/s); one token over 300
-// positions 13 us.
+// all the query heads that share them.  Measured (a call among others, from Python): 8 tokens over 65531
+// positions, 64/8 heads of 128, 55 us (4.9 TB/s, 0.72 of the measured copy rate); 48 ragged sequences of one token, 32/8
+// heads, 65.5 us (4.6 TB/s); one token over 300 positions 13 us.  Over the contexts' lengths the first is 18 us and
+// 7.2 TB/s, the second 21 us and 6.9 TB/s (pages of 16; of 128: 20 us and 7.2 TB/s): what is fixed, start, item
+// boundaries, join and tail, keeps the calls from the copy rate, not the loads.
 #include "attn_rows.cuh"
 #include "attn_tc.cuh"
 
@@ -95,8 +96,8 @@ template <int D>
 struct TreePolicy {
     static constexpr bool kReread = false;
     const TreeArgs &a;
-    long long *pre;         // units before each sequence (shared memory)
-    long long u, u1;        // this CTA's next unit, and the end of its units
+    long long *pre;         // length of the line before each sequence (shared memory)
+    long long u, u1;        // this CTA's next place on the line, and the end of its range
     int G, TB, box;         // box: cache rows of one copy (a page's, 64 at most)
 
     struct RowInfo {

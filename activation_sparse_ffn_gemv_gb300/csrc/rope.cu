@@ -13,7 +13,7 @@
 // consecutive elements and a shuffle of every partner: 183 us for 16384 tokens of
 // 64 + 8 heads).  A warp takes U rows per lane group, all of one token and one kind (query, key
 // or value), so that addresses, weights, cosines and sines are found once for them and
-// all its loads are in flight together: 122.7 us there, 5.8 TB/s (0.86 of the measured copy
+// all its loads are in flight together: 124 us there, 5.75 TB/s (0.85 of the measured copy
 // rate); one token of 32 + 32 heads 1.8 us.
 #include "common.cuh"
 #include "internal.h"

@@ -457,7 +457,8 @@ sffn_status sffn_qk_norm_rope(int dtype, const void *q, int64_t q_stride, const 
  *   scale       finite, > 0 (usually 1 / sqrt(head_dim)).
  *   out         [T, n_heads, head_dim]; not one of the inputs.
  * Scores, the softmax's sums and the output accumulate in 32 bits; the weights
- * enter the second product as bf16.  Rows of other sequences and later rows of the
+ * enter the second product as bf16, so an output is off by up to 2^-8 of the weighted
+ * mean of |v| beside its own rounding.  Rows of other sequences and later rows of the
  * same one have no influence, whatever they hold (infinities and NaN included).
  * 0 <= T <= 1048576 (0: a no-op), 1 <= n_seq <= 65536. */
 sffn_status sffn_attn_prompt(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
@@ -484,7 +485,9 @@ sffn_status sffn_attn_prompt(const void *q, int64_t q_stride, const void *k, int
  * A sequence with a negative ctx_lens, more than 64 new tokens, tokens outside [0, T]
  * or more positions than its table's row holds is skipped (its rows are not
  * written) and recorded (SFFN_ERR_DEVICE); a page outside the cache reads as zeros
- * and is recorded.  Cache contents that a token does not see have no influence,
+ * and is recorded.  Scores, the softmax's sums and the output accumulate in 32 bits; with a bf16
+ * cache the weights enter the second product as bf16 (as in sffn_attn_prompt), with an fp32
+ * cache everything is fp32.  Cache contents that a token does not see have no influence,
  * whatever they hold.  The split of the work over the device depends on the lengths
  * alone: equal calls give equal bits.
  * 0 <= T <= 65536 (0: a no-op), 1 <= n_seq <= 1024, 1 <= table_width. */
