@@ -45,7 +45,7 @@ def timed_out(S, ws, call):  # noqa: F811
     torch.cuda.synchronize()
     took = time.monotonic() - t0
     assert S.read_device_error(ws) == S.ERR_TIMEOUT and S.read_device_error(ws) == 0
-    assert 1.5 < took < 6.0, took  # two seconds of waiting, at most one more for what was left out
+    assert 1.5 < took < 10.0, took  # two seconds of waiting, one more for the copies in flight, loading the module
 
 
 # which load of each CTA: the first K, the first V, one inside an item, one of a later item, one that only
