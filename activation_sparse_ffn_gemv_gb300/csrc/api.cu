@@ -148,6 +148,13 @@ sffn_status check_cache(const sffn_kv_cache *c, int dtype, int n_kv_heads, int h
     return SFFN_OK;
 }
 
+// A cache by itself, and query heads that go with it.
+sffn_status check_cached_heads(const sffn_kv_cache *c, int n_heads) {
+    if (!c || (c->dtype != SFFN_F32 && c->dtype != SFFN_BF16)) return SFFN_ERR_INVALID_ARG;
+    const sffn_status st = check_heads(n_heads, c->n_kv_heads, c->head_dim);
+    return st != SFFN_OK ? st : check_cache(c, c->dtype, c->n_kv_heads, c->head_dim);
+}
+
 int log2_of(int v) {
     int n = 0;
     while ((1 << n) < v) ++n;
@@ -475,6 +482,15 @@ size_t sffn_attn_workspace_size(int which, int T, int n_seq, int n_heads, int n_
                      f = make_tree_plan(SFFN_F32, T, n_heads, n_kv_heads, head_dim).total;
         return b > f ? b : f;
     }
+    if (which == 4) {
+        if (T > kTreeMaxT || n_seq < 1 || n_seq > kTreeMaxSeq || device_sm_count() <= 0) return 0;
+        return make_shared_plan(T, n_heads, n_kv_heads, head_dim).total;
+    }
+    if (which == 5) return kAlign;
+    if (which == 6) {
+        if (T > kTreeMaxT || device_sm_count() <= 0) return 0;
+        return make_pages_plan(T, n_heads, n_kv_heads, head_dim).total;
+    }
     return 0;
 }
 
@@ -625,6 +641,164 @@ sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, 
     a.rows_max = p.rows_max;
     a.err = static_cast<int32_t *>(workspace);
     st = run_attn_tree(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+// ---- long contexts ----
+
+sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                             const int32_t *page_table, int table_width, const int32_t *ctx_lens,
+                             const int32_t *cu_tokens, int n_seq, const int32_t *group_seqs,
+                             const int32_t *prefix_lens, int n_groups, const uint64_t *tree_mask, float scale,
+                             void *out, void *workspace, size_t ws_bytes, sffn_stream_t stream) {
+    sffn_status st = check_cached_heads(cache, n_heads);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > kTreeMaxT || n_seq < 1 || n_seq > kTreeMaxSeq || table_width < 1) return SFFN_ERR_SHAPE;
+    if (n_groups < 1 || n_groups > kSharedMaxGroups) return SFFN_ERR_SHAPE;
+    if (!(scale > 0.f) || std::isinf(scale)) return SFFN_ERR_INVALID_ARG;
+    if (T == 0) return SFFN_OK;
+    if (!q || !page_table || !ctx_lens || !cu_tokens || !group_seqs || !prefix_lens || !out) return SFFN_ERR_INVALID_ARG;
+    st = check_rows(q, q_stride, n_heads, cache->head_dim, cache->dtype == SFFN_BF16 ? 2 : 4);
+    if (st != SFFN_OK) return st;
+    if (!aligned16(out)) return SFFN_ERR_ALIGNMENT;
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7u) != 0) return SFFN_ERR_ALIGNMENT;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    const SharedPlan p = make_shared_plan(T, n_heads, cache->n_kv_heads, cache->head_dim);
+    st = check_ws(workspace, ws_bytes, p.total);
+    if (st != SFFN_OK) return st;
+    SharedArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.n_heads = n_heads;
+    a.n_kv_heads = cache->n_kv_heads;
+    a.group = n_heads / cache->n_kv_heads;
+    a.ck = cache->k;
+    a.cv = cache->v;
+    a.page_shift = log2_of(cache->page_size);
+    a.n_pages = cache->n_pages;
+    a.page_table = page_table;
+    a.table_width = table_width;
+    a.ctx_lens = ctx_lens;
+    a.cu_tokens = cu_tokens;
+    a.n_seq = n_seq;
+    a.group_seqs = group_seqs;
+    a.prefix_lens = prefix_lens;
+    a.n_groups = n_groups;
+    a.tree_mask = tree_mask;
+    a.scale = scale;
+    a.out = out;
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_attn_shared(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+sffn_status sffn_page_bounds(const sffn_kv_cache *cache, const int32_t *pages, int n, void *bounds, void *workspace,
+                             size_t ws_bytes, sffn_stream_t stream) {
+    sffn_status st = check_cached_heads(cache, cache ? cache->n_kv_heads : 0);
+    if (st != SFFN_OK) return st;
+    if (n < 0 || n > (1 << 20)) return SFFN_ERR_SHAPE;
+    if (n == 0) return SFFN_OK;
+    if (!pages || !bounds) return SFFN_ERR_INVALID_ARG;
+    if (!aligned16(bounds)) return SFFN_ERR_ALIGNMENT;
+    st = check_ws(workspace, ws_bytes, kAlign);
+    if (st != SFFN_OK) return st;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    BoundsArgs a = {};
+    a.ck = cache->k;
+    a.n_kv_heads = cache->n_kv_heads;
+    a.page_shift = log2_of(cache->page_size);
+    a.n_pages = cache->n_pages;
+    a.pages = pages;
+    a.n = n;
+    a.bounds = bounds;
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_page_bounds(a, cache->dtype, cache->head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+size_t sffn_page_select_workspace_size(int T, int n_kv_heads, int table_width) {
+    if (T < 0 || T > kTreeMaxT || n_kv_heads < 1 || n_kv_heads > 1024 || table_width < 1 || table_width > kSelectMaxPages)
+        return 0;
+    return page_select_workspace(T, n_kv_heads, table_width);
+}
+
+sffn_status sffn_page_select(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                             const void *bounds, const int32_t *page_table, int table_width, int n_seq,
+                             const int32_t *seqs, const int32_t *positions, int n_first, int n_recent, int n_keep,
+                             int32_t *sel, int32_t *n_sel, void *workspace, size_t ws_bytes, sffn_stream_t stream) {
+    sffn_status st = check_cached_heads(cache, n_heads);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > kTreeMaxT || table_width < 1 || table_width > kSelectMaxPages || n_seq < 1) return SFFN_ERR_SHAPE;
+    if (n_keep < 1 || n_keep > kMaxKeep) return SFFN_ERR_SHAPE;
+    if (n_first < 0 || n_recent < 1 || n_first > n_keep - n_recent) return SFFN_ERR_INVALID_ARG;
+    if (T == 0) return SFFN_OK;
+    if (!q || !bounds || !page_table || !seqs || !positions || !sel || !n_sel) return SFFN_ERR_INVALID_ARG;
+    st = check_rows(q, q_stride, n_heads, cache->head_dim, cache->dtype == SFFN_BF16 ? 2 : 4);
+    if (st != SFFN_OK) return st;
+    if (!aligned16(bounds)) return SFFN_ERR_ALIGNMENT;
+    st = check_ws(workspace, ws_bytes, page_select_workspace(T, cache->n_kv_heads, table_width));
+    if (st != SFFN_OK) return st;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    SelectPagesArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.n_heads = n_heads;
+    a.n_kv_heads = cache->n_kv_heads;
+    a.group = n_heads / cache->n_kv_heads;
+    a.at = {page_table, table_width, n_seq, log2_of(cache->page_size), cache->n_pages, seqs, positions};
+    a.bounds = bounds;
+    a.n_first = n_first;
+    a.n_recent = n_recent;
+    a.n_keep = n_keep;
+    a.sel = sel;
+    a.n_sel = n_sel;
+    a.scores = reinterpret_cast<float *>(static_cast<char *>(workspace) + kAlign);
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_page_select(a, cache->dtype, cache->head_dim, (cudaStream_t)stream);
+    if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
+    return st;
+}
+
+sffn_status sffn_attn_pages(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                            const int32_t *page_table, int table_width, int n_seq, const int32_t *seqs,
+                            const int32_t *positions, const int32_t *sel, const int32_t *n_sel, int n_keep,
+                            float scale, void *out, void *workspace, size_t ws_bytes, sffn_stream_t stream) {
+    sffn_status st = check_cached_heads(cache, n_heads);
+    if (st != SFFN_OK) return st;
+    if (T < 0 || T > kTreeMaxT || table_width < 1 || n_seq < 1) return SFFN_ERR_SHAPE;
+    if (n_keep < 1 || n_keep > kMaxKeep) return SFFN_ERR_SHAPE;
+    if (!(scale > 0.f) || std::isinf(scale)) return SFFN_ERR_INVALID_ARG;
+    if (T == 0) return SFFN_OK;
+    if (!q || !page_table || !seqs || !positions || !sel || !n_sel || !out) return SFFN_ERR_INVALID_ARG;
+    st = check_rows(q, q_stride, n_heads, cache->head_dim, cache->dtype == SFFN_BF16 ? 2 : 4);
+    if (st != SFFN_OK) return st;
+    if (!aligned16(out)) return SFFN_ERR_ALIGNMENT;
+    if (device_sm_count() <= 0) return SFFN_ERR_CUDA;
+    const PagesPlan p = make_pages_plan(T, n_heads, cache->n_kv_heads, cache->head_dim);
+    st = check_ws(workspace, ws_bytes, p.total);
+    if (st != SFFN_OK) return st;
+    PagesArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.T = T;
+    a.n_heads = n_heads;
+    a.n_kv_heads = cache->n_kv_heads;
+    a.group = n_heads / cache->n_kv_heads;
+    a.at = {page_table, table_width, n_seq, log2_of(cache->page_size), cache->n_pages, seqs, positions};
+    a.ck = cache->k;
+    a.cv = cache->v;
+    a.sel = sel;
+    a.n_sel = n_sel;
+    a.n_keep = n_keep;
+    a.scale = scale;
+    a.out = out;
+    a.err = static_cast<int32_t *>(workspace);
+    st = run_attn_pages(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
     return st;
 }

@@ -207,4 +207,70 @@ struct TreePlan {
 TreePlan make_tree_plan(int dtype, int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_tree(const TreeArgs &a, const TreePlan &p, int dtype, int head_dim, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Long contexts
+// ---------------------------------------------------------------------------
+
+constexpr int kSharedMaxGroups = 256;  // groups of one sffn_attn_shared call
+struct SharedArgs : TreeArgs {
+    const int32_t *group_seqs, *prefix_lens;
+    int n_groups;
+};
+struct SharedPlan {
+    size_t total;
+};
+SharedPlan make_shared_plan(int T, int n_heads, int n_kv_heads, int head_dim);
+sffn_status run_attn_shared(const SharedArgs &a, const SharedPlan &p, int dtype, int head_dim, cudaStream_t s);
+
+struct BoundsArgs {
+    const void *ck;
+    int n_kv_heads, page_shift, n_pages;
+    const int32_t *pages;
+    int n;
+    void *bounds;
+    int32_t *err;
+};
+sffn_status run_page_bounds(const BoundsArgs &a, int dtype, int head_dim, cudaStream_t s);
+
+// Where T tokens stand in the paged cache: sequence and position of each.
+struct Places {
+    const int32_t *page_table;
+    int table_width, n_seq, page_shift, n_pages;
+    const int32_t *seqs, *positions;
+};
+
+constexpr int kSelectMaxPages = 32768;  // table width of sffn_page_select
+constexpr int kMaxKeep = 4096;          // chosen pages of a token and key head
+struct SelectPagesArgs {
+    const void *q;
+    long long q_stride;
+    int T, n_heads, n_kv_heads, group;
+    Places at;
+    const void *bounds;
+    int n_first, n_recent, n_keep;
+    int32_t *sel, *n_sel;
+    float *scores;  // [T, n_kv_heads, table_width]
+    int32_t *err;
+};
+size_t page_select_workspace(int T, int n_kv_heads, int table_width);
+sffn_status run_page_select(const SelectPagesArgs &a, int dtype, int head_dim, cudaStream_t s);
+
+struct PagesArgs {
+    const void *q;
+    long long q_stride;
+    int T, n_heads, n_kv_heads, group;
+    Places at;
+    const void *ck, *cv;
+    const int32_t *sel, *n_sel;
+    int n_keep;
+    float scale;
+    void *out;
+    int32_t *err;
+};
+struct PagesPlan {
+    size_t total;
+};
+PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim);
+sffn_status run_attn_pages(const PagesArgs &a, const PagesPlan &p, int dtype, int head_dim, cudaStream_t s);
+
 }  // namespace sffn

@@ -29,6 +29,7 @@ _PRESET = {"speed": PRESET_SPEED, "balanced": PRESET_BALANCED, "quality": PRESET
 NOALLOC_SCRATCH_BYTES = 4 << 20
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 WS_QK_NORM_ROPE, WS_ATTN_PROMPT, WS_ATTN_TREE = 0, 1, 2
+WS_ATTN_SHARED, WS_PAGE_BOUNDS, WS_ATTN_PAGES = 4, 5, 6
 
 _WDTYPE = {"f32": F32, "bf16": BF16, "int4_g64": INT4_G64}
 _ACT = {"relu": ACT_RELU, "silu": ACT_SILU}
@@ -128,6 +129,16 @@ def lib():
         L.sffn_attn_prompt.restype = I
         L.sffn_attn_tree.argtypes = [P, I64, I, I, KV, P, I, P, P, I, P, F, P, P, S, P]
         L.sffn_attn_tree.restype = I
+        L.sffn_attn_shared.argtypes = [P, I64, I, I, KV, P, I, P, P, I, P, P, I, P, F, P, P, S, P]
+        L.sffn_attn_shared.restype = I
+        L.sffn_page_bounds.argtypes = [KV, P, I, P, P, S, P]
+        L.sffn_page_bounds.restype = I
+        L.sffn_page_select_workspace_size.argtypes = [I, I, I]
+        L.sffn_page_select_workspace_size.restype = S
+        L.sffn_page_select.argtypes = [P, I64, I, I, KV, P, P, I, I, P, P, I, I, I, P, P, P, S, P]
+        L.sffn_page_select.restype = I
+        L.sffn_attn_pages.argtypes = [P, I64, I, I, KV, P, I, I, P, P, P, P, I, F, P, P, S, P]
+        L.sffn_attn_pages.restype = I
         _lib = L
     return _lib
 
@@ -512,6 +523,12 @@ def _made_on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
+def _here(t: torch.Tensor, where: str):
+    """A call runs on the current device: its tensors have to be there."""
+    if t.device.index != torch.cuda.current_device():
+        raise SffnError(ERR_INVALID_ARG, where)
+
+
 class KVCache:
     """A paged key/value cache: k and v [n_pages, n_kv_heads, page_size, head_dim], fp32
     or bf16, contiguous.  Keeps the tensors alive and the C struct."""
@@ -639,5 +656,127 @@ def attn_tree(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len
                               _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
                               _vec(out, T * hq * D, dt, where), *_space(workspace, where),
                               _launch_stream(stream))
+    _check(st, where)
+    return out
+
+
+# ---- long contexts ----
+
+def attn_shared(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_lens: torch.Tensor,
+                cu_tokens: torch.Tensor, group_seqs: torch.Tensor, prefix_lens: torch.Tensor, tree_mask=None, scale=None,
+                out=None, workspace=None, stream=None):
+    """attn_tree for sequences that share prefixes: group g is sequences group_seqs[g] .. group_seqs[g + 1] - 1
+    (int32 [n_groups + 1]) and has its first prefix_lens[g] positions in common (int32 [n_groups]); the whole
+    pages among them are read once for the group.  Returns out [T, n_heads, D]."""
+    where = "sffn_attn_shared"
+    qshape, dt = q.shape, q.dtype
+    qs = _rows(q, qshape, where)
+    _here(q, where)
+    _here(cache.k, where)
+    T, hq, D = qshape
+    _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
+    _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
+    n_seq, width = page_table.shape
+    n_groups = prefix_lens.numel()
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_ATTN_SHARED, T, n_seq, hq, cache.n_kv_heads, D, q.device)
+    i32 = torch.int32
+    st = lib().sffn_attn_shared(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where), width,
+                                _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
+                                _vec(group_seqs, n_groups + 1, i32, where), _vec(prefix_lens, 0, i32, where), n_groups,
+                                _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
+                                _vec(out, T * hq * D, dt, where), *_space(workspace, where), _launch_stream(stream))
+    _check(st, where)
+    return out
+
+
+def page_bounds(cache: KVCache, pages: torch.Tensor, bounds=None, workspace=None, stream=None):
+    """Key bounds of the pages listed (int32 [n]; -1: nothing to do), into bounds: bf16 [n_pages, n_kv_heads, 2, D],
+    largest keys, then least (zeros where not listed, if none are given).  Returns bounds."""
+    where = "sffn_page_bounds"
+    _here(cache.k, where)
+    n, hkv, D = pages.numel(), cache.n_kv_heads, cache.head_dim
+    with _made_on(stream):
+        if bounds is None:
+            bounds = torch.zeros((cache.n_pages, hkv, 2, D), dtype=torch.bfloat16, device=cache.k.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_PAGE_BOUNDS, n, 1, hkv, hkv, D, cache.k.device)
+    st = lib().sffn_page_bounds(cache.ref(), _vec(pages, 0, torch.int32, where), n,
+                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where),
+                                *_space(workspace, where), _launch_stream(stream))
+    _check(st, where)
+    return bounds
+
+
+def alloc_page_select_workspace(T: int, n_kv_heads: int, table_width: int, device=None) -> torch.Tensor:
+    nbytes = int(lib().sffn_page_select_workspace_size(int(T), int(n_kv_heads), int(table_width)))
+    if nbytes == 0:
+        raise SffnError(ERR_SHAPE, "sffn_page_select_workspace_size")
+    return torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def page_select(q: torch.Tensor, cache: KVCache, bounds: torch.Tensor, page_table: torch.Tensor, seqs: torch.Tensor,
+                positions: torch.Tensor, n_keep: int, n_first: int = 1, n_recent: int = 1, sel=None, n_sel=None,
+                workspace=None, stream=None):
+    """The n_keep pages that each token of q [T, n_heads, D] reads, per key head: the first n_first, the last n_recent
+    and those with the largest scores against their key bounds.  seqs, positions int32 [T]: each token's row
+    of page_table [n_seq, width] and its position.  Returns (sel [T, n_kv_heads, n_keep] ascending, then -1; n_sel [T])."""
+    where = "sffn_page_select"
+    qshape, dt = q.shape, q.dtype
+    qs = _rows(q, qshape, where)
+    _here(q, where)
+    _here(cache.k, where)
+    T, hq, D = qshape
+    hkv = cache.n_kv_heads
+    _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
+    _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
+    n_seq, width = page_table.shape
+    i32 = torch.int32
+    with _made_on(stream):
+        if sel is None:
+            sel = torch.empty((T, hkv, max(n_keep, 0)), dtype=i32, device=q.device)
+        if n_sel is None:
+            n_sel = torch.empty(T, dtype=i32, device=q.device)
+        if workspace is None:
+            workspace = alloc_page_select_workspace(T, hkv, width, q.device)
+    st = lib().sffn_page_select(q.data_ptr(), qs, T, hq, cache.ref(),
+                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where),
+                                _vec(page_table, 0, i32, where), width, n_seq, _vec(seqs, T, i32, where),
+                                _vec(positions, T, i32, where), n_first, n_recent, n_keep,
+                                _vec(sel, T * hkv * n_keep, i32, where), _vec(n_sel, T, i32, where),
+                                *_space(workspace, where), _launch_stream(stream))
+    _check(st, where)
+    return sel, n_sel
+
+
+def attn_pages(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seqs: torch.Tensor, positions: torch.Tensor,
+               sel: torch.Tensor, n_sel: torch.Tensor, scale=None, out=None, workspace=None, stream=None):
+    """Attention of each token of q [T, n_heads, D] over the positions up to its own in its chosen pages (sel int32
+    [T, n_kv_heads, n_keep], n_sel int32 [T], as page_select returns them).  Returns out [T, n_heads, D]."""
+    where = "sffn_attn_pages"
+    qshape, dt = q.shape, q.dtype
+    qs = _rows(q, qshape, where)
+    _here(q, where)
+    _here(cache.k, where)
+    T, hq, D = qshape
+    hkv = cache.n_kv_heads
+    _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
+    _need(page_table.dim() == 2 and sel.dim() == 3, ERR_INVALID_ARG, where)
+    n_seq, width = page_table.shape
+    n_keep = sel.shape[2]
+    _need(sel.shape[0] >= T and sel.shape[1] == hkv, ERR_SHAPE, where)
+    i32 = torch.int32
+    with _made_on(stream):
+        if out is None:
+            out = torch.empty((T, hq, D), dtype=dt, device=q.device)
+        if workspace is None:
+            workspace = alloc_attn_workspace(WS_ATTN_PAGES, T, n_seq, hq, hkv, D, q.device)
+    st = lib().sffn_attn_pages(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where), width, n_seq,
+                               _vec(seqs, T, i32, where), _vec(positions, T, i32, where), _vec(sel, 0, i32, where),
+                               _vec(n_sel, T, i32, where), n_keep, D ** -0.5 if scale is None else scale,
+                               _vec(out, T * hq * D, dt, where), *_space(workspace, where), _launch_stream(stream))
     _check(st, where)
     return out

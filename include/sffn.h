@@ -496,6 +496,91 @@ sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, 
                            const int32_t *cu_tokens, int n_seq, const uint64_t *tree_mask, float scale, void *out,
                            void *workspace, size_t ws_bytes, sffn_stream_t stream);
 
+/* ---- Long contexts ----
+ *
+ * What sffn_attn_tree reads grows with every sequence's whole context.  Two ways of reading less:
+ *   sffn_attn_shared   sequences that begin with the same pages read those once for all of them;
+ *   sffn_page_bounds, sffn_page_select, sffn_attn_pages
+ *                      each token reads the few pages whose keys can matter to it: the pages' key
+ *                      bounds are kept beside the cache, a cheap score of the queries against
+ *                      them picks the pages, and the attention runs over those alone.
+ * Heads, rows and the cache as above; workspaces from sffn_attn_workspace_size (which: 4 = sffn_attn_shared,
+ * 5 = sffn_page_bounds with T pages, 6 = sffn_attn_pages) and sffn_page_select_workspace_size. */
+
+/* sffn_attn_tree for sequences that share prefixes: same result, but a group's common prefix is read once for
+ * all its tokens.  Arguments as sffn_attn_tree, and
+ *   group_seqs   int32 [n_groups + 1], device: group g is sequences group_seqs[g] .. group_seqs[g + 1] - 1;
+ *                ascending, from 0 to n_seq (empty groups are fine).
+ *   prefix_lens  int32 [n_groups], device: positions that the sequences of the group have in common, 0 or
+ *                more.  The whole pages among them are the first entries of every table row of the group,
+ *                alike in all of them (read from its first sequence's row); positions behind the last whole
+ *                page are read from each sequence's own row.
+ * A sequence of a group that is not a range of sequences, whose prefix is negative or longer than its table's row, or
+ * whose whole prefix pages hold more than its ctx_lens positions, is skipped and recorded like one that breaks
+ * sffn_attn_tree's rules.
+ * 0 <= T <= 65536 (0: a no-op), 1 <= n_seq <= 1024, 1 <= n_groups <= 256. */
+sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                             const int32_t *page_table, int table_width, const int32_t *ctx_lens,
+                             const int32_t *cu_tokens, int n_seq, const int32_t *group_seqs,
+                             const int32_t *prefix_lens, int n_groups, const uint64_t *tree_mask, float scale,
+                             void *out, void *workspace, size_t ws_bytes, sffn_stream_t stream);
+
+/* Key bounds of whole pages: for each listed page and key head, per column the largest and the least of the
+ * page's keys, rounded outwards to whole multiples of a step:
+ *   step = 2^e, e the least integer >= -100 with max |key| <= 127 * 2^e (over the page's keys of that head);
+ *   hi = ceil(max / step) * step,  lo = floor(min / step) * step.
+ * bf16 holds both exactly.  Keys count as at most 2^100 in magnitude, a NaN as both 2^100 and -2^100.
+ *   pages    int32 [n], device: pages of the cache (every position of them written).  -1: nothing to do (a step
+ *            in which a sequence has filled no page); others outside the cache are skipped and
+ *            recorded (SFFN_ERR_DEVICE).  A page may be listed twice.
+ *   bounds   bf16 [n_pages, n_kv_heads, 2, head_dim]: hi, then lo; the listed pages' entries are written.
+ * 0 <= n <= 1048576 (0: a no-op). */
+sffn_status sffn_page_bounds(const sffn_kv_cache *cache, const int32_t *pages, int n, void *bounds, void *workspace,
+                             size_t ws_bytes, sffn_stream_t stream);
+
+/* Bytes of workspace for sffn_page_select (0 for an invalid request). */
+size_t sffn_page_select_workspace_size(int T, int n_kv_heads, int table_width);
+
+/* The pages that each of T tokens reads, per key head.  Token t stands at logical position p = positions[t] of
+ * the sequence whose pages are row seqs[t] of page_table; pages are numbered by position, and its own is
+ * m = p / page_size.  With m + 1 <= n_keep it reads all pages 0 .. m.  Else it reads the first n_first, the
+ * last n_recent (its own among them) and, up to n_keep in all, those of the others with the largest
+ *   score(page) = max over the key head's query heads of sum_d max(c_d, 0) hi_d + min(c_d, 0) lo_d,
+ * ties to the lower page; c is the query rounded to whole multiples of a step (found as in
+ * sffn_page_bounds, over the query heads of the key head; in units of that step; NaN counts as 0).  But for that rounding
+ * the score bounds every key's score in the page from above.  The sums are exact in 32 bits, so the choice
+ * does not depend on the order in which they are made.
+ *   q          [T, n_heads, head_dim] in the cache's dtype, token stride q_stride.
+ *   cache      shape and type (keys and values are not read).
+ *   bounds     as written by sffn_page_bounds, for every page below each token's n_recent last ones.
+ *   page_table int32 [n_seq, table_width], table_width <= 32768.  seqs, positions  int32 [T], device.
+ *   sel        int32 [T, n_kv_heads, n_keep]: the pages' numbers in ascending order, then -1.
+ *   n_sel      int32 [T]: how many (min(m + 1, n_keep), the same for all heads).
+ * A token of negative position is padding: n_sel 0.  One whose sequence is outside [0, n_seq) or whose position is
+ * outside its table's row has n_sel 0 and is recorded (SFFN_ERR_DEVICE); the bounds of a page outside the cache count
+ * as zeros and are recorded.
+ * n_first >= 0, n_recent >= 1, n_first + n_recent <= n_keep <= 4096; 0 <= T <= 65536 (0: a no-op), n_seq >= 1. */
+sffn_status sffn_page_select(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                             const void *bounds, const int32_t *page_table, int table_width, int n_seq,
+                             const int32_t *seqs, const int32_t *positions, int n_first, int n_recent, int n_keep,
+                             int32_t *sel, int32_t *n_sel, void *workspace, size_t ws_bytes, sffn_stream_t stream);
+
+/* Attention of T tokens, each over the positions up to its own in its chosen pages, per key head:
+ *   out_t = sum_j softmax_j(scale * q_t . k_j) v_j,  j <= positions[t] in the pages sel[t, h, 0 .. n_sel[t] - 1].
+ *   sel, n_sel   as sffn_page_select writes them, or made by the caller: 0 <= n_sel[t] <= n_keep; pages ascending, none
+ *                past the token's own.  An entry that is, or is outside the table, reads as a page of zeros and is
+ *                recorded, as is a page outside the cache.
+ *   page_table, seqs, positions  as sffn_page_select.  A token of negative position is padding: its row of out
+ *                is left as it is.  One whose sequence, position or n_sel is out of range is skipped (likewise)
+ *                and recorded.  With n_sel 0 the row is zeros.
+ *   scale        finite, > 0.   out  [T, n_heads, head_dim].
+ * Precision as sffn_attn_tree; what a token does not see has no influence, whatever it holds; equal calls give
+ * equal bits.  0 <= T <= 65536 (0: a no-op), n_seq >= 1, 1 <= n_keep <= 4096. */
+sffn_status sffn_attn_pages(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
+                            const int32_t *page_table, int table_width, int n_seq, const int32_t *seqs,
+                            const int32_t *positions, const int32_t *sel, const int32_t *n_sel, int n_keep,
+                            float scale, void *out, void *workspace, size_t ws_bytes, sffn_stream_t stream);
+
 /* Copy the workspace's device error word to *code (host) and clear it; waits
  * for `stream`.  0 = no error; otherwise an sffn_status value. */
 sffn_status sffn_read_device_error(void *workspace, int32_t *code, sffn_stream_t stream);
