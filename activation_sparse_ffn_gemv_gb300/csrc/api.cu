@@ -690,6 +690,9 @@ sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads
     a.scale = scale;
     a.out = out;
     a.err = static_cast<int32_t *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
+    a.home = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_home);
+    a.rows_max = p.rows_max;
     st = run_attn_shared(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
     return st;
@@ -798,6 +801,8 @@ sffn_status sffn_attn_pages(const void *q, int64_t q_stride, int T, int n_heads,
     a.scale = scale;
     a.out = out;
     a.err = static_cast<int32_t *>(workspace);
+    a.cuts = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + p.off_cuts);
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
     st = run_attn_pages(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
     return st;

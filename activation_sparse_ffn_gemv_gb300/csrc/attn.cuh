@@ -57,18 +57,15 @@ SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
     return q;
 }
 
-// pre[s] = length of the line before sequence s, pre[n_seq] = all of it (shared memory, every thread of
+// pre[i] = sum of length(0) .. length(i - 1), pre[n] = all of it (shared memory, every thread of
 // the CTA takes part; scratch: >= 33 long longs).
-SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch, bool record) {
+template <typename F>
+SFFN_DEV void line_prefix(int n, long long *pre, long long *scratch, F length) {
     const int nt = blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = nt >> 5;
     long long base = 0;
-    for (int s0 = 0; s0 < a.n_seq; s0 += nt) {
-        const int s = s0 + threadIdx.x;
-        long long v = 0;
-        if (s < a.n_seq) {
-            const TreeSeq q = tree_seq(a, s, record);
-            v = (long long)q.tiles * a.n_kv_heads * q.span();
-        }
+    for (int i0 = 0; i0 < n; i0 += nt) {
+        const int i = i0 + threadIdx.x;
+        const long long v = i < n ? length(i) : 0;
         long long incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -82,12 +79,20 @@ SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch,
             if (w < warp) before += scratch[w];
             all += scratch[w];
         }
-        if (s < a.n_seq) pre[s] = base + before + incl - v;
+        if (i < n) pre[i] = base + before + incl - v;
         base += all;
         __syncthreads();
     }
-    if (threadIdx.x == 0) pre[a.n_seq] = base;
+    if (threadIdx.x == 0) pre[n] = base;
     __syncthreads();
+}
+
+// Length of the line before each sequence, and all of it.
+SFFN_DEV void tree_prefix(const TreeArgs &a, long long *pre, long long *scratch, bool record) {
+    line_prefix(a.n_seq, pre, scratch, [&](int s) {
+        const TreeSeq q = tree_seq(a, s, record);
+        return (long long)q.tiles * a.n_kv_heads * q.span();
+    });
 }
 
 // Last sequence s with pre[s] <= u (u < pre[n_seq]): the one that place u of the line belongs to.
@@ -134,5 +139,55 @@ SFFN_DEV TreePiece tree_piece(const TreeArgs &a, const long long *pre, long long
 SFFN_HOST_DEV size_t tree_slot_floats(int rows_max, int D) {
     return (size_t)rows_max * D + (size_t)((2 * rows_max + 3) & ~3);
 }
+
+// A row of a cut item, put together by one warp from partial results: M = max of the pieces' maxima,
+// out = sum(exp(m_i - M) o_i) / sum(exp(m_i - M) l_i), the pieces in the order in which they are added.
+// A lane holds C = D / 32 consecutive columns.
+template <int C>
+struct JoinedRow {
+    float o[C], l, M;
+    SFFN_DEV JoinedRow() : l(0.f), M(-INFINITY) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = 0.f;
+    }
+    // Pieces 0 .. n - 1: sums_of(i) points to a piece's (maximum, sum), row_of(i) to its unnormalised row.
+    template <typename Sums, typename Row>
+    SFFN_DEV void add(int n_all, int lane, Sums sums_of, Row row_of) {
+        for (int b = 0; b < n_all; b += 32) {  // 32 pieces at a time
+            const int n = min(32, n_all - b);
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(sums_of(b + lane)));
+            const float Mn = fmaxf(M, warp_max(ml.x)), ref = Mn == -INFINITY ? 0.f : Mn;
+            // a piece without a key that this row sees has no weight
+            const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : expf(ml.x - ref), keep = expf(M - ref);
+            l = l * keep + warp_sum(f * ml.y);
+#pragma unroll
+            for (int i = 0; i < C; ++i) o[i] *= keep;
+            M = Mn;
+#pragma unroll 8
+            for (int k = 0; k < n; ++k) {
+                const float fk = __shfl_sync(0xffffffffu, f, k);
+                const float *p = row_of(b + k) + lane * C;
+                if constexpr (C == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+                    o[0] += fk * x.x, o[1] += fk * x.y, o[2] += fk * x.z, o[3] += fk * x.w;
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+                    o[0] += fk * x.x, o[1] += fk * x.y;
+                }
+            }
+        }
+    }
+    template <typename T>
+    SFFN_DEV void write(T *row, int lane) const {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        T *dst = row + lane * C;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if constexpr (sizeof(T) == 4) dst[i] = o[i] * inv;
+            else dst[i] = __float2bfloat16_rn(o[i] * inv);
+        }
+    }
+};
 
 }  // namespace sffn

@@ -46,7 +46,8 @@ constexpr float kLazyLog2 = 8.f;             // the running maximum moves when p
 // (a TMA box is 128 rows of one block).  true: by groups of 8 rows, each with its column blocks in
 // turn, so that any multiple of 8 rows with all its columns is one box (a page).
 // ONE: every item has one row tile (both pipelines read the same Q_0; the memory goes to the ring).
-template <int D, int STAGES, bool GROUPED, bool ONE>
+// TMA_OUT: whole row tiles leave by TMA.
+template <int D, int STAGES, bool GROUPED, bool ONE, bool TMA_OUT = !ONE>
 struct Cfg {
     static constexpr int kHalves = D / 64;                      // 64-element (128-byte) column blocks
     static constexpr int kBlock = 128 * 128;                    // bytes of a column block: 128 rows x 128 bytes
@@ -60,7 +61,8 @@ struct Cfg {
     // Row of a K or V tile that its i-th 16-byte chunk belongs to.
     SFFN_DEV static int row_of(int i) { return GROUPED ? (i / (64 * kHalves)) * 8 + ((i >> 3) & 7) : (i >> 3) & 127; }
     static constexpr int kColO = 256;                           // TMEM columns: S_0, S_1 (128 each), O_0, O_1
-    static constexpr int kOut = ONE ? 2048 : 4096;              // a softmax warp's: 64 (128) bytes of its 32 output rows
+    static constexpr bool kTmaOut = TMA_OUT;
+    static constexpr int kOut = TMA_OUT ? 4096 : 2048;          // a softmax warp's: 64 (128) bytes of its 32 output rows
     static constexpr int kSmem = (kQ + kStages) * kTile + (ONE ? 4 : 8) * kOut + 1024 /*alignment*/;
 };
 
@@ -81,6 +83,7 @@ struct Work {
     int seq, tok0;      // tree: sequence, first token of the item within its new tokens
     bool whole;         // tree: the item's every key (else a partial result)
     int slot;           // tree: partial result slot
+    int kind;           // shared prefixes: which part of its rows' keys the item has
 };
 
 // 2^x, good to about 2^-22 of it (a bf16 weight needs 2^-9); weights below 2^-126 are zero.
@@ -126,8 +129,9 @@ SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x008
 // Low 32 bits with the first n set (n clamped to 0 .. 32).
 SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// P: the policy (prompts or tree).  It gives
+// P: the policy (prompts, tree, shared prefixes, chosen pages).  It gives
 //   start                  before the first item (every warp calls it)
+//   kOneToken              an item has one token: the other rows of Q_0 are zeros
 //   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
 //   place, load_kv         where a key tile lies, looked up a tile ahead; the load of its K or V
@@ -203,8 +207,13 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         return __all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kHoldNs)) || wait_slow(bar, parity);
     };
 
+    if constexpr (P::kOneToken) {
+        for (int i = tid; i < C::kQ * C::kTile / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(sm_q)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     griddep_wait();
-    const int TB = 128 / G;
+    const int TB = P::kOneToken ? 1 : 128 / G;
     __shared__ Work s_work[kItems];
     policy.start();
     griddep_launch_dependents();
@@ -640,9 +649,9 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     tc::tmem_wait_st();
                 }
                 const int o_h = w.h * G, o_row = w.q_row + t * TB;
-                const bool full = !C::kOne && w.nt >= (t + 1) * TB;
+                const bool full = C::kTmaOut && w.nt >= (t + 1) * TB;
                 give_back();  // before the stores, which the release would wait for
-                if constexpr (!C::kOne) {
+                if constexpr (C::kTmaOut) {
                     // A whole row tile leaves by TMA, 64 columns at a time: the warps go on while it is
                     // written (their own stores took 4000 cycles an item, stalling the loads after them).
                     unsigned char *buf = sm_out + t * 4 * C::kOut;
@@ -728,7 +737,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             seen = !dealt && n > 0 && n >= tiles - 1;  // (an item without work for this group tells it nothing)
         }
     done:
-        if (!C::kOne && quad == 0 && lane == 0) tc::bulk_wait();
+        if (C::kTmaOut && quad == 0 && lane == 0) tc::bulk_wait();
     }
     tc::fence_before_sync();
     __syncthreads();

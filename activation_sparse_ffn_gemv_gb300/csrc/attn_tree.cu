@@ -95,6 +95,7 @@ using Cfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
 template <int D>
 struct TreePolicy {
     static constexpr bool kReread = false;
+    static constexpr bool kOneToken = false;
     const TreeArgs &a;
     long long *pre;         // length of the line before each sequence (shared memory)
     long long u, u1;        // this CTA's next place on the line, and the end of its range
@@ -221,9 +222,7 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
     atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, map_q, a.scale, a.group, a.err, smem_raw + kPrefixBytes);
 }
 
-// Joins the pieces of cut items: for each row, M = max of the pieces' maxima,
-// out = sum(exp(m_i - M) o_i) / sum(exp(m_i - M) l_i), the pieces in the order of
-// their CTAs.
+// Joins the pieces of cut items (JoinedRow), in the order of their CTAs.
 // There are `parts` blocks for each place between two CTAs' ranges; those of all the places that cut
 // an item share its rows, a warp a row at a time (an item cut often has many
 // pieces to read and as many more blocks).  What a block has to do depends on the call's inputs
@@ -237,41 +236,10 @@ template <typename T, int D>
 SFFN_DEV void join_row(const TreeArgs &a, long long row, int w0, int w1, int r, int lane) {
     const size_t sf = tree_slot_floats(a.rows_max, D);
     auto slot = [&](int w) { return a.part + sf * (size_t)(2 * w + (w == w0 ? 1 : 0)); };
-    constexpr int C = D / 32;  // columns of a lane
-    float o[C], l = 0.f, M = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-    for (int wb = w0; wb <= w1; wb += 32) {  // 32 pieces at a time
-        const int n = min(32, w1 - wb + 1);
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(slot(wb + lane) + (size_t)a.rows_max * D + 2 * r));
-        const float Mn = fmaxf(M, warp_max(ml.x)), ref = Mn == -INFINITY ? 0.f : Mn;
-        // a piece without a key that this row sees has no weight
-        const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : expf(ml.x - ref), keep = expf(M - ref);
-        l = l * keep + warp_sum(f * ml.y);
-#pragma unroll
-        for (int i = 0; i < C; ++i) o[i] *= keep;
-        M = Mn;
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const float *p = slot(wb + k) + (size_t)r * D + lane * C;
-            if constexpr (C == 4) {
-                const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
-                o[0] += fk * x.x, o[1] += fk * x.y, o[2] += fk * x.z, o[3] += fk * x.w;
-            } else {
-                const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
-                o[0] += fk * x.x, o[1] += fk * x.y;
-            }
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    T *dst = static_cast<T *>(a.out) + (size_t)row * D + lane * C;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        if constexpr (sizeof(T) == 4) dst[i] = o[i] * inv;
-        else dst[i] = __float2bfloat16_rn(o[i] * inv);
-    }
+    JoinedRow<D / 32> j;
+    j.add(w1 - w0 + 1, lane, [&](int i) { return slot(w0 + i) + (size_t)a.rows_max * D + 2 * r; },
+          [&](int i) { return slot(w0 + i) + (size_t)r * D; });
+    j.write(static_cast<T *>(a.out) + (size_t)row * D, lane);
 }
 
 template <typename T, int D>

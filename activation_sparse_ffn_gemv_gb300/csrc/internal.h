@@ -12,6 +12,7 @@
 namespace sffn {
 
 constexpr size_t kAlign = 256;
+constexpr size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }
 inline size_t align_up(size_t v, size_t a = kAlign) { return (v + a - 1) / a * a; }
 // Every workspace starts with a control block of kControlBytes:
 //   byte 0  int32  device error word (any entry point)
@@ -215,9 +216,11 @@ constexpr int kSharedMaxGroups = 256;  // groups of one sffn_attn_shared call
 struct SharedArgs : TreeArgs {
     const int32_t *group_seqs, *prefix_lens;
     int n_groups;
+    float *home;  // rows of whole items, of prefixes and of own positions
 };
 struct SharedPlan {
-    size_t total;
+    int grid, rows_max;
+    size_t off_part, off_home, total;
 };
 SharedPlan make_shared_plan(int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_shared(const SharedArgs &a, const SharedPlan &p, int dtype, int head_dim, cudaStream_t s);
@@ -265,10 +268,13 @@ struct PagesArgs {
     int n_keep;
     float scale;
     void *out;
+    int4 *cuts;   // for each CTA: token, key head, first and last CTA of the item that its range's beginning cuts
+    float *part;  // partial results of cut items
     int32_t *err;
 };
 struct PagesPlan {
-    size_t total;
+    int grid;
+    size_t off_cuts, off_part, total;
 };
 PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_pages(const PagesArgs &a, const PagesPlan &p, int dtype, int head_dim, cudaStream_t s);
