@@ -136,52 +136,143 @@ SFFN_DEV Token token_of(const Places &p, int t, int32_t *err) {
     return k;
 }
 
-constexpr int kScoreThreads = 128;
+// Scores are a matrix product: pages (bounds hi | lo, 2 D columns) times query rows (max(c, 0) | min(c, 0)), then the
+// maximum over a token's rows.  The codes are whole numbers of at most 127 and the bounds multiples of one
+// step, so bf16 holds both and the tensor cores' fp32 sums are exact.
+//
+// A CTA has a tile of tokens, one key head and a stretch of pages.  The tokens' rows (`rows` each: the
+// group's heads, some twice so that they fill columns evenly) lie in shared memory; a warp holds 16 pages' bounds in
+// registers as the 16 x 16 operand and runs all rows past them, 8 at a time.  The order of the columns is free
+// in such a sum: lane c of four takes columns 8 c .. 8 c + 7 of each 32, so operands are read 16 bytes at a
+// time, straight from the bounds.  (mma.sync: a decode step has 8 rows a token, where the bound is the
+// bounds' bytes and not the product.)
+// Consecutive tokens of one sequence (a run) read its bounds once.
+constexpr int kScoreWarps = 4;
+constexpr int kScorePages = 16 * kScoreWarps;  // pages of a CTA at a time
+constexpr int kScoreRows = 64;                 // rows of a CTA at most
 
-// A CTA: one token and key head, 128 pages, one a thread.
+SFFN_DEV void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// tile: tokens of a CTA (tile * rows <= kScoreRows, or one token); rows: of a token, 1, 2, 4 or a multiple of 8;
+// stretch: pages of a CTA.
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads) k_page_scores(const SelectPagesArgs a) {
-    __shared__ float c[64][D];  // the query heads' codes
-    __shared__ float s_most[kScoreThreads / 32];
+__global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPagesArgs a, int tile, int rows, int stretch) {
+    constexpr int kStride = 2 * D + 32;  // elements of a row (64 bytes apart mod 128: no bank conflicts)
+    constexpr int KB = 2 * D / 32;       // blocks of 32 columns
+    __shared__ __align__(16) __nv_bfloat16 s_code[kScoreRows][kStride];
+    __shared__ int s_seq[kScoreRows], s_last[kScoreRows];  // a token's sequence, and its last page with a score
     griddep_wait();
     griddep_launch_dependents();
-    const int t = blockIdx.x, h = blockIdx.z, p0 = blockIdx.y * kScoreThreads, tid = threadIdx.x;
-    const Token k = token_of(a.at, t, nullptr);
-    const int last = k.mine - a.n_recent;  // the last page that a score decides about
-    if (k.mine + 1 <= a.n_keep || p0 > last) return;
-    const T *q = static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)h * a.group * D;
-    float most = 0.f;
-    for (int i = tid; i < a.group * D; i += kScoreThreads) {
-        const float x = within((float)q[i], 0.f);
-        c[i / D][i % D] = x;
-        most = fmaxf(most, fabsf(x));
+    const int t0 = blockIdx.x * tile, nt = min(tile, a.T - t0), h = blockIdx.z, p0 = blockIdx.y * stretch;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid < tile) {
+        Token k{0, -1};
+        if (tid < nt) k = token_of(a.at, t0 + tid, nullptr);
+        s_seq[tid] = k.seq;
+        s_last[tid] = k.mine + 1 <= a.n_keep ? -1 : k.mine - a.n_recent;  // with fewer pages all are taken
     }
-    most = warp_max(most);
-    if ((tid & 31) == 0) s_most[tid >> 5] = most;
     __syncthreads();
-    for (int w = 0; w < kScoreThreads / 32; ++w) most = fmaxf(most, s_most[w]);
-    const float inv = pow2(-step_exponent(most));
-    for (int i = tid; i < a.group * D; i += kScoreThreads) c[i / D][i % D] = rintf(c[i / D][i % D] * inv);
-    __syncthreads();
-    const int page = p0 + tid;
-    if (page > last) return;
-    const int pg = a.at.page_table[(size_t)k.seq * a.at.table_width + page];
-    float score = 0.f;
-    if (pg < 0 || pg >= a.at.n_pages) {
-        record_error(a.err, SFFN_ERR_DEVICE);
-    } else {
-        score = -INFINITY;
-        const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bounds) + ((size_t)pg * a.n_kv_heads + h) * 2 * D;
-        for (int g = 0; g < a.group; ++g) {
-            float s = 0.f;
-            for (int d = 0; d < D; ++d) {
-                const float x = c[g][d];
-                s += x * bf16_to_f32(b[x > 0.f ? d : D + d]);
+    bool any = false;
+    for (int i = 0; i < nt; ++i) any |= s_last[i] >= p0;
+    if (!any) return;
+    // codes: a warp a token
+    for (int i = warp; i < nt; i += kScoreWarps) {
+        const T *q = static_cast<const T *>(a.q) + (size_t)(t0 + i) * a.q_stride + (size_t)h * a.group * D;
+        const int units = a.group * D / 8;  // of 8 elements
+        float most = 0.f;
+        for (int u = lane; u < units; u += 32) {
+            float x[8];
+            load8(q + u * 8, x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) most = fmaxf(most, fabsf(within(x[e], 0.f)));
+        }
+        const float inv = pow2(-step_exponent(warp_max(most)));
+        for (int u = lane; u < rows * D / 8; u += 32) {
+            const int r = u * 8 / D, d = u * 8 % D;
+            float x[8];
+            load8(q + (r % a.group) * D + d, x);
+            uint32_t up[4], dn[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x0 = rintf(within(x[2 * e], 0.f) * inv), x1 = rintf(within(x[2 * e + 1], 0.f) * inv);
+                __nv_bfloat162 pu = __floats2bfloat162_rn(fmaxf(x0, 0.f), fmaxf(x1, 0.f)),
+                               pd = __floats2bfloat162_rn(fminf(x0, 0.f), fminf(x1, 0.f));
+                up[e] = *reinterpret_cast<uint32_t *>(&pu);
+                dn[e] = *reinterpret_cast<uint32_t *>(&pd);
             }
-            score = fmaxf(score, s);
+            *reinterpret_cast<uint4 *>(&s_code[i * rows + r][d]) = make_uint4(up[0], up[1], up[2], up[3]);
+            *reinterpret_cast<uint4 *>(&s_code[i * rows + r][D + d]) = make_uint4(dn[0], dn[1], dn[2], dn[3]);
         }
     }
-    a.scores[((size_t)t * a.n_kv_heads + h) * a.at.table_width + page] = score;
+    __syncthreads();
+    const int g = lane >> 2, c = lane & 3;  // row of the operands, and which columns
+    const int reduce = rows >= 8 ? 4 : rows / 2;  // lanes that hold a token's columns (0: each its own two)
+    for (int r0 = 0, r1; r0 < nt; r0 = r1) {  // runs
+        int last = s_last[r0];
+        for (r1 = r0 + 1; r1 < nt && s_seq[r1] == s_seq[r0]; ++r1) last = max(last, s_last[r1]);
+        const int end = min(p0 + stretch, last + 1);
+        for (int pb = p0 + warp * 16; pb < end; pb += kScorePages) {
+            uint4 x[KB], y[KB];  // the bounds of pages pb + g and pb + g + 8
+            const int32_t *table = a.at.page_table + (size_t)s_seq[r0] * a.at.table_width + pb + g;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int pg = pb + g + 8 * half < end ? table[8 * half] : -1;
+                const bool there = pg >= 0 && pg < a.at.n_pages;
+                if (!there && c == 0 && pb + g + 8 * half < end) record_error(a.err, SFFN_ERR_DEVICE);
+                const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bounds) +
+                                         ((size_t)(there ? pg : 0) * a.n_kv_heads + h) * 2 * D + c * 8;
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (there) v = ldg_v4(b + k * 32);
+                    (half ? y : x)[k] = v;
+                }
+            }
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            for (int n = r0 * rows / 8; n * 8 < r1 * rows; ++n) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                const __nv_bfloat16 *code = &s_code[n * 8 + g][c * 8];
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    const uint4 z = *reinterpret_cast<const uint4 *>(code + k * 32);
+                    mma_16x8x16(d, x[k].x, y[k].x, x[k].y, y[k].y, z.x, z.y);
+                    mma_16x8x16(d, x[k].z, y[k].z, x[k].w, y[k].w, z.z, z.w);
+                }
+                // d[0], d[1]: page g, rows 2 c and 2 c + 1; d[2], d[3]: page g + 8
+                if (rows > 8) {  // several products a token
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], d[e]);
+                    if ((n + 1) * 8 % rows) continue;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d[e] = m[e], m[e] = -INFINITY;
+                }
+                auto put = [&](int i, int half, float v) {  // token i of the tile
+                    const int page = pb + g + 8 * half;
+                    if (i >= r0 && i < r1 && page <= s_last[i] && page < end)
+                        a.scores[((size_t)(t0 + i) * a.n_kv_heads + h) * a.at.table_width + page] = v;
+                };
+                if (rows == 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) put(n * 8 + 2 * c + (e & 1), e >> 1, d[e]);
+                    continue;
+                }
+                float u = fmaxf(d[0], d[1]), v = fmaxf(d[2], d[3]);
+                for (int o = 1; o < reduce; o <<= 1) {
+                    u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                }
+                const int i = (n * 8 + 2 * c) / rows;
+                if (c % reduce == 0) {
+                    put(i, 0, u);
+                    put(i, 1, v);
+                }
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -217,7 +308,7 @@ __global__ void __launch_bounds__(NT) k_page_choose(const SelectPagesArgs a) {
         key[r] = 0;
         if (page >= c0 && page < c1) {
             const uint32_t b = __float_as_uint(__ldcg(score + page) + 0.f);  // (-0 is 0)
-            key[r] = b & 0x80000000u ? ~b : b | 0x80000000u;
+            key[r] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);
         }
     }
     if (tid < 32) s_count[tid] = 0;
@@ -275,15 +366,26 @@ cudaError_t launch_bounds_k(const BoundsArgs &a, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_select(const SelectPagesArgs &a, cudaStream_t s) {
-    const int width = a.at.table_width;
+    const int width = a.at.table_width, G = a.group;
+    int rows = G > 4 ? (G + 7) / 8 * 8 : (G > 2 ? 4 : G);
+    int tile = 1;  // as many tokens as a sequence has in the mean, as far as their rows go
+    while (2 * tile * rows <= kScoreRows && 2 * tile * a.at.n_seq <= a.T) tile *= 2;
+    if (tile == 1 && rows < 8) rows = 8;  // (a token alone: whole products)
+    const long long tiles = ((long long)a.T + tile - 1) / tile * a.n_kv_heads, fill = 4LL * device_sm_count();
+    // stretches of pages that give every SM four CTAs, then longer ones: the codes are made once for each
+    long long cut = (fill + tiles - 1) / tiles;
+    const int most = (width + kScorePages - 1) / kScorePages;
+    if (cut > most) cut = most;
+    const int stretch = (most + (int)cut - 1) / (int)cut * kScorePages;
     cudaError_t e = launch_k(k_page_scores<T, D>,
-                             dim3((unsigned)a.T, (unsigned)((width + kScoreThreads - 1) / kScoreThreads), (unsigned)a.n_kv_heads),
-                             dim3(kScoreThreads), 0, s, a);
+                             dim3((unsigned)((a.T + tile - 1) / tile), (unsigned)((width + stretch - 1) / stretch),
+                                  (unsigned)a.n_kv_heads),
+                             dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch);
     if (e != cudaSuccess) return e;
-    const dim3 rows((unsigned)a.T * (unsigned)a.n_kv_heads);
-    if (width <= 256 * 4) return launch_k(k_page_choose<256, 4>, rows, dim3(256), 0, s, a);
-    if (width <= 256 * 16) return launch_k(k_page_choose<256, 16>, rows, dim3(256), 0, s, a);
-    return launch_k(k_page_choose<1024, 32>, rows, dim3(1024), 0, s, a);
+    const dim3 lists((unsigned)a.T * (unsigned)a.n_kv_heads);
+    if (width <= 256 * 4) return launch_k(k_page_choose<256, 4>, lists, dim3(256), 0, s, a);
+    if (width <= 256 * 16) return launch_k(k_page_choose<256, 16>, lists, dim3(256), 0, s, a);
+    return launch_k(k_page_choose<1024, 32>, lists, dim3(1024), 0, s, a);
 }
 
 }  // namespace
