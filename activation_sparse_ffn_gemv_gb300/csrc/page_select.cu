@@ -158,8 +158,8 @@ SFFN_DEV void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, 
 }
 
 // tile: tokens of a CTA (tile * rows <= kScoreRows, or one token); rows: of a token, 1, 2, 4 or a multiple of 8;
-// stretch: pages of a CTA.
-template <typename T, int D>
+// stretch: pages of a CTA; NB: products of 8 rows at a time (several chains of sums for the tensor cores to work on).
+template <typename T, int D, int NB>
 __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPagesArgs a, int tile, int rows, int stretch) {
     constexpr int kStride = 2 * D + 32;  // elements of a row (64 bytes apart mod 128: no bank conflicts)
     constexpr int KB = 2 * D / 32;       // blocks of 32 columns
@@ -179,6 +179,17 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
     bool any = false;
     for (int i = 0; i < nt; ++i) any |= s_last[i] >= p0;
     if (!any) return;
+    if (NB == 1) {  // a token alone: the first pages' bounds come to L2 while its codes are made
+        const int page = p0 + warp * 16 + (lane & 15);
+        if (page <= s_last[0] && page < p0 + stretch) {
+            const int pg = a.at.page_table[(size_t)s_seq[0] * a.at.table_width + page];
+            if (pg >= 0 && pg < a.at.n_pages) {
+                const char *b = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.bounds) +
+                                                               ((size_t)pg * a.n_kv_heads + h) * 2 * D);
+                for (int i = (lane >> 4) * 128; i < 4 * D; i += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
+            }
+        }
+    }
     // codes: a warp a token
     for (int i = warp; i < nt; i += kScoreWarps) {
         const T *q = static_cast<const T *>(a.q) + (size_t)(t0 + i) * a.q_stride + (size_t)h * a.group * D;
@@ -232,43 +243,56 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
                     (half ? y : x)[k] = v;
                 }
             }
+            auto put = [&](int i, int half, float v) {  // token i of the tile
+                const int page = pb + g + 8 * half;
+                if (i >= r0 && i < r1 && page <= s_last[i] && page < end)
+                    a.scores[((size_t)(t0 + i) * a.n_kv_heads + h) * a.at.table_width + page] = v;
+            };
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            for (int n = r0 * rows / 8; n * 8 < r1 * rows; ++n) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                const __nv_bfloat16 *code = &s_code[n * 8 + g][c * 8];
+            const int n0 = r0 * rows / 8, n1 = (r1 * rows + 7) / 8;
+            for (int nb = n0; nb < n1; nb += NB) {
+                float d[NB][4];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KB; ++k) {
-                    const uint4 z = *reinterpret_cast<const uint4 *>(code + k * 32);
-                    mma_16x8x16(d, x[k].x, y[k].x, x[k].y, y[k].y, z.x, z.y);
-                    mma_16x8x16(d, x[k].z, y[k].z, x[k].w, y[k].w, z.z, z.w);
-                }
-                // d[0], d[1]: page g, rows 2 c and 2 c + 1; d[2], d[3]: page g + 8
-                if (rows > 8) {  // several products a token
+                    uint4 z[NB];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], d[e]);
-                    if ((n + 1) * 8 % rows) continue;
+                    for (int j = 0; j < NB; ++j)
+                        z[j] = *reinterpret_cast<const uint4 *>(&s_code[min(nb + j, n1 - 1) * 8 + g][c * 8 + k * 32]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) d[e] = m[e], m[e] = -INFINITY;
-                }
-                auto put = [&](int i, int half, float v) {  // token i of the tile
-                    const int page = pb + g + 8 * half;
-                    if (i >= r0 && i < r1 && page <= s_last[i] && page < end)
-                        a.scores[((size_t)(t0 + i) * a.n_kv_heads + h) * a.at.table_width + page] = v;
-                };
-                if (rows == 1) {
+                    for (int j = 0; j < NB; ++j) mma_16x8x16(d[j], x[k].x, y[k].x, x[k].y, y[k].y, z[j].x, z[j].y);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) put(n * 8 + 2 * c + (e & 1), e >> 1, d[e]);
-                    continue;
+                    for (int j = 0; j < NB; ++j) mma_16x8x16(d[j], x[k].z, y[k].z, x[k].w, y[k].w, z[j].z, z[j].w);
                 }
-                float u = fmaxf(d[0], d[1]), v = fmaxf(d[2], d[3]);
-                for (int o = 1; o < reduce; o <<= 1) {
-                    u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                }
-                const int i = (n * 8 + 2 * c) / rows;
-                if (c % reduce == 0) {
-                    put(i, 0, u);
-                    put(i, 1, v);
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int n = nb + j;
+                    if (n >= n1) break;
+                    float (&f)[4] = d[j];
+                    // f[0], f[1]: page g, rows 2 c and 2 c + 1; f[2], f[3]: page g + 8
+                    if (rows > 8) {  // several products a token
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], f[e]);
+                        if ((n + 1) * 8 % rows) continue;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[e] = m[e], m[e] = -INFINITY;
+                    }
+                    if (rows == 1) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) put(n * 8 + 2 * c + (e & 1), e >> 1, f[e]);
+                        continue;
+                    }
+                    float u = fmaxf(f[0], f[1]), v = fmaxf(f[2], f[3]);
+                    for (int o = 1; o < reduce; o <<= 1) {
+                        u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                    }
+                    const int i = (n * 8 + 2 * c) / rows;
+                    if (c % reduce == 0) {
+                        put(i, 0, u);
+                        put(i, 1, v);
+                    }
                 }
             }
         }
@@ -276,22 +300,32 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
 }
 
 // ---------------------------------------------------------------------------
-// Choice: one CTA a token and key head, its scores in registers.  The cut (the `need`-th largest key)
-// is found bit by bit: the largest value that at least `need` keys reach.  Each warp holds
-// consecutive pages, 32 at a time, so ballots give the ascending order.
+// Choice: NW warps a token and key head, the scores in registers.  The cut (the `need`-th largest key) is found bit
+// by bit from the highest that differs: the largest value that at least `need` keys reach; when exactly
+// `need` do, that is the choice.  Each warp holds consecutive pages, 32 at a time, so ballots give the ascending
+// order.
 // ---------------------------------------------------------------------------
 
-template <int NT, int R>
-__global__ void __launch_bounds__(NT) k_page_choose(const SelectPagesArgs a) {
-    constexpr int NW = NT / 32;
+// Rows of a CTA.
+template <int NW>
+struct ChooseRows {
+    static constexpr int value = NW == 1 ? 4 : 1;
+};
+
+template <int NW, int R>
+__global__ void __launch_bounds__(32 * NW * ChooseRows<NW>::value) k_page_choose(const SelectPagesArgs a) {
+    constexpr int NT = 32 * NW;
     __shared__ int s_count[32], s_above[NW], s_equal[NW];
+    __shared__ uint32_t s_most[NW], s_least[NW];
     griddep_wait();
     griddep_launch_dependents();
-    const int t = blockIdx.x / a.n_kv_heads, h = blockIdx.x - t * a.n_kv_heads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned row = NW == 1 ? blockIdx.x * ChooseRows<NW>::value + (threadIdx.x >> 5) : blockIdx.x;
+    if (row >= (unsigned)a.T * (unsigned)a.n_kv_heads) return;
+    const int t = (int)(row / (unsigned)a.n_kv_heads), h = (int)(row - (unsigned)t * (unsigned)a.n_kv_heads);
+    const int tid = NW == 1 ? threadIdx.x & 31 : threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Token k = token_of(a.at, t, h == 0 && tid == 0 ? a.err : nullptr);
     const int n = min(k.mine + 1, a.n_keep);
-    int32_t *sel = a.sel + (size_t)blockIdx.x * a.n_keep;
+    int32_t *sel = a.sel + (size_t)row * a.n_keep;
     if (h == 0 && tid == 0) a.n_sel[t] = n;
     for (int i = n + tid; i < a.n_keep; i += NT) sel[i] = -1;
     if (k.mine + 1 <= a.n_keep) {
@@ -299,9 +333,12 @@ __global__ void __launch_bounds__(NT) k_page_choose(const SelectPagesArgs a) {
         return;
     }
     const int need = a.n_keep - a.n_first - a.n_recent;
-    const int c0 = a.n_first, c1 = k.mine - a.n_recent + 1;  // candidates [c0, c1)
-    const float *score = a.scores + (size_t)blockIdx.x * a.at.table_width;
-    uint32_t key[R];  // in the order of the scores; 0: not a candidate
+    const int c0 = a.n_first, c1 = k.mine - a.n_recent + 1;  // candidates [c0, c1), more than `need`
+    for (int i = tid; i < a.n_first; i += NT) sel[i] = i;
+    for (int i = tid; i < a.n_recent; i += NT) sel[a.n_keep - a.n_recent + i] = c1 + i;
+    if (need == 0) return;
+    const float *score = a.scores + (size_t)row * a.at.table_width;
+    uint32_t key[R], most = 1, least = 0xffffffffu;  // in the order of the scores; 0: not a candidate
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int page = (warp * R + r) * 32 + lane;
@@ -309,47 +346,64 @@ __global__ void __launch_bounds__(NT) k_page_choose(const SelectPagesArgs a) {
         if (page >= c0 && page < c1) {
             const uint32_t b = __float_as_uint(__ldcg(score + page) + 0.f);  // (-0 is 0)
             key[r] = max(1u, b & 0x80000000u ? ~b : b | 0x80000000u);
+            most = max(most, key[r]);
+            least = min(least, key[r]);
         }
     }
-    if (tid < 32) s_count[tid] = 0;
-    __syncthreads();
-    uint32_t cut = 0;
-    if (need > 0) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t v = cut | (1u << bit);
-            int m = 0;
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if constexpr (NW > 1) {
+        if (tid < 32) s_count[tid] = 0;
+        if (lane == 0) s_most[warp] = most, s_least[warp] = least;
+        __syncthreads();
+        for (int w = 0; w < NW; ++w) most = max(most, s_most[w]), least = min(least, s_least[w]);
+    }
+    // every candidate has the bits of `least` above the highest that differs
+    int bit = most == least ? -1 : 31 - __clz(most ^ least);
+    uint32_t cut = bit < 0 ? least : least & ~((2u << bit) - 1u);
+    bool exact = false;  // those that reach `cut` are the choice
+    for (; bit >= 0 && !exact; --bit) {
+        const uint32_t v = cut | (1u << bit);
+        int m = 0;
 #pragma unroll
-            for (int r = 0; r < R; ++r) m += key[r] >= v;
-            m = __reduce_add_sync(0xffffffffu, m);
+        for (int r = 0; r < R; ++r) m += key[r] >= v;
+        m = __reduce_add_sync(0xffffffffu, m);
+        if constexpr (NW > 1) {
             if (lane == 0 && m) atomicAdd(&s_count[bit], m);
             __syncthreads();
-            if (s_count[bit] >= need) cut = v;
+            m = s_count[bit];
         }
-    } else {
-        cut = 0xffffffffu;  // above every key
+        if (m >= need) cut = v;
+        exact = m == need;
     }
-    int above = 0, equal = 0;
+    if (exact) --cut;  // nothing at the cut is taken: all above it is
+    int before = 0, ties = 0, spare = 0;  // above the cut and at it in the warps before this one; of the latter, how many are taken
+    if constexpr (NW > 1) {
+        int above = 0, equal = 0, all = 0;
 #pragma unroll
-    for (int r = 0; r < R; ++r) above += key[r] > cut, equal += key[r] == cut;
-    above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
-    if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
-    __syncthreads();
-    int before = 0, ties = 0, all = 0;  // above the cut and at it, in the warps before this one; above in all
-    for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += s_above[w], ties += s_equal[w];
-        all += s_above[w];
+        for (int r = 0; r < R; ++r) above += key[r] > cut, equal += key[r] == cut;
+        above = __reduce_add_sync(0xffffffffu, above);
+        equal = __reduce_add_sync(0xffffffffu, equal);
+        if (lane == 0) s_above[warp] = above, s_equal[warp] = equal;
+        __syncthreads();
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += s_above[w], ties += s_equal[w];
+            all += s_above[w];
+        }
+        spare = need - all;
+    } else if (!exact) {
+        int above = 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) above += key[r] > cut;
+        spare = need - __reduce_add_sync(0xffffffffu, above);
     }
-    const int spare = need - all;  // of those at the cut, the first `spare` are taken
-    for (int i = tid; i < a.n_first; i += NT) sel[i] = i;
-    for (int i = tid; i < a.n_recent; i += NT) sel[a.n_keep - a.n_recent + i] = c1 + i;
     int at = a.n_first + before + min(ties, spare);
+    const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const uint32_t up = __ballot_sync(0xffffffffu, key[r] > cut), eq = __ballot_sync(0xffffffffu, key[r] == cut);
-        const uint32_t below = (1u << lane) - 1u;
-        const int my_tie = ties + __popc(eq & below);
-        const bool tie = key[r] == cut && my_tie < spare;
+        // the first of those at the cut
+        const bool tie = key[r] == cut && ties + __popc(eq & below) < spare;
         const uint32_t take = up | __ballot_sync(0xffffffffu, tie);
         if ((take >> lane) & 1u) sel[at + __popc(take & below)] = (warp * R + r) * 32 + lane;
         at += __popc(take);
@@ -371,21 +425,26 @@ cudaError_t launch_select(const SelectPagesArgs &a, cudaStream_t s) {
     int tile = 1;  // as many tokens as a sequence has in the mean, as far as their rows go
     while (2 * tile * rows <= kScoreRows && 2 * tile * a.at.n_seq <= a.T) tile *= 2;
     if (tile == 1 && rows < 8) rows = 8;  // (a token alone: whole products)
-    const long long tiles = ((long long)a.T + tile - 1) / tile * a.n_kv_heads, fill = 4LL * device_sm_count();
-    // stretches of pages that give every SM four CTAs, then longer ones: the codes are made once for each
+    // Stretches of pages so that every SM has several CTAs: many where a token is alone (its sequence may be short, and
+    // most of them empty), fewer where the codes of many tokens are made for each.
+    const long long tiles = ((long long)a.T + tile - 1) / tile * a.n_kv_heads, fill = (tile == 1 ? 24LL : 4LL) * device_sm_count();
     long long cut = (fill + tiles - 1) / tiles;
     const int most = (width + kScorePages - 1) / kScorePages;
     if (cut > most) cut = most;
     const int stretch = (most + (int)cut - 1) / (int)cut * kScorePages;
-    cudaError_t e = launch_k(k_page_scores<T, D>,
-                             dim3((unsigned)((a.T + tile - 1) / tile), (unsigned)((width + stretch - 1) / stretch),
-                                  (unsigned)a.n_kv_heads),
-                             dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch);
+    const dim3 grid((unsigned)((a.T + tile - 1) / tile), (unsigned)((width + stretch - 1) / stretch), (unsigned)a.n_kv_heads);
+    cudaError_t e = tile * rows <= 8
+                        ? launch_k(k_page_scores<T, D, 1>, grid, dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch)
+                        : launch_k(k_page_scores<T, D, 4>, grid, dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch);
     if (e != cudaSuccess) return e;
-    const dim3 lists((unsigned)a.T * (unsigned)a.n_kv_heads);
-    if (width <= 256 * 4) return launch_k(k_page_choose<256, 4>, lists, dim3(256), 0, s, a);
-    if (width <= 256 * 16) return launch_k(k_page_choose<256, 16>, lists, dim3(256), 0, s, a);
-    return launch_k(k_page_choose<1024, 32>, lists, dim3(1024), 0, s, a);
+    const unsigned lists = (unsigned)a.T * (unsigned)a.n_kv_heads;
+    if (width <= 1024) {  // a warp a list where there are enough of them
+        if (lists >= 16u * (unsigned)device_sm_count())
+            return launch_k(k_page_choose<1, 32>, dim3((lists + 3) / 4), dim3(128), 0, s, a);
+        return launch_k(k_page_choose<8, 4>, dim3(lists), dim3(256), 0, s, a);
+    }
+    if (width <= 4096) return launch_k(k_page_choose<16, 8>, dim3(lists), dim3(512), 0, s, a);
+    return launch_k(k_page_choose<32, 32>, dim3(lists), dim3(1024), 0, s, a);
 }
 
 }  // namespace
