@@ -692,6 +692,7 @@ sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads
     a.err = static_cast<int32_t *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
     a.home = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_home);
+    a.entries = static_cast<char *>(workspace) + p.off_entries;
     a.rows_max = p.rows_max;
     st = run_attn_shared(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());

@@ -1,16 +1,20 @@
 // attn_pages.cu -- attention of each token over its chosen pages of the paged cache (sm_103a).
 //
-// An item is a (token, key head): G rows against the n_sel chosen pages, taken one after the other as
-// if they were consecutive positions.  The work of all items is one line as in attn.cuh (units of 64
-// positions and kTreeItemCost more per item), token by token and head by head, cut evenly over the
+// An item is a (token, key head, row tile): up to 32 of the G rows against the n_sel chosen pages, taken one after the
+// other as if they were consecutive positions.  The work of all items is one line as in attn.cuh (units of 64
+// positions and kItemCost more per item), token by token and head by head, cut evenly over the
 // CTAs; items that lie in one CTA's range are finished there, the pieces of a cut item are joined by
 // k_pages_join.
 #include "attn_rows.cuh"
-#include "attn_tc.cuh"
+#include "attn_few.cuh"
 
 namespace sffn {
 
 namespace {
+
+// Units that an item costs by itself (48 tokens of up to 2048 positions, 8 key heads: 58.1 us with 2, 54.0 with 4, 54.5
+// with 6).
+constexpr int kItemCost = 4;
 
 // Pages of token t, 0 if it reads none; -1: its row is left as it is (padding, or it breaks the contract).
 SFFN_DEV int pages_of(const PagesArgs &a, int t, bool record) {
@@ -24,11 +28,12 @@ SFFN_DEV int pages_of(const PagesArgs &a, int t, bool record) {
 }
 
 SFFN_DEV int pages_units(const PagesArgs &a, int n) { return (int)((((long long)n << a.at.page_shift) + kTreeUnit - 1) / kTreeUnit); }
-SFFN_DEV int pages_span(const PagesArgs &a, int n) { return n > 0 ? pages_units(a, n) + kTreeItemCost : 0; }
+SFFN_DEV int pages_span(const PagesArgs &a, int n) { return n > 0 ? pages_units(a, n) + kItemCost : 0; }
 
 // A piece of an item.
 struct PagesPiece {
     int t, h, n;   // token, key head, its pages
+    int tile;      // row tile
     int un0, un1;  // units
     bool whole;
 };
@@ -59,7 +64,7 @@ struct PagesWalk {
                 for (int e = 0; e < a.n_heads * D * (int)sizeof(T) / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
             }
         }
-        sum *= a.n_kv_heads;
+        sum *= a.n_kv_heads * a.tiles;
         long long incl = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -79,7 +84,7 @@ struct PagesWalk {
         if (b < W && before <= u && u < before + sum) {  // the token is one of this thread's
             int i = t0;
             for (;; ++i) {
-                const long long len = (long long)pages_span(a, pages_of(a, i, false)) * a.n_kv_heads;
+                const long long len = (long long)pages_span(a, pages_of(a, i, false)) * a.n_kv_heads * a.tiles;
                 if (u < before + len) break;
                 before += len;
             }
@@ -91,12 +96,12 @@ struct PagesWalk {
         at = s_at;
         n = b < W ? pages_of(a, t, false) : 0;
         if (tid == 0) {
-            int4 cut = make_int4(-1, 0, 0, 0);  // token, head, first and last CTA of the cut item
+            int4 cut = make_int4(-1, 0, 0, 0);  // token, its item, first and last CTA of the cut item
             if (b > 0 && b < W) {
-                const int span = pages_span(a, n), h = (int)((u - at) / span);
-                const long long i0 = at + (long long)h * span;
-                const int w0 = tree_owner(total, i0 + kTreeItemCost, W), w1 = tree_owner(total, i0 + span - 1, W);
-                if (w0 < b && b <= w1) cut = make_int4(t, h, w0, w1);
+                const int span = pages_span(a, n), item = (int)((u - at) / span);
+                const long long i0 = at + (long long)item * span;
+                const int w0 = tree_owner(total, i0 + kItemCost, W), w1 = tree_owner(total, i0 + span - 1, W);
+                if (w0 < b && b <= w1) cut = make_int4(t, item, w0, w1);
             }
             a.cuts[b] = cut;
         }
@@ -107,17 +112,17 @@ struct PagesWalk {
         for (;;) {
             if (u >= u1) return false;
             int span = pages_span(a, n);
-            while (u >= at + (long long)span * a.n_kv_heads) {  // on to the token that place u belongs to
-                at += (long long)span * a.n_kv_heads;
+            while (u >= at + (long long)span * a.n_kv_heads * a.tiles) {  // on to the token that place u belongs to
+                at += (long long)span * a.n_kv_heads * a.tiles;
                 n = pages_of(a, ++t, false);
                 span = pages_span(a, n);
             }
             const long long local = u - at;
-            const int h = (int)(local / span), off = (int)(local - (long long)h * span);
+            const int item = (int)(local / span), off = (int)(local - (long long)item * span);
             const int end = (int)min((long long)span, off + (u1 - u));
             u += end - off;
-            p.t = t, p.h = h, p.n = n;
-            p.un0 = max(0, off - kTreeItemCost), p.un1 = max(0, end - kTreeItemCost);
+            p.t = t, p.h = item / a.tiles, p.tile = item % a.tiles, p.n = n;
+            p.un0 = max(0, off - kItemCost), p.un1 = max(0, end - kItemCost);
             p.whole = p.un0 == 0 && end == span;
             if (p.un0 < p.un1) return true;
         }
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_pages_rows(const PagesArg
             for (int i = 0; i < rows::Acc<D>::RPT; ++i) acc.o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             __syncthreads();
         }
-        float *slot = a.part + tree_slot_floats(G, D) * (size_t)(2 * blockIdx.x + (p.un0 > 0 ? 0 : 1));
+        float *slot = a.part + tree_slot_floats(a.row_tile, D) * (size_t)(2 * blockIdx.x + (p.un0 > 0 ? 0 : 1));
         const int c = (tid % rows::Acc<D>::CT) * 4, g = (tid / rows::Acc<D>::CT) * rows::Acc<D>::RPT;
 #pragma unroll
         for (int i = 0; i < rows::Acc<D>::RPT; ++i) {
@@ -193,104 +198,65 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_pages_rows(const PagesArg
                 *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
             } else {
                 *reinterpret_cast<float4 *>(slot + (size_t)r * D + c) = o;
-                if (c == 0) *reinterpret_cast<float2 *>(slot + (size_t)G * D + 2 * r) = make_float2(sm.m[r], sm.l[r]);
+                if (c == 0) *reinterpret_cast<float2 *>(slot + (size_t)a.row_tile * D + 2 * r) = make_float2(sm.m[r], sm.l[r]);
             }
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// bf16: attn_tc.cuh over the paged cache
+// bf16: attn_few.cuh over the paged cache
 // ---------------------------------------------------------------------------
 
 template <int D>
-using Cfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
-
-template <int D>
 struct PagesPolicy {
-    static constexpr bool kReread = false;
-    static constexpr bool kOneToken = true;
     const PagesArgs &a;
     PagesWalk walk;
-    int G, box;  // box: cache rows of one copy (a page's, 64 at most)
 
-    struct RowInfo {};
+    SFFN_DEV explicit PagesPolicy(const PagesArgs &args) : a(args), walk(args) {}
 
-    SFFN_DEV explicit PagesPolicy(const PagesArgs &args) : a(args), walk(args), G(args.group), box(min(64, 1 << args.at.page_shift)) {}
-
-    SFFN_DEV void start() { walk.template start<__nv_bfloat16, D>(); }
-    SFFN_DEV bool next(atc::Work &w) {
+    SFFN_DEV bool next(few::Work &w) {
         PagesPiece p;
         if (!walk.next(p)) return false;
-        // (a piece behind the last position that the token sees has one key tile without keys)
-        const int k0 = p.un0 * kTreeUnit, k1 = max(k0, min(seen(a, p.t, p.h, p.n), p.un1 * kTreeUnit));
-        const int n = max(1, (k1 - k0 + atc::kKeys - 1) / atc::kKeys);
-        w.h = p.h;
         w.q_row = p.t;
         w.nt = 1;
-        w.k0 = k0;
-        w.k1 = w.exist = k1;
-        w.tiles = n;
-        w.n[0] = (n + 1) / 2;
-        w.n[1] = n / 2;
-        w.mask_from[0] = w.mask_from[1] = (k1 - k0) / atc::kKeys;
+        w.h = p.h;
+        w.r0 = p.tile * a.row_tile;
+        w.rows = min(a.row_tile, a.group - w.r0);
+        w.k0 = p.un0 * kTreeUnit;
+        w.k1 = w.all = max(w.k0, min(seen(a, p.t, p.h, p.n), p.un1 * kTreeUnit));  // (none behind the last that it sees)
         w.whole = p.whole;
         w.slot = 2 * blockIdx.x + (p.un0 > 0 ? 0 : 1);
         return true;
     }
-    // Row of the cache (head h's) that holds place `j` of the token's pages, on page pg; past the end if that is not one.
-    SFFN_DEV long long cache_row(const atc::Work &w, int j, int pg) const {
-        return (((long long)(pg < 0 ? a.at.n_pages : pg) * a.n_kv_heads + (pg < 0 ? 0 : w.h)) << a.at.page_shift) +
-               (pg < 0 ? 0 : j & ((1 << a.at.page_shift) - 1));
-    }
-    // Page of this lane's part of key tile j, a box of `box` rows (16 boxes at most); looked up a
-    // tile ahead of its use.
-    SFFN_DEV int place(const atc::Work &w, int j, int lane) const {
-        const int off = j * atc::kKeys + lane * box;
-        return lane * box < atc::kKeys && off < w.k1 - w.k0 ? cache_page(a, w.q_row, w.h, w.k0 + off) : 0;
-    }
-    SFFN_DEV void load_kv(const atc::Work &w, int j, int pg, const CUtensorMap *map, unsigned char *dst, uint64_t *bar,
-                          int lane, uint64_t pol) const {
-        constexpr int H = Cfg<D>::kHalves;
-        const int kb = w.k0 + j * atc::kKeys, left = min(atc::kKeys, w.k1 - kb), boxes = (left + box - 1) / box;
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * H));
-        __syncwarp();
-        if (lane < boxes) {
-            const int row = (int)cache_row(w, kb + lane * box, pg);
-            tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, row >> 3, bar, pol);
-        }
-    }
-    SFFN_DEV RowInfo row_info(const atc::Work &, int) const { return RowInfo{}; }
-    SFFN_DEV void visible(const atc::Work &w, const RowInfo &, int j, uint32_t (&vis)[4]) const {
-        const int n = w.k1 - w.k0 - j * atc::kKeys;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vis[i] = atc::low_bits(n - 32 * i);
-    }
-    SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &, int j) const {
+    SFFN_DEV int page_of(const few::Work &w, int j) const {
         const int pg = cache_page(a, w.q_row, w.h, j);
-        if (pg < 0) return nullptr;
-        return static_cast<const uint16_t *>(a.cv) + (size_t)cache_row(w, j, pg) * D;
+        return pg < 0 ? a.at.n_pages : pg;
     }
-    SFFN_DEV bool partial(const atc::Work &w) const { return !w.whole; }
-    SFFN_DEV unsigned char *begin_row(const atc::Work &w, int, int head, bool valid, float m, float l, float &inv) const {
-        inv = l == 0.f ? 0.f : 1.f / l;
-        if (!valid) return nullptr;
-        if (w.whole)
-            return reinterpret_cast<unsigned char *>(static_cast<uint16_t *>(a.out) +
-                                                     ((size_t)w.q_row * a.n_heads + (size_t)w.h * G + head) * D);
-        float *slot = a.part + tree_slot_floats(G, D) * (size_t)w.slot;
-        *reinterpret_cast<float2 *>(slot + (size_t)G * D + 2 * head) = make_float2(m * a.scale, l);
-        return reinterpret_cast<unsigned char *>(slot + (size_t)head * D);
+    SFFN_DEV const __nv_bfloat16 *query(const few::Work &w, int row) const {
+        return static_cast<const __nv_bfloat16 *>(a.q) + (size_t)w.q_row * a.q_stride + (size_t)(w.h * a.group + row) * D;
+    }
+    SFFN_DEV bool sees(const few::Work &, int, int) const { return false; }
+    SFFN_DEV __nv_bfloat16 *out_row(const few::Work &w, int row) const {
+        return static_cast<__nv_bfloat16 *>(a.out) + ((size_t)w.q_row * a.n_heads + (size_t)w.h * a.group + row) * D;
+    }
+    SFFN_DEV float *part_row(const few::Work &w, int, int r, float m, float l, bool sums) const {
+        if (w.whole) return nullptr;
+        float *slot = a.part + tree_slot_floats(a.row_tile, D) * (size_t)w.slot;
+        if (sums) *reinterpret_cast<float2 *>(slot + (size_t)a.row_tile * D + 2 * r) = make_float2(m, l);
+        return slot + (size_t)r * D;
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(atc::kThreads, 1)
-    k_pages_tc(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-               const __grid_constant__ CUtensorMap map_v, const PagesArgs a) {
+template <int D, int NT>
+__global__ void __launch_bounds__(few::kThreads, 2)
+    k_pages_few(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const PagesArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
+    griddep_wait();
+    griddep_launch_dependents();
     PagesPolicy<D> policy(a);
-    atc::attention_cta<Cfg<D>, D>(policy, map_q, map_k, map_v, map_q, a.scale, a.group, a.err, smem_raw);
+    policy.walk.template start<__nv_bfloat16, D>();
+    few::attention<D, NT>(policy, map_k, map_v, a.at.page_shift, a.n_kv_heads, a.scale, a.err, smem_raw);
 }
 
 // ---------------------------------------------------------------------------
@@ -308,44 +274,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_pages_join(const PagesArgs 
     const int4 cut = __ldcg(a.cuts + w);
     if (cut.x < 0) return;
     const int w0 = cut.z, w1 = cut.w, blocks = (w1 - w0) * parts, b = (w - w0 - 1) * parts + part;
-    const size_t sf = tree_slot_floats(a.group, D);
+    const size_t sf = tree_slot_floats(a.row_tile, D);
+    const int h = cut.y / a.tiles, r0 = cut.y % a.tiles * a.row_tile, rows = min(a.row_tile, a.group - r0);
     auto slot = [&](int k) { return a.part + sf * (size_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)); };
-    for (int r = b * kJoinWarps + (threadIdx.x >> 5); r < a.group; r += blocks * kJoinWarps) {
+    for (int r = b * kJoinWarps + (threadIdx.x >> 5); r < rows; r += blocks * kJoinWarps) {
         JoinedRow<D / 32> j;
-        j.add(w1 - w0 + 1, lane, [&](int k) { return slot(k) + (size_t)a.group * D + 2 * r; },
+        j.add(w1 - w0 + 1, lane, [&](int k) { return slot(k) + (size_t)a.row_tile * D + 2 * r; },
               [&](int k) { return slot(k) + (size_t)r * D; });
-        j.write(static_cast<T *>(a.out) + ((size_t)cut.x * a.n_heads + (size_t)cut.y * a.group + r) * D, lane);
+        j.write(static_cast<T *>(a.out) + ((size_t)cut.x * a.n_heads + (size_t)h * a.group + r0 + r) * D, lane);
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_join(const PagesArgs &a, int grid, cudaStream_t s) {
     if (grid < 2) return cudaSuccess;  // one CTA: nothing is cut
-    const int parts = (a.group + 2 * kJoinWarps - 1) / (2 * kJoinWarps);
+    const int parts = (a.row_tile + 2 * kJoinWarps - 1) / (2 * kJoinWarps);
     return launch_k(k_pages_join<T, D>, dim3((unsigned)((grid - 1) * parts)), dim3(32 * kJoinWarps), 0, s, a, parts);
 }
 
 template <int D>
-cudaError_t launch_f32(const PagesArgs &a, int grid, cudaStream_t s) {
+cudaError_t launch_f32(PagesArgs a, int grid, cudaStream_t s) {
+    a.row_tile = a.group;
+    a.tiles = 1;
     cudaError_t e = set_max_smem((const void *)k_pages_rows<D>, (int)sizeof(rows::Smem<D>));
     if (e == cudaSuccess) e = launch_k(k_pages_rows<D>, dim3(grid), dim3(rows::kThreads), sizeof(rows::Smem<D>), s, a);
     return e == cudaSuccess ? launch_join<float, D>(a, grid, s) : e;
 }
 
+template <int D, int NT>
+cudaError_t launch_few(PagesArgs a, int grid, cudaStream_t s) {
+    const int ps = 1 << a.at.page_shift;
+    a.row_tile = a.group < 8 * NT ? a.group : 8 * NT;
+    a.tiles = (a.group + a.row_tile - 1) / a.row_tile;
+    CUtensorMap mk, mv;
+    // the cache as [8-row group][column block][row][64]: a box is 16 rows of a page, or the page, and all columns
+    const uint64_t dk[4] = {64, 8, D / 64, (uint64_t)a.at.n_pages * a.n_kv_heads * ps / 8}, sk[3] = {D * 2, 128, D * 16};
+    const uint32_t bk[4] = {64, 8, D / 64, (uint32_t)(ps < few::kKeys ? ps : few::kKeys) / 8};
+    if (!make_map_bf16(&mk, a.ck, 4, dk, sk, bk) || !make_map_bf16(&mv, a.cv, 4, dk, sk, bk)) return cudaErrorNotSupported;
+    constexpr int smem = few::Cfg<D>::kSmem;
+    cudaError_t e = set_max_smem((const void *)k_pages_few<D, NT>, smem);
+    if (e == cudaSuccess) e = launch_k(k_pages_few<D, NT>, dim3(2 * grid), dim3(few::kThreads), smem, s, mk, mv, a);
+    return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(a, 2 * grid, s) : e;
+}
+
 template <int D>
 cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
-    const int ps = 1 << a.at.page_shift;
-    CUtensorMap mq, mk, mv;
-    const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, sq[2] = {D * 2, (uint64_t)a.q_stride * 2};
-    // the cache as [8-row group][column block][row][64]: a box is a page's rows (64 at most), all columns
-    const uint64_t dk[4] = {64, 8, D / 64, (uint64_t)a.at.n_pages * a.n_kv_heads * ps / 8}, sk[3] = {D * 2, 128, D * 16};
-    const uint32_t bq[3] = {64, (uint32_t)a.group, 1}, bk[4] = {64, 8, D / 64, (uint32_t)(ps < 64 ? ps : 64) / 8};
-    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 4, dk, sk, bk) ||
-        !make_map_bf16(&mv, a.cv, 4, dk, sk, bk))
-        return cudaErrorNotSupported;
-    cudaError_t e = set_max_smem((const void *)k_pages_tc<D>, Cfg<D>::kSmem);
-    if (e == cudaSuccess) e = launch_k(k_pages_tc<D>, dim3(grid), dim3(atc::kThreads), Cfg<D>::kSmem, s, mq, mk, mv, a);
-    return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(a, grid, s) : e;
+    return a.group <= 8 ? launch_few<D, 1>(a, grid, s) : (a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, 4>(a, grid, s));
 }
 
 }  // namespace
@@ -355,9 +329,9 @@ PagesPlan make_pages_plan(int, int n_heads, int n_kv_heads, int head_dim) {
     p.grid = device_sm_count();
     size_t o = align_up(kControlBytes);
     p.off_cuts = o;
-    o = align_up(o + sizeof(int4) * (size_t)p.grid);
+    o = align_up(o + sizeof(int4) * 2 * (size_t)p.grid);
     p.off_part = o;
-    o = align_up(o + sizeof(float) * 2 * (size_t)p.grid * tree_slot_floats(n_heads / n_kv_heads, head_dim));
+    o = align_up(o + sizeof(float) * 4 * (size_t)p.grid * tree_slot_floats(n_heads / n_kv_heads, head_dim));
     p.total = o;
     return p;
 }

@@ -129,9 +129,8 @@ SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x008
 // Low 32 bits with the first n set (n clamped to 0 .. 32).
 SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// P: the policy (prompts, tree, shared prefixes, chosen pages).  It gives
+// P: the policy (prompts, tree or shared prefixes).  It gives
 //   start                  before the first item (every warp calls it)
-//   kOneToken              an item has one token: the other rows of Q_0 are zeros
 //   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
 //   place, load_kv         where a key tile lies, looked up a tile ahead; the load of its K or V
@@ -207,13 +206,8 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
         return __all_sync(0xffffffffu, mbar_try_wait_for(bar, parity, kHoldNs)) || wait_slow(bar, parity);
     };
 
-    if constexpr (P::kOneToken) {
-        for (int i = tid; i < C::kQ * C::kTile / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(sm_q)[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-    }
     griddep_wait();
-    const int TB = P::kOneToken ? 1 : 128 / G;
+    const int TB = 128 / G;
     __shared__ Work s_work[kItems];
     policy.start();
     griddep_launch_dependents();

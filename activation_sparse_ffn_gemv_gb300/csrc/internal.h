@@ -216,11 +216,13 @@ constexpr int kSharedMaxGroups = 256;  // groups of one sffn_attn_shared call
 struct SharedArgs : TreeArgs {
     const int32_t *group_seqs, *prefix_lens;
     int n_groups;
-    float *home;  // rows of whole items, of prefixes and of own positions
+    int row_tile;   // rows of a row tile that are tokens' rows
+    float *home;    // rows of whole items, of prefixes and of own positions
+    void *entries;  // what the join has to know
 };
 struct SharedPlan {
     int grid, rows_max;
-    size_t off_part, off_home, total;
+    size_t off_part, off_home, off_entries, total;
 };
 SharedPlan make_shared_plan(int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_shared(const SharedArgs &a, const SharedPlan &p, int dtype, int head_dim, cudaStream_t s);
@@ -268,7 +270,8 @@ struct PagesArgs {
     int n_keep;
     float scale;
     void *out;
-    int4 *cuts;   // for each CTA: token, key head, first and last CTA of the item that its range's beginning cuts
+    int row_tile, tiles;  // rows of a row tile, row tiles of a key head's rows
+    int4 *cuts;   // for each CTA: token, its item, first and last CTA of the item that its range's beginning cuts
     float *part;  // partial results of cut items
     int32_t *err;
 };
