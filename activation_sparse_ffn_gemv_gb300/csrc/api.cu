@@ -690,11 +690,15 @@ sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads
     a.scale = scale;
     a.out = out;
     a.err = static_cast<int32_t *>(workspace);
-    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
-    a.home = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_home);
-    a.entries = static_cast<char *>(workspace) + p.off_entries;
-    a.rows_max = p.rows_max;
-    st = run_attn_shared(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
+    char *ws = static_cast<char *>(workspace);
+    a.sms = p.sms;
+    a.parts[0] = a.parts[1] = reinterpret_cast<float *>(ws + p.off_part);
+    a.rows_max[0] = a.rows_max[1] = p.rows_max;
+    a.part_few = reinterpret_cast<float *>(ws + p.off_few);
+    a.home = reinterpret_cast<float *>(ws + p.off_home);
+    a.entries = ws + p.off_entries;
+    a.seq_of = reinterpret_cast<int32_t *>(ws + p.off_seq_of);
+    st = run_attn_shared(a, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());
     return st;
 }

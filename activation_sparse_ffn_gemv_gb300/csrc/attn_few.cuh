@@ -4,15 +4,16 @@
 //   o_r = sum_j w_rj v_j / sum_j w_rj,  w_rj = exp(scale q_r . k_j - m_r)
 //
 // With 8 rows a key the bound is HBM, the keys and values read once, and what keeps a kernel from it is
-// latency: where an item begins (its pages are looked up, its first keys come), where it ends (the
-// parts are joined and written).  So each warp works on its own: it has a ring of 16-key tiles that it fills by
-// TMA from one lane, and goes on loading the next item while it finishes one; two CTAs of four warps share an SM.
+// latency: where an item begins (its pages are looked up, its first keys come), where it ends (its rows
+// are written).  So each warp works by itself, on a stretch of the line of work of its own: it has a ring of 16-key
+// tiles that it fills by TMA from one lane, and goes on loading the next item while it finishes one; two CTAs
+// of four warps share an SM.  (Four warps an item, joined in shared memory at its end: 3000 cycles an item for the join
+// alone.)
 //
 // The products are mma.sync with the keys as the 16-row operand and the rows as the 8 columns (tcgen05 tiles
 // have 128 rows; 8 of them would be used): S^T = K Q^T, then O^T += V^T P^T, V's operand read transposed by
 // ldmatrix and P^T made of S^T's registers by two 8 x 8 transpositions.  A tile of 16 keys costs a warp
-// 16 products of D = 128 for every 8 rows.  The four warps of a CTA take the tiles of a piece in turn and join
-// their results (maximum, sum, row) in shared memory at its end.
+// 16 products of D = 128 for every 8 rows.
 //
 // A weight of zero times an infinite or NaN value would be NaN: where a tile has keys that some row does not see and
 // V holds such a value, its product is made value by value, leaving out what a row does not see.
@@ -28,25 +29,26 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kKeys = 16;           // keys of a tile
 constexpr float kLazyLog2 = 8.f;    // the running maximum moves when passed by 2^8
+constexpr uint32_t kHoldNs = 1000000;  // the hardware may hold a waiting warp for 1 ms at a time
 
 template <int D>
 struct Cfg {
     static constexpr int kTile = kKeys * D * 2;               // bytes of K or V
     static constexpr int kStages = D == 128 ? 3 : 6;          // K and V pairs of a warp's ring
     static constexpr int kRing = kWarps * kStages * 2 * kTile;
-    static constexpr int kPad = 68;                           // floats of a row of 64 columns in the join
-    static constexpr int kJoin = kWarps * 8 * kPad * 4;
-    static constexpr int kSmem = kRing + kJoin + 1024 /*alignment*/;
+    static constexpr int kSmem = kRing + 1024 /*alignment*/;
 };
 
-// A piece of an item: `nt` tokens' rows of key head h against the keys at places [k0, k1).
+// Rows of the largest row tile (registers: 4 results a lane for every row and 64 columns).
+constexpr int max_rows(int D) { return D == 128 ? 16 : 32; }
+
+// A piece of an item: rows of key head h against the keys at places [k0, k1).
 struct Work {
-    int q_row, nt;    // first token, tokens
+    int q_row;        // first token
     int r0, rows;     // first row (token * G + query head) of the row tile, rows
     int h;
     int k0, k1, all;  // keys below `all` are seen by every row
-    int seq, tok0;    // the policy's own
-    int whole, slot, kind;
+    int seq, ctx, whole, slot, kind;  // the policy's own
 };
 
 SFFN_DEV float ex2(float x) {
@@ -82,12 +84,34 @@ SFFN_DEV void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
 }
 SFFN_DEV bool nonfinite2(uint32_t w) { return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0; }
 
+// A tile load and the announcement of its bytes, issued by one lane of a converged warp: the operands are the same in every
+// lane, and as the compiler sees that, they go straight to the uniform registers that the instruction takes.
+SFFN_DEV void load_warp(uint32_t dst, const CUtensorMap *map, int group, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;\n\t}\n" ::"r"(dst),
+        "l"(map), "r"(0), "r"(group), "r"(bar), "l"(policy)
+        : "memory");
+}
+SFFN_DEV void expect_warp(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+
 // P: the policy.  It gives
-//   bool next(Work &)          the CTA's pieces in turn (every warp walks by itself)
+//   bool next(Work &)          the warp's pieces in turn
 //   int page_of(w, key)        the cache's page behind a place; n_pages or more: none (zeros)
 //   const bf16 *query(w, row)  a row's query
 //   bool sees(w, row, key)     of a key at or past `all`
-//   T *out_row / float *part   where a row goes (null: the other one does)
+//   bool partial(w)            whether the result is a partial one
+//   bf16 *out_row(w, row)      where a row goes
+//   float *part_row, part_sums where a row (`r` of the tile) of a partial result goes, and its (maximum, sum)
 // NT: products of 8 rows; rows of a tile: 8 NT at most.
 template <int D, int NT, typename P>
 SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &map_v, int page_shift, int n_kv_heads,
@@ -95,17 +119,13 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
     using C = Cfg<D>;
     constexpr int NS = C::kStages, KB = D / 16;
     __shared__ uint64_t full[kWarps][NS];
-    __shared__ float2 s_ml[kWarps][8 * NT];
-    __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const uint32_t raw_addr = smem_u32(smem_raw), base = (raw_addr + 1023u) & ~1023u;
     unsigned char *ring = smem_raw + (base - raw_addr) + warp * NS * 2 * C::kTile;
     const uint32_t ring_addr = base + (uint32_t)(warp * NS * 2 * C::kTile);
-    float *join = reinterpret_cast<float *>(smem_raw + (base - raw_addr) + C::kRing);
     if (tid == 0) {
         for (int w = 0; w < kWarps; ++w)
             for (int i = 0; i < NS; ++i) mbar_init(&full[w][i], 1);
-        s_abort = 0;
         mbar_fence_init();
         tc::prefetch_tensormap(&map_k);
         tc::prefetch_tensormap(&map_v);
@@ -114,49 +134,52 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
 
     // ---- loads: this warp's tiles, one after the other through the pieces, NS ahead at most ----
     P ahead = policy;                    // a walk of its own
-    const int box = min(kKeys, 1 << page_shift), boxes = kKeys / box;  // rows of a copy, copies of a tile
+    const int box = min(kKeys, 1 << page_shift);  // rows of a copy: a tile is one, or two of 8
     const uint64_t keep = l2_evict_first_policy();
-    Work lw;
-    int li = 0, ln = 0, issued = 0;      // tile of the piece, tiles of it (for this warp), tiles issued
-    int pages[2] = {0, 0};               // this lane's pages of 32 tiles from li on: tile li + lane, both halves
-    bool more = true;
-    auto tiles_of = [&](const Work &w) { return max(0, ((w.k1 - w.k0 + kKeys - 1) / kKeys - warp + kWarps - 1) / kWarps); };
-    auto key_of = [&](const Work &w, int i) { return w.k0 + (i * kWarps + warp) * kKeys; };
-    auto given_up = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
+    Work lw, nw;                         // the piece whose tiles are loaded, and the one after it
+    int li = 0, ln = 0, issued = 0, islot = 0;  // tile of the piece, tiles of it, tiles issued, ring position
+    int pages[2] = {0, 0}, npages[2] = {0, 0};  // this lane's pages of 32 tiles: tile (li & ~31) + lane, both halves
+    int nn;                              // the next piece's tiles (-1: there is none)
+    bool dead = false;                   // a wait has run out, nothing is loaded or written any more
+    auto tiles_of = [&](const Work &w) { return (w.k1 - w.k0 + kKeys - 1) / kKeys; };
+    auto key_of = [&](const Work &w, int i) { return w.k0 + i * kKeys; };
+    auto look_up = [&](const Work &w, int i, int (&pg)[2]) {  // pages of tiles i + lane
+        const int key = key_of(w, i + lane);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            if (b * box < kKeys && key + b * box < w.k1) pg[b] = ahead.page_of(w, key + b * box);
+    };
+    auto fetch = [&]() {  // the next piece, and its first pages, a piece ahead of their use
+        nn = ahead.next(nw) ? tiles_of(nw) : -1;
+        if (nn > 0) look_up(nw, 0, npages);
+    };
+    fetch();
     auto issue = [&]() {
-        while (more && li == ln) {
-            more = ahead.next(lw);
-            li = 0;
-            ln = more ? tiles_of(lw) : 0;
+        while (li == ln && nn >= 0) {
+            lw = nw, li = 0, ln = nn;
+            pages[0] = npages[0], pages[1] = npages[1];
+            fetch();
         }
-        if (!more || given_up()) return;
-        if ((li & 31) == 0) {
-            const int i = li + lane, key = key_of(lw, i);
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                if (b < boxes && i < ln && key + b * box < lw.k1) pages[b] = ahead.page_of(lw, key + b * box);
-        }
-        const int s = issued % NS, key = key_of(lw, li), src = li & 31;
-        int n = 0;
-        int row[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int pg = __shfl_sync(0xffffffffu, pages[b], src);
-            if (b < boxes && key + b * box < lw.k1) {
-                ++n;
-                row[b] = (int)((((long long)pg * n_kv_heads + lw.h) << page_shift) + ((key + b * box) & ((1 << page_shift) - 1)));
-            }
-        }
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&full[warp][s], (uint32_t)(n * box * D * 4));
-            unsigned char *dst = ring + s * 2 * C::kTile;
-            for (int b = 0; b < n; ++b) {
-                tc::tma_load_4d(dst + b * box * D * 2, &map_k, 0, 0, 0, row[b] >> 3, &full[warp][s], keep);
-                tc::tma_load_4d(dst + C::kTile + b * box * D * 2, &map_v, 0, 0, 0, row[b] >> 3, &full[warp][s], keep);
-            }
+        if (li == ln || dead) return;
+        const int key = key_of(lw, li);
+        if ((li & 31) == 0 && li > 0) look_up(lw, li, pages);
+        // 8-row groups of the cache: below 2^28
+        auto group = [&](int pg, int k) {
+            return ((pg * n_kv_heads + lw.h) << (page_shift - 3)) + ((k & ((1 << page_shift) - 1)) >> 3);
+        };
+        const int g0 = group(__shfl_sync(0xffffffffu, pages[0], li & 31), key), two = box < kKeys && key + box < lw.k1;
+        const int g1 = two ? group(__shfl_sync(0xffffffffu, pages[1], li & 31), key + box) : 0;
+        const uint32_t bar = smem_u32(&full[warp][islot]), dst = ring_addr + (uint32_t)(islot * 2 * C::kTile);
+        expect_warp(bar, (uint32_t)((1 + two) * box * D * 4));
+        load_warp(dst, &map_k, g0, bar, keep);
+        load_warp(dst + C::kTile, &map_v, g0, bar, keep);
+        if (two) {
+            load_warp(dst + box * D * 2, &map_k, g1, bar, keep);
+            load_warp(dst + C::kTile + box * D * 2, &map_v, g1, bar, keep);
         }
         ++li;
         ++issued;
+        if (++islot == NS) islot = 0;
     };
     for (int i = 0; i < NS; ++i) issue();
 
@@ -164,14 +187,16 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
     // K by rows (keys) and columns, V transposed.
     const int mi = lane >> 3, l8 = lane & 7;
     const int k_row = l8 + (mi & 1) * 8, k_col = (mi >> 1) * 8, v_row = l8 + (mi >> 1) * 8, v_col = (mi & 1) * 8;
+    // (a chunk's place is its number and the row's, exclusive-or: along a row the even chunks differ in bits 5 and 6)
     auto at = [&](int r, int col) {
         return (uint32_t)((r >> 3) * (D / 64) * 1024 + (col >> 6) * 1024 + (r & 7) * 128 + ((((col & 63) >> 3) ^ (r & 7)) << 4));
     };
     const float cf = scale * 1.44269504088896341f;  // the exponent in powers of two
-    int used = 0, landed = 0;  // tiles taken, and those that came
-    Work w;
-    while (policy.next(w)) {
-        uint32_t q[NT][KB][2];
+    const uint32_t k_lane = at(k_row, k_col), v_lane = at(v_row, v_col);
+    int landed = 0, slot = 0;  // tiles that came, ring position and its parity
+    uint32_t par = 0;
+    uint32_t q[NT][KB][2];
+    auto load_q = [&](const Work &w) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int row = n * 8 + g;
@@ -182,6 +207,11 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
                 q[n][k][1] = __ldg(src + k * 8 + c + 4);
             }
         }
+    };
+    Work w, w2;
+    bool have = policy.next(w);
+    if (have) load_q(w);
+    for (; have; w = w2) {
         float o[NT][KB][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -191,18 +221,23 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
             l[n][0] = l[n][1] = 0.f;
         }
         const int tiles = tiles_of(w);
-        for (int i = 0; i < tiles; ++i, ++used) {
-            const int st = used % NS, kb = key_of(w, i);
-            // (once a wait has run out nothing is loaded or written any more, and the loops come to their end)
-            if (!given_up()) {
-                if (__all_sync(0xffffffffu, mbar_wait(&full[warp][st], (uint32_t)((used / NS) & 1)))) {
+        for (int i = 0; i < tiles; ++i) {
+            const int st = slot, kb = key_of(w, i);
+            if (!dead) {
+                bool came = __all_sync(0xffffffffu, mbar_try_wait(&full[warp][st], par));
+                if (!came) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (!came && !__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs))
+                        came = __all_sync(0xffffffffu, mbar_try_wait_for(&full[warp][st], par, kHoldNs));
+                }
+                if (came) {
                     ++landed;
-                } else if (lane == 0) {
-                    s_abort = 1;
-                    record_error(err, SFFN_ERR_TIMEOUT);
+                } else {
+                    dead = true;
+                    if (lane == 0) record_error(err, SFFN_ERR_TIMEOUT);
                 }
             }
-            __syncwarp();
+            if (++slot == NS) slot = 0, par ^= 1;
             const uint32_t kt = ring_addr + (uint32_t)(st * 2 * C::kTile), vt = kt + C::kTile;
             float s[NT][4];
             {
@@ -214,7 +249,7 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
 #pragma unroll
                 for (int k = 0; k < KB; ++k) {
                     uint32_t a[4];
-                    ldmatrix4(kt + at(k_row, k * 16 + k_col), a);
+                    ldmatrix4(((kt + k_lane) ^ ((k & 3) << 5)) + (k >> 2) * 1024, a);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma(NT == 1 && (k & 1) ? s2[n] : s[n], a, q[n][k][0], q[n][k][1]);
                 }
@@ -290,7 +325,7 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
 #pragma unroll
                 for (int k = 0; k < KB; ++k) {
                     uint32_t a[4];
-                    ldmatrix4_trans(vt + at(v_row, k * 16 + v_col), a);
+                    ldmatrix4_trans(((vt + v_lane) ^ ((k & 3) << 5)) + (k >> 2) * 1024, a);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma(o[n][k], a, pt[n][0], pt[n][1]);
                 }
@@ -322,53 +357,39 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
             __syncwarp();  // every lane has read the tile
             issue();
         }
-        // ---- join the warps' results ----
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[n][e];
-#pragma unroll
-                for (int f = 4; f < 32; f <<= 1) x += __shfl_xor_sync(0xffffffffu, x, f);
-                if (g == 0) s_ml[warp][n * 8 + 2 * c + e] = make_float2(m[n][e], x);
-            }
+        // the next piece's queries come while this one's rows are written
+        have = policy.next(w2);
+        if (have) load_q(w2);
+        if (dead) continue;
+        const bool partial = policy.partial(w);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            const int row = n * 8 + 2 * c;  // and the one after it
             if (n * 8 >= w.rows) break;
 #pragma unroll
-            for (int dh = 0; dh < D / 64; ++dh) {
-                float *mine = join + warp * 8 * C::kPad;
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int f = 4; f < 32; f <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], f);
+            if (partial) {  // 32 bytes of four rows at a time
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        mine[(2 * c + (e & 1)) * C::kPad + k * 16 + g + (e >> 1) * 8] = o[n][dh * 4 + k][e];
-                __syncthreads();
-                const int row = tid >> 4, col = (tid & 15) * 4;
-                float M = -INFINITY, L = 0.f;
+                for (int e = 0; e < 2; ++e) {
+                    if (row + e >= w.rows) continue;
+                    float *dst = policy.part_row(w, w.r0 + row + e, row + e) + g;
 #pragma unroll
-                for (int x = 0; x < kWarps; ++x) M = fmaxf(M, s_ml[x][n * 8 + row].x);
-                const float ref = M == -INFINITY ? 0.f : M;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    const float2 ml = s_ml[x][n * 8 + row];
-                    const float f = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2((ml.x - ref) * cf);  // (no key: no weight)
-                    const float4 y = *reinterpret_cast<const float4 *>(join + (x * 8 + row) * C::kPad + col);
-                    L += f * ml.y;
-                    v.x += f * y.x, v.y += f * y.y, v.z += f * y.z, v.w += f * y.w;
+                    for (int k = 0; k < KB; ++k) dst[k * 16] = o[n][k][e], dst[k * 16 + 8] = o[n][k][2 + e];
+                    if (g == 0) *policy.part_sums(w, w.r0 + row + e, row + e) = make_float2(m[n][e] * scale, l[n][e]);
                 }
-                if (n * 8 + row < w.rows && !s_abort) {
-                    float *part = policy.part_row(w, w.r0 + n * 8 + row, n * 8 + row, M * scale, L, dh == 0 && col == 0);
-                    if (part) {
-                        *reinterpret_cast<float4 *>(part + dh * 64 + col) = v;
-                    } else {
-                        const float inv = L == 0.f ? 0.f : 1.f / L;
-                        *reinterpret_cast<uint2 *>(policy.out_row(w, w.r0 + n * 8 + row) + dh * 64 + col) =
-                            make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+            } else {  // pairs of columns of row g, by the transpose of pairs of rows
+                const float i0 = l[n][0] == 0.f ? 0.f : 1.f / l[n][0], i1 = l[n][1] == 0.f ? 0.f : 1.f / l[n][1];
+                const bool there = n * 8 + g < w.rows;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(policy.out_row(w, w.r0 + (there ? n * 8 + g : 0))) + c;
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t v = transpose8(pack_bf16(o[n][k][2 * half] * i0, o[n][k][2 * half + 1] * i1));
+                        if (there) dst[k * 8 + half * 4] = v;
                     }
-                }
-                __syncthreads();
             }
         }
     }

@@ -1,9 +1,9 @@
 // attn_pages.cu -- attention of each token over its chosen pages of the paged cache (sm_103a).
 //
-// An item is a (token, key head, row tile): up to 32 of the G rows against the n_sel chosen pages, taken one after the
+// An item is a (token, key head, row tile): up to 32 (16 of 128 elements) of the G rows against the n_sel chosen pages, taken one after the
 // other as if they were consecutive positions.  The work of all items is one line as in attn.cuh (units of 64
 // positions and kItemCost more per item), token by token and head by head, cut evenly over the
-// CTAs; items that lie in one CTA's range are finished there, the pieces of a cut item are joined by
+// warps (fp32: the CTAs); items that lie in one range are finished there, the pieces of a cut item are joined by
 // k_pages_join.
 #include "attn_rows.cuh"
 #include "attn_few.cuh"
@@ -12,9 +12,9 @@ namespace sffn {
 
 namespace {
 
-// Units that an item costs by itself (48 tokens of up to 2048 positions, 8 key heads: 58.1 us with 2, 54.0 with 4, 54.5
-// with 6).
-constexpr int kItemCost = 4;
+// Units (of 64 positions) that an item costs by itself (48 tokens of up to 2048 positions, 8 key heads: 55.5 us with 1,
+// 57.1 with 2, 57.5 with 4).
+constexpr int kItemCost = 1;
 
 // Pages of token t, 0 if it reads none; -1: its row is left as it is (padding, or it breaks the contract).
 SFFN_DEV int pages_of(const PagesArgs &a, int t, bool record) {
@@ -38,21 +38,23 @@ struct PagesPiece {
     bool whole;
 };
 
-// A CTA's walk along the line.
+// A CTA's (or a warp's) walk along the line.
 struct PagesWalk {
     const PagesArgs &a;
     long long u, u1;  // next place, end of the range
-    long long at;     // where token t's items begin
-    int t, n;         // token, its pages
+    long long at;     // where the item of place u (or the one before it, all done) begins
+    int t, n, span;   // token, its pages, length of its items
+    int h, tile;      // the item
+    int range;        // which range this is
 
     SFFN_DEV explicit PagesWalk(const PagesArgs &args) : a(args) {}
 
-    // Every thread of the CTA: its range and the token at its beginning; rows of tokens without pages are
-    // zeroed (dealt to the CTAs by token); tells the join which item the range's beginning cuts.
-    template <typename T, int D>
+    // Every thread of the CTA: its range (RANGES = 1), or its warp's, and the token at the range's beginning; rows of
+    // tokens without pages are zeroed (dealt to the CTAs by token); tells the join which item the beginning cuts.
+    template <typename T, int D, int RANGES>
     SFFN_DEV void start() {
-        __shared__ long long s_scan[33], s_at;
-        __shared__ int s_t;
+        __shared__ long long s_scan[33], s_at[RANGES];
+        __shared__ int s_t[RANGES];
         const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
         const int per = (a.T + nt - 1) / nt, t0 = min(a.T, tid * per), t1 = min(a.T, t0 + per);
         long long sum = 0;
@@ -78,50 +80,61 @@ struct PagesWalk {
             if (w < warp) before += s_scan[w];
             total += s_scan[w];
         }
-        const int W = tree_ctas(total, gridDim.x), b = blockIdx.x;
-        u = b < W ? tree_cut(total, b, W) : 0;
-        u1 = b < W ? tree_cut(total, b + 1, W) : 0;
-        if (b < W && before <= u && u < before + sum) {  // the token is one of this thread's
-            int i = t0;
-            for (;; ++i) {
-                const long long len = (long long)pages_span(a, pages_of(a, i, false)) * a.n_kv_heads * a.tiles;
-                if (u < before + len) break;
-                before += len;
+        const int W = tree_ctas(total, gridDim.x * RANGES);
+        for (int r = 0; r < RANGES; ++r) {
+            const int b = blockIdx.x * RANGES + r;
+            if (b >= W) break;
+            const long long place = tree_cut(total, b, W);
+            if (before <= place && place < before + sum) {  // the token is one of this thread's
+                long long begin = before;
+                int i = t0;
+                for (;; ++i) {
+                    const long long len = (long long)pages_span(a, pages_of(a, i, false)) * a.n_kv_heads * a.tiles;
+                    if (place < begin + len) break;
+                    begin += len;
+                }
+                s_t[r] = i;
+                s_at[r] = begin;
             }
-            s_t = i;
-            s_at = before;
         }
         __syncthreads();
-        t = s_t;
-        at = s_at;
-        n = b < W ? pages_of(a, t, false) : 0;
-        if (tid == 0) {
-            int4 cut = make_int4(-1, 0, 0, 0);  // token, its item, first and last CTA of the cut item
-            if (b > 0 && b < W) {
-                const int span = pages_span(a, n), item = (int)((u - at) / span);
-                const long long i0 = at + (long long)item * span;
-                const int w0 = tree_owner(total, i0 + kItemCost, W), w1 = tree_owner(total, i0 + span - 1, W);
-                if (w0 < b && b <= w1) cut = make_int4(t, item, w0, w1);
-            }
-            a.cuts[b] = cut;
+        const int r = RANGES == 1 ? 0 : warp, b = blockIdx.x * RANGES + r;
+        range = b;
+        u = u1 = 0;
+        h = tile = 0;
+        int4 cut = make_int4(-1, 0, 0, 0);  // token, its item, first and last range of the cut item
+        if (b < W) {
+            u = tree_cut(total, b, W);
+            u1 = tree_cut(total, b + 1, W);
+            t = s_t[r];
+            n = pages_of(a, t, false);
+            span = pages_span(a, n);
+            const int item = (int)((u - s_at[r]) / span);
+            at = s_at[r] + (long long)item * span;
+            h = item / a.tiles;
+            tile = item - h * a.tiles;
+            const int w0 = tree_owner(total, at + kItemCost, W), w1 = tree_owner(total, at + span - 1, W);
+            if (w0 < b && b <= w1) cut = make_int4(t, item, w0, w1);
         }
+        if (RANGES == 1 ? tid == 0 : lane == 0) a.cuts[b] = cut;
     }
 
     // The next piece with units (false: none is left).
     SFFN_DEV bool next(PagesPiece &p) {
         for (;;) {
             if (u >= u1) return false;
-            int span = pages_span(a, n);
-            while (u >= at + (long long)span * a.n_kv_heads * a.tiles) {  // on to the token that place u belongs to
-                at += (long long)span * a.n_kv_heads * a.tiles;
-                n = pages_of(a, ++t, false);
-                span = pages_span(a, n);
+            if (u >= at + span) {  // on to the next item
+                at += span;
+                if (++tile == a.tiles) tile = 0, ++h;
+                if (h == a.n_kv_heads) {
+                    h = 0;
+                    do n = pages_of(a, ++t, false); while (n <= 0);  // (place u is some token's)
+                    span = pages_span(a, n);
+                }
             }
-            const long long local = u - at;
-            const int item = (int)(local / span), off = (int)(local - (long long)item * span);
-            const int end = (int)min((long long)span, off + (u1 - u));
+            const int off = (int)(u - at), end = (int)min((long long)span, off + (u1 - u));
             u += end - off;
-            p.t = t, p.h = item / a.tiles, p.tile = item % a.tiles, p.n = n;
+            p.t = t, p.h = h, p.tile = tile, p.n = n;
             p.un0 = max(0, off - kItemCost), p.un1 = max(0, end - kItemCost);
             p.whole = p.un0 == 0 && end == span;
             if (p.un0 < p.un1) return true;
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_pages_rows(const PagesArg
     griddep_wait();
     griddep_launch_dependents();
     PagesWalk walk(a);
-    walk.start<float, D>();
+    walk.start<float, D, 1>();
     const int tid = threadIdx.x, G = a.group, ps = 1 << a.at.page_shift;
     PagesPiece p;
     while (walk.next(p)) {
@@ -219,14 +232,13 @@ struct PagesPolicy {
         PagesPiece p;
         if (!walk.next(p)) return false;
         w.q_row = p.t;
-        w.nt = 1;
         w.h = p.h;
         w.r0 = p.tile * a.row_tile;
         w.rows = min(a.row_tile, a.group - w.r0);
         w.k0 = p.un0 * kTreeUnit;
         w.k1 = w.all = max(w.k0, min(seen(a, p.t, p.h, p.n), p.un1 * kTreeUnit));  // (none behind the last that it sees)
         w.whole = p.whole;
-        w.slot = 2 * blockIdx.x + (p.un0 > 0 ? 0 : 1);
+        w.slot = 2 * walk.range + (p.un0 > 0 ? 0 : 1);
         return true;
     }
     SFFN_DEV int page_of(const few::Work &w, int j) const {
@@ -240,11 +252,12 @@ struct PagesPolicy {
     SFFN_DEV __nv_bfloat16 *out_row(const few::Work &w, int row) const {
         return static_cast<__nv_bfloat16 *>(a.out) + ((size_t)w.q_row * a.n_heads + (size_t)w.h * a.group + row) * D;
     }
-    SFFN_DEV float *part_row(const few::Work &w, int, int r, float m, float l, bool sums) const {
-        if (w.whole) return nullptr;
-        float *slot = a.part + tree_slot_floats(a.row_tile, D) * (size_t)w.slot;
-        if (sums) *reinterpret_cast<float2 *>(slot + (size_t)a.row_tile * D + 2 * r) = make_float2(m, l);
-        return slot + (size_t)r * D;
+    SFFN_DEV bool partial(const few::Work &w) const { return !w.whole; }
+    SFFN_DEV float *part_row(const few::Work &w, int, int r) const {
+        return a.part + tree_slot_floats(a.row_tile, D) * (size_t)w.slot + (size_t)r * D;
+    }
+    SFFN_DEV float2 *part_sums(const few::Work &w, int, int r) const {
+        return reinterpret_cast<float2 *>(part_row(w, 0, a.row_tile) + 2 * r);
     }
 };
 
@@ -255,12 +268,12 @@ __global__ void __launch_bounds__(few::kThreads, 2)
     griddep_wait();
     griddep_launch_dependents();
     PagesPolicy<D> policy(a);
-    policy.walk.template start<__nv_bfloat16, D>();
+    policy.walk.template start<__nv_bfloat16, D, few::kWarps>();
     few::attention<D, NT>(policy, map_k, map_v, a.at.page_shift, a.n_kv_heads, a.scale, a.err, smem_raw);
 }
 
 // ---------------------------------------------------------------------------
-// Join: `parts` blocks for each place between two CTAs' ranges; those of all the places that cut an
+// Join: `parts` blocks for each place between two ranges; those of all the places that cut an
 // item share its rows, a warp a row.
 // ---------------------------------------------------------------------------
 
@@ -286,10 +299,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_pages_join(const PagesArgs 
 }
 
 template <typename T, int D>
-cudaError_t launch_join(const PagesArgs &a, int grid, cudaStream_t s) {
-    if (grid < 2) return cudaSuccess;  // one CTA: nothing is cut
+cudaError_t launch_join(const PagesArgs &a, int ranges, cudaStream_t s) {
+    if (ranges < 2) return cudaSuccess;  // one: nothing is cut
     const int parts = (a.row_tile + 2 * kJoinWarps - 1) / (2 * kJoinWarps);
-    return launch_k(k_pages_join<T, D>, dim3((unsigned)((grid - 1) * parts)), dim3(32 * kJoinWarps), 0, s, a, parts);
+    return launch_k(k_pages_join<T, D>, dim3((unsigned)((ranges - 1) * parts)), dim3(32 * kJoinWarps), 0, s, a, parts);
 }
 
 template <int D>
@@ -314,12 +327,13 @@ cudaError_t launch_few(PagesArgs a, int grid, cudaStream_t s) {
     constexpr int smem = few::Cfg<D>::kSmem;
     cudaError_t e = set_max_smem((const void *)k_pages_few<D, NT>, smem);
     if (e == cudaSuccess) e = launch_k(k_pages_few<D, NT>, dim3(2 * grid), dim3(few::kThreads), smem, s, mk, mv, a);
-    return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(a, 2 * grid, s) : e;
+    return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(a, 2 * grid * few::kWarps, s) : e;
 }
 
 template <int D>
 cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
-    return a.group <= 8 ? launch_few<D, 1>(a, grid, s) : (a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, 4>(a, grid, s));
+    if (a.group <= 8) return launch_few<D, 1>(a, grid, s);
+    return a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, few::max_rows(D) / 8>(a, grid, s);
 }
 
 }  // namespace
@@ -329,9 +343,13 @@ PagesPlan make_pages_plan(int, int n_heads, int n_kv_heads, int head_dim) {
     p.grid = device_sm_count();
     size_t o = align_up(kControlBytes);
     p.off_cuts = o;
-    o = align_up(o + sizeof(int4) * 2 * (size_t)p.grid);
+    const size_t ranges = 2 * few::kWarps * (size_t)p.grid;
+    o = align_up(o + sizeof(int4) * ranges);
     p.off_part = o;
-    o = align_up(o + sizeof(float) * 4 * (size_t)p.grid * tree_slot_floats(n_heads / n_kv_heads, head_dim));
+    // bf16: a slot pair a warp, of a row tile; fp32: a CTA, of all rows
+    const int G = n_heads / n_kv_heads, most = few::max_rows(head_dim);
+    const size_t b = ranges * tree_slot_floats(G < most ? G : most, head_dim), f = p.grid * tree_slot_floats(G, head_dim);
+    o = align_up(o + sizeof(float) * 2 * (b > f ? b : f));
     p.total = o;
     return p;
 }

@@ -216,16 +216,25 @@ constexpr int kSharedMaxGroups = 256;  // groups of one sffn_attn_shared call
 struct SharedArgs : TreeArgs {
     const int32_t *group_seqs, *prefix_lens;
     int n_groups;
-    int row_tile;   // rows of a row tile that are tokens' rows
-    float *home;    // rows of whole items, of prefixes and of own positions
-    void *entries;  // what the join has to know
+    int sms;                // SMs
+    // of prefixes, of own positions:
+    int tile_rows[2];       // rows (token * G + query head) of a row tile
+    int cost[2];            // units that an item costs by itself
+    int per[2];             // ranges (CTAs or warps) an SM has of the kernel that takes them
+    float *parts[2];        // slots for the pieces of cut items
+    int rows_max[2];        // rows of a slot
+    int split;              // two kernels
+    float *part_few;        // attn_few.cuh's slots
+    float *home;            // rows of whole items, of prefixes and of own positions
+    void *entries;          // what the join has to know of the sequences
+    int32_t *seq_of;        // a token's sequence
 };
 struct SharedPlan {
-    int grid, rows_max;
-    size_t off_part, off_home, off_entries, total;
+    int sms, rows_max;
+    size_t off_part, off_few, off_home, off_entries, off_seq_of, total;
 };
 SharedPlan make_shared_plan(int T, int n_heads, int n_kv_heads, int head_dim);
-sffn_status run_attn_shared(const SharedArgs &a, const SharedPlan &p, int dtype, int head_dim, cudaStream_t s);
+sffn_status run_attn_shared(const SharedArgs &a, int dtype, int head_dim, cudaStream_t s);
 
 struct BoundsArgs {
     const void *ck;
@@ -271,7 +280,7 @@ struct PagesArgs {
     float scale;
     void *out;
     int row_tile, tiles;  // rows of a row tile, row tiles of a key head's rows
-    int4 *cuts;   // for each CTA: token, its item, first and last CTA of the item that its range's beginning cuts
+    int4 *cuts;   // for each range: token, its item, first and last range of the item that its beginning cuts
     float *part;  // partial results of cut items
     int32_t *err;
 };
