@@ -7,6 +7,7 @@
 // k_pages_join.
 #include "attn_rows.cuh"
 #include "attn_few.cuh"
+#include "attn_tc.cuh"
 
 namespace sffn {
 
@@ -273,6 +274,278 @@ __global__ void __launch_bounds__(few::kThreads, 2)
 }
 
 // ---------------------------------------------------------------------------
+// bf16, many tokens of a sequence: attn_tc.cuh over the union of their pages
+//
+// A row tile has TB = 128 / G consecutive tokens; a run of them that are of one sequence is an item (for each key head).
+// Neighbouring tokens choose mostly the same pages, so the item reads the union of their pages once, and a row's mask leaves
+// out the pages that its token has not chosen: with 18 tokens of 48 of 480 pages each, about 90 pages are read where
+// the tokens one by one read 864.  k_pages_runs finds the runs and counts each union; the loading warp merges the (ascending)
+// lists as it goes, a lane a token, and leaves each key tile's pages and the tokens that have them in a small ring.
+// ---------------------------------------------------------------------------
+
+constexpr int kUnionWidth = 32768;  // pages of a table row that the count's bit set holds
+
+__global__ void __launch_bounds__(128) k_pages_runs(const PagesArgs a, int tokens, int d_bytes) {
+    __shared__ uint32_t s_set[kUnionWidth / 32];
+    __shared__ int s_seq[128], s_n[128], s_run[128], s_sum[4];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0), h = blockIdx.y, tid = threadIdx.x;
+    if (tid < nt) {
+        s_n[tid] = pages_of(a, t0 + tid, h == 0);
+        s_seq[tid] = a.at.seqs[t0 + tid];
+    }
+    __syncthreads();
+    if (tid < nt) {
+        int len = 0;  // tokens of the run that begins here (0: none does)
+        if (s_n[tid] > 0 && (tid == 0 || s_n[tid - 1] <= 0 || s_seq[tid - 1] != s_seq[tid]))
+            for (len = 1; tid + len < nt && s_n[tid + len] > 0 && s_seq[tid + len] == s_seq[tid];) ++len;
+        s_run[tid] = len;
+        if (h == 0) a.runs[t0 + tid] = len;
+        if (s_n[tid] == 0) {  // a token without pages has zeros
+            uint4 *row = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.out) +
+                                                   ((size_t)(t0 + tid) * a.n_heads + (size_t)h * a.group) * d_bytes);
+            for (int e = 0; e < a.group * d_bytes / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    __syncthreads();
+    const int words = (min(a.at.table_width, kUnionWidth) + 31) / 32;
+    for (int i = 0; i < nt; ++i) {
+        const int len = s_run[i];
+        if (len == 0) continue;
+        for (int x = tid; x < words; x += 128) s_set[x] = 0;
+        __syncthreads();
+        for (int x = tid; x < len * a.n_keep; x += 128) {
+            const int j = i + x / a.n_keep, k = x % a.n_keep;
+            if (k >= s_n[j]) continue;
+            const int page = list_of(a, t0 + j, h)[k];
+            if (page < 0 || page > a.at.positions[t0 + j] >> a.at.page_shift) record_error(a.err, SFFN_ERR_DEVICE);
+            else atomicOr(&s_set[page >> 5], 1u << (page & 31));
+        }
+        __syncthreads();
+        int n = 0;
+        for (int x = tid; x < words; x += 128) n += __popc(s_set[x]);
+        n = __reduce_add_sync(0xffffffffu, n);
+        if ((tid & 31) == 0) s_sum[tid >> 5] = n;
+        __syncthreads();
+        if (tid == 0) a.unions[(size_t)(t0 + i) * a.n_kv_heads + h] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+        __syncthreads();
+    }
+}
+
+template <int D>
+using TileCfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
+
+// A key tile's pages (16 at most) and, for each, the tokens of the run that have it.
+struct TilePages {
+    int page[16];  // -1: none
+    uint32_t tokens[16][4];
+};
+constexpr int kTileRing = 16;  // key tiles that the loading warp may be ahead of the last softmax warp, and more
+
+// Q: tokens of a row tile / 32, rounded up.
+template <int D, int Q>
+struct UnionPolicy {
+    static constexpr bool kReread = true;
+    const PagesArgs &a;
+    TilePages *ring;
+    int G, TB, box, ps;   // box: cache rows of one copy (a page's, 64 at most)
+    int piece, pieces;    // this CTA's next (row tile, key head), all of them
+    int t, t1, h, base;   // next token of the row tile, its end, key head; key tiles so far
+    // the loading warp's merge: of tokens lane + 32 q, the next page, the one after it, where that stands
+    int cur[Q], nxt[Q], at[Q], len[Q], mine[Q], left;
+    const int32_t *list[Q];
+
+    struct RowInfo {
+        int tok, page, off;  // token of the run; its own page and place in it
+    };
+
+    SFFN_DEV UnionPolicy(const PagesArgs &args, TilePages *r)
+        : a(args), ring(r), G(args.group), TB(128 / args.group), box(min(64, 1 << args.at.page_shift)), ps(1 << args.at.page_shift) {}
+
+    SFFN_DEV void start() {
+        piece = blockIdx.x;
+        pieces = (a.T + TB - 1) / TB * a.n_kv_heads;
+        t = t1 = base = 0;
+    }
+    // The last row tiles, whose contexts are the longest, first; forwards and backwards in turn.
+    SFFN_DEV bool next_tile() {
+        const int W = gridDim.x, round = piece / W, p = round & 1 ? 2 * round * W + W - 1 - piece : piece;
+        if (p >= pieces) return false;  // (true of the last round alone)
+        piece += W;
+        h = p % a.n_kv_heads;
+        t = (pieces / a.n_kv_heads - 1 - p / a.n_kv_heads) * TB;
+        t1 = min(a.T, t + TB);
+        return true;
+    }
+    SFFN_DEV int entry(int q, int k) const {  // a token's k-th page, past its end or out of range: none
+        if (k >= len[q]) return 0x7fffffff;
+        const int page = __ldg(list[q] + k);
+        return page < 0 || page > mine[q] ? -1 : page;
+    }
+    SFFN_DEV void advance(int q) {
+        do {
+            cur[q] = nxt[q];
+            nxt[q] = entry(q, ++at[q]);
+        } while (cur[q] < 0);
+    }
+    SFFN_DEV bool next(atc::Work &w) {
+        const int lane = threadIdx.x & 31;
+        for (;;) {
+            if (t >= t1 && !next_tile()) return false;
+            const uint32_t heads = __ballot_sync(0xffffffffu, t + lane < t1 && a.runs[t + lane] > 0);
+            if (!heads) {
+                t += 32;
+                continue;
+            }
+            t += __ffs(heads) - 1;
+            break;
+        }
+        const int n = a.runs[t];
+        left = a.unions[(size_t)t * a.n_kv_heads + h];
+        int last = 0, most = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int i = lane + 32 * q;
+            cur[q] = nxt[q] = 0x7fffffff;
+            len[q] = at[q] = 0;
+            if (i < n) {
+                const int pos = a.at.positions[t + i];
+                mine[q] = pos >> a.at.page_shift;
+                len[q] = a.n_sel[t + i];
+                list[q] = list_of(a, t + i, h);
+                nxt[q] = entry(q, 0);
+                last = max(last, pos);
+                most = max(most, len[q]);
+                advance(q);
+            }
+        }
+        w.h = h;
+        w.q_row = t;
+        w.nt = n;
+        w.k0 = 0;
+        w.k1 = __reduce_max_sync(0xffffffffu, most) * ps;  // (places of a token's own list: value_row)
+        w.ctx = __reduce_max_sync(0xffffffffu, last);
+        w.seq = a.at.seqs[t];
+        // (entries that are none of a table's pages are not counted: a run may have no page at all)
+        w.tiles = (int)max(1ll, ((long long)left * ps + atc::kKeys - 1) / atc::kKeys);
+        w.n[0] = (w.tiles + 1) / 2;
+        w.n[1] = w.tiles / 2;
+        w.mask_from[0] = w.mask_from[1] = 0;
+        w.whole = true;
+        w.base = base;
+        base += w.tiles;
+        t += n;
+        return true;
+    }
+    // The pages of key tile j, merged in order; returns the cache's page of this lane's box.
+    SFFN_DEV int place(const atc::Work &w, int j, int lane) {
+        TilePages &info = ring[(w.base + j) % kTileRing];
+        const int n = ps < atc::kKeys ? atc::kKeys / ps : 1;
+        __syncwarp();
+        if (ps > atc::kKeys && j % (ps / atc::kKeys) != 0) {  // the page goes on
+            const TilePages &old = ring[(w.base + j - 1) % kTileRing];
+            if (lane == 0) info.page[0] = old.page[0];
+            if (lane < 4) info.tokens[0][lane] = old.tokens[0][lane];
+        } else {
+            for (int x = 0; x < n; ++x) {
+                int page = cur[0];
+#pragma unroll
+                for (int q = 1; q < Q; ++q) page = min(page, cur[q]);
+                page = __reduce_min_sync(0xffffffffu, page);
+                if (left <= 0 || page == 0x7fffffff) page = -1;
+                --left;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const bool has = page >= 0 && cur[q] == page;
+                    const uint32_t b = __ballot_sync(0xffffffffu, has);
+                    if (lane == 0) info.tokens[x][q] = b;
+                    if (has) advance(q);
+                }
+                if (lane == 0) info.page[x] = page;
+            }
+        }
+        __syncwarp();
+        const int x = lane * box / ps;
+        if (lane * box >= atc::kKeys) return -1;
+        const int page = info.page[x];
+        if (page < 0) return -1;
+        const int pg = a.at.page_table[(size_t)w.seq * a.at.table_width + page];
+        if (pg >= 0 && pg < a.at.n_pages) return pg;
+        record_error(a.err, SFFN_ERR_DEVICE);
+        return a.at.n_pages;
+    }
+    SFFN_DEV void load_kv(const atc::Work &w, int j, int pg, const CUtensorMap *map, unsigned char *dst, uint64_t *bar,
+                          int lane, uint64_t pol) const {
+        constexpr int H = TileCfg<D>::kHalves;
+        const bool mine = lane * box < atc::kKeys && pg >= 0;  // (the boxes of a tile that has them are its first)
+        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * H));
+        __syncwarp();
+        if (mine) {
+            const int at_row = (j * atc::kKeys + lane * box) & (ps - 1);
+            const int group = ((pg * a.n_kv_heads + (pg < a.at.n_pages ? w.h : 0)) << (a.at.page_shift - 3)) + (at_row >> 3);
+            tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, group, bar, pol);
+        }
+    }
+    SFFN_DEV bool exists(const atc::Work &w, int j, int row) const {
+        const TilePages &info = ring[(w.base + j) % kTileRing];
+        const int page = info.page[ps < atc::kKeys ? row / ps : 0];
+        return page >= 0 && (long long)page * ps + ((j * atc::kKeys + row) & (ps - 1)) <= w.ctx;
+    }
+    SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
+        const int pos = a.at.positions[w.q_row + tok];
+        return RowInfo{tok, pos >> a.at.page_shift, pos & (ps - 1)};
+    }
+    SFFN_DEV void visible(const atc::Work &w, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
+        const TilePages &info = ring[(w.base + j) % kTileRing];
+        auto seen = [&](int x, int from) {  // keys of the tile's page x, from place `from` of the page on, that the row sees
+            const int page = info.page[x];
+            const bool has = (info.tokens[x][r.tok >> 5] >> (r.tok & 31)) & 1;
+            return !has ? 0 : (page == r.page ? max(0, r.off + 1 - from) : ps);
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t v = 0;
+            if (ps >= 32) {
+                v = atc::low_bits(seen(ps < atc::kKeys ? 32 * q / ps : 0, (j * atc::kKeys + 32 * q) & (ps - 1)));
+            } else {
+                for (int x = 0; x < 32 / ps; ++x)
+                    v |= (atc::low_bits(seen((32 * q) / ps + x, 0)) & atc::low_bits(ps)) << (x * ps);
+            }
+            vis[q] = v;
+        }
+    }
+    SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &r, int key) const {
+        const int tk = w.q_row + r.tok, k = key >> a.at.page_shift;
+        if (k >= a.n_sel[tk]) return nullptr;
+        const int page = list_of(a, tk, w.h)[k];
+        if (page < 0 || page > r.page || (page == r.page && (key & (ps - 1)) > r.off)) return nullptr;
+        const int pg = a.at.page_table[(size_t)w.seq * a.at.table_width + page];
+        if (pg < 0 || pg >= a.at.n_pages) return nullptr;
+        return static_cast<const uint16_t *>(a.cv) +
+               ((((size_t)pg * a.n_kv_heads + w.h) << a.at.page_shift) + (key & (ps - 1))) * D;
+    }
+    SFFN_DEV bool partial(const atc::Work &) const { return false; }
+    SFFN_DEV unsigned char *begin_row(const atc::Work &w, int tok, int head, bool valid, float, float l, float &inv) const {
+        inv = l == 0.f ? 0.f : 1.f / l;
+        if (!valid) return nullptr;
+        return reinterpret_cast<unsigned char *>(static_cast<uint16_t *>(a.out) +
+                                                 ((size_t)(w.q_row + tok) * a.n_heads + (size_t)w.h * G + head) * D);
+    }
+};
+
+template <int D, int Q>
+__global__ void __launch_bounds__(atc::kThreads, 1)
+    k_pages_union(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v, const PagesArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    __shared__ TilePages ring[kTileRing];
+    UnionPolicy<D, Q> policy(a, ring);
+    atc::attention_cta<TileCfg<D>, D>(policy, map_q, map_k, map_v, map_q, a.scale, a.group, a.err, smem_raw);
+}
+
+// ---------------------------------------------------------------------------
 // Join: `parts` blocks for each place between two ranges; those of all the places that cut an
 // item share its rows, a warp a row.
 // ---------------------------------------------------------------------------
@@ -330,15 +603,34 @@ cudaError_t launch_few(PagesArgs a, int grid, cudaStream_t s) {
     return e == cudaSuccess ? launch_join<__nv_bfloat16, D>(a, 2 * grid * few::kWarps, s) : e;
 }
 
+template <int D, int Q>
+cudaError_t launch_union(const PagesArgs &a, int grid, cudaStream_t s) {
+    const int G = a.group, TB = 128 / G, ps = 1 << a.at.page_shift;
+    const unsigned tiles = (unsigned)((a.T + TB - 1) / TB);
+    CUtensorMap mq, mk, mv;
+    const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, sq[2] = {D * 2, (uint64_t)a.q_stride * 2};
+    const uint64_t dk[4] = {64, 8, D / 64, (uint64_t)a.at.n_pages * a.n_kv_heads * ps / 8}, sk[3] = {D * 2, 128, D * 16};
+    const uint32_t bq[3] = {64, (uint32_t)G, (uint32_t)TB}, bk[4] = {64, 8, D / 64, (uint32_t)(ps < 64 ? ps : 64) / 8};
+    if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 4, dk, sk, bk) ||
+        !make_map_bf16(&mv, a.cv, 4, dk, sk, bk))
+        return cudaErrorNotSupported;
+    cudaError_t e = launch_k(k_pages_runs, dim3(tiles, (unsigned)a.n_kv_heads), dim3(128), 0, s, a, TB, D * 2);
+    if (e == cudaSuccess) e = set_max_smem((const void *)k_pages_union<D, Q>, TileCfg<D>::kSmem);
+    return e == cudaSuccess ? launch_k(k_pages_union<D, Q>, dim3(grid), dim3(atc::kThreads), TileCfg<D>::kSmem, s, mq, mk, mv, a) : e;
+}
+
 template <int D>
 cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
+    // Half a row tile of tokens, or more, of the mean sequence: their union.
+    if ((long long)a.T * a.group >= 64LL * a.at.n_seq && a.at.table_width <= kUnionWidth)
+        return a.group >= 4 ? launch_union<D, 1>(a, grid, s) : launch_union<D, 4>(a, grid, s);
     if (a.group <= 8) return launch_few<D, 1>(a, grid, s);
     return a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, few::max_rows(D) / 8>(a, grid, s);
 }
 
 }  // namespace
 
-PagesPlan make_pages_plan(int, int n_heads, int n_kv_heads, int head_dim) {
+PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim) {
     PagesPlan p = {};
     p.grid = device_sm_count();
     size_t o = align_up(kControlBytes);
@@ -350,6 +642,10 @@ PagesPlan make_pages_plan(int, int n_heads, int n_kv_heads, int head_dim) {
     const int G = n_heads / n_kv_heads, most = few::max_rows(head_dim);
     const size_t b = ranges * tree_slot_floats(G < most ? G : most, head_dim), f = p.grid * tree_slot_floats(G, head_dim);
     o = align_up(o + sizeof(float) * 2 * (b > f ? b : f));
+    p.off_runs = o;
+    o = align_up(o + sizeof(int32_t) * (size_t)T);
+    p.off_unions = o;
+    o = align_up(o + sizeof(int32_t) * (size_t)T * n_kv_heads);
     p.total = o;
     return p;
 }

@@ -150,6 +150,7 @@ struct PromptPolicy {
     struct RowInfo {
         int pos;  // the row's position
     };
+    SFFN_DEV bool exists(const atc::Work &w, int j, int row) const { return w.k0 + j * atc::kKeys + row < w.exist; }
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const { return RowInfo{w.i0 + tok}; }
     SFFN_DEV void visible(const atc::Work &, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
         const int n = r.pos + 1 - j * atc::kKeys;

@@ -403,6 +403,7 @@ struct SharedPolicy {
             tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, row >> 3, bar, pol);
         }
     }
+    SFFN_DEV bool exists(const atc::Work &w, int j, int row) const { return w.k0 + j * atc::kKeys + row < w.exist; }
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
         return RowInfo{w.kind == 2 ? 0 : token_mask(a, w.q_row + tok, w.tok0 + tok)};  // (of a prefix every key is seen)
     }

@@ -78,7 +78,7 @@ struct Work {
     int k0, k1;         // keys [k0, k1) (logical positions)
     int exist;          // keys below this one exist
     int i0;             // prompt: position of the first token
-    int base;           // prompt: row of key 0
+    int base;           // prompt: row of key 0; pages: key tiles of the items before
     int ctx;            // tree: committed positions
     int seq, tok0;      // tree: sequence, first token of the item within its new tokens
     bool whole;         // tree: the item's every key (else a partial result)
@@ -129,12 +129,13 @@ SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x008
 // Low 32 bits with the first n set (n clamped to 0 .. 32).
 SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
-// P: the policy (prompts, tree or shared prefixes).  It gives
+// P: the policy (prompts, tree, shared prefixes or chosen pages).  It gives
 //   start                  before the first item (every warp calls it)
 //   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
 //   place, load_kv         where a key tile lies, looked up a tile ahead; the load of its K or V
 //   row_info, visible      a row's own data; which keys of a masked tile it sees, as four words
+//   exists                 whether there is a key at a row of a masked tile
 //   value_row              a key's value row in memory (null: the row does not see the key)
 //   begin_row, partial     where a row's output goes; whether as fp32 partial result
 template <typename C, int D, typename P>
@@ -440,7 +441,6 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                         const int iv = k_at + 1, vs = iv % NS;
                         if (!wait(&kv_full[vs], (uint32_t)((iv / NS) & 1))) goto done;
                         uint4 *v = reinterpret_cast<uint4 *>(sm_kv + vs * C::kTile);
-                        const int kb = w.k0 + kt * kKeys;
 #pragma unroll 1
                         for (int i0 = quad * 32 + lane; i0 < C::kTile / 16; i0 += 512) {
                             uint4 x[4];
@@ -458,7 +458,7 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                                     const uint32_t b0 = nonfinite_bits(y.x), b1 = nonfinite_bits(y.y),
                                                    b2 = nonfinite_bits(y.z), b3 = nonfinite_bits(y.w);
                                     if (!(b0 | b1 | b2 | b3)) continue;
-                                    if (kb + C::row_of(i) < w.exist) {
+                                    if (policy.exists(w, kt, C::row_of(i))) {
                                         s_bad = 1;
                                         __threadfence_block();
                                     }

@@ -171,6 +171,7 @@ struct TreePolicy {
             tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, row >> 3, bar, pol);
         }
     }
+    SFFN_DEV bool exists(const atc::Work &w, int j, int row) const { return w.k0 + j * atc::kKeys + row < w.exist; }
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
         const int i = w.tok0 + tok;
         const uint64_t m = a.tree_mask ? a.tree_mask[w.q_row + tok] : (i == 63 ? ~0ull : (1ull << (i + 1)) - 1ull);

@@ -282,11 +282,12 @@ struct PagesArgs {
     int row_tile, tiles;  // rows of a row tile, row tiles of a key head's rows
     int4 *cuts;   // for each range: token, its item, first and last range of the item that its beginning cuts
     float *part;  // partial results of cut items
+    int32_t *runs, *unions;  // of a token that begins a run: the run's tokens; the pages of their union, per key head
     int32_t *err;
 };
 struct PagesPlan {
     int grid;
-    size_t off_cuts, off_part, total;
+    size_t off_cuts, off_part, off_runs, off_unions, total;
 };
 PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_pages(const PagesArgs &a, const PagesPlan &p, int dtype, int head_dim, cudaStream_t s);

@@ -282,6 +282,107 @@ def test_attn_pages(S, lens, at, hq, hkv, D, page, dt, keep):  # noqa: F811
     assert torch.equal(out, c.attend(S, sel, n_sel, workspace=ws))  # equal calls, equal bits
 
 
+MANY = [
+    # positions, tokens of each sequence (many of one: they share what they read), hq, hkv, D, page, keep
+    ([900, 700], [list(range(500, 640)), list(range(70))], 4, 4, 64, 8, 20),
+    ([5000], [list(range(4000, 4100))], 7, 1, 128, 128, 6),
+    ([6000], [list(range(5000, 5130))], 8, 2, 64, 512, 3),
+    ([900], [list(range(790, 900))], 40, 8, 128, 64, 5),
+    ([800, 300, 100], [list(range(700, 790)), [299], list(range(40, 100))], 16, 2, 64, 16, 11),
+    ([300, 77], [list(range(300)), list(range(77))], 28, 4, 128, 32, 4),
+    ([260], [[3 * i for i in range(80)]], 12, 12, 128, 16, 7),
+    ([40], [list(range(40))], 128, 2, 64, 8, 2),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,at,hq,hkv,D,page,keep", MANY)
+def test_attn_pages_many_tokens_of_a_sequence(S, lens, at, hq, hkv, D, page, keep):  # noqa: F811
+    c = Tokens(S, lens, at, hq, hkv, D, page, "bf16", sum(lens) + hq)
+    sel, n_sel = c.select(S, keep, 1 if keep > 1 else 0)
+    ws = S.alloc_attn_workspace(S.WS_ATTN_PAGES, len(c.pos), len(lens), hq, hkv, D)
+    out = c.attend(S, sel, n_sel, workspace=ws)
+    assert S.read_device_error(ws) == 0
+    c.check_attention(out, sel, n_sel)
+    assert torch.equal(out, c.attend(S, sel, n_sel, workspace=ws))  # equal calls, equal bits
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("hq,D", [(8, 128), (2, 64)])
+def test_attn_pages_many_tokens_padding_and_contract_errors(S, hq, D):  # noqa: F811
+    """Padding, tokens without pages, tokens and list entries out of range among many tokens of two sequences."""
+    c = Tokens(S, [400, 200], [list(range(250, 380)), list(range(100, 190))], hq, 2, D, 16, "bf16", 9)
+    sel, n_sel = c.select(S, 6)
+    T, pos, seqs, n = len(c.pos), list(c.pos), list(c.seqs), n_sel.tolist()
+    ws = S.alloc_attn_workspace(S.WS_ATTN_PAGES, T, 2, hq, 2, D)
+
+    def run(error, changed, n_new=n, lists=sel, zero=()):
+        out = torch.full((T, hq, D), 9.0, dtype=torch.bfloat16, device="cuda")
+        c.attend(S, lists, i32(n_new), out=out, workspace=ws)
+        assert S.read_device_error(ws) == error and S.read_device_error(ws) == 0
+        assert torch.isfinite(out.float()).all()
+        rows = [t for t in range(T) if t not in changed]
+        d = Tokens.__new__(Tokens)
+        d.__dict__.update(c.__dict__)
+        d.pos, d.seqs, d.q = [pos[t] for t in rows], [seqs[t] for t in rows], c.q[rows]
+        d.check_attention(out[rows], sel[rows], n_sel[rows])
+        return out
+
+    run(0, [])
+    c.pos = [-1 if t in (0, 7, 60, 61, 140, T - 1) else p for t, p in enumerate(pos)]
+    out = run(0, [0, 7, 60, 61, 140, T - 1])
+    assert (out[[0, 7, 60, 61, 140, T - 1]] == 9).all()
+    c.pos = list(pos)
+    out = run(0, [3, 4, 131, T - 1], [0 if t in (3, 4, 131, T - 1) else x for t, x in enumerate(n)])
+    assert not out[[3, 4, 131, T - 1]].any()
+    for what, bad in (("pos", 10 ** 7), ("seqs", 2), ("seqs", -1)):
+        c.pos, c.seqs = list(pos), list(seqs)
+        getattr(c, what)[50] = bad
+        assert (run(S.ERR_DEVICE, [50])[50] == 9).all()
+    c.pos, c.seqs = pos, seqs
+    assert (run(S.ERR_DEVICE, [33], [7 if t == 33 else x for t, x in enumerate(n)])[33] == 9).all()
+    for bad in (25, -1, 1 << 20, -(1 << 31)):  # list entries past the token's own page or outside the table
+        hurt = sel.clone()
+        hurt[20, 1, 0] = bad
+        run(S.ERR_DEVICE, [20], lists=hurt)
+    table = c.table.clone()
+    for bad in (c.cache.n_pages, -1):  # a page of the second sequence outside the cache: its tokens' rows
+        c.table[1, 5] = bad
+        run(S.ERR_DEVICE, list(range(130, T)))
+    c.table = table
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D,page", [(128, 32), (64, 16)])
+def test_attn_pages_many_tokens_unseen_places_have_no_influence(S, bad, D, page):  # noqa: F811
+    args = ([400], [list(range(200, 330))], 8, 2, D, page, "bf16", 6)
+    c = Tokens(S, *args, fill=0.0)
+    sel, n_sel = c.select(S, 3)
+    out = c.attend(S, sel, n_sel)
+    c.check_attention(out, sel, n_sel)
+    d = Tokens(S, *args, fill=bad)
+    assert torch.equal(d.attend(S, sel, n_sel), out)
+    # one position, as key and value or as value alone: only the tokens that see it show it
+    for j, key in ((101, True), (250, True), (77, False), (310, False)):
+        d = Tokens(S, *args, fill=0.0)
+        pg = int(d.table[0, j // page])
+        d.p.cv[pg, :, j % page] = bad
+        if key:
+            d.p.ck[pg, :, j % page] = bad
+        got = d.attend(S, sel, n_sel)
+        seen = 0
+        for t, p in enumerate(d.pos):
+            for h in range(2):
+                rows = slice(h * 4, h * 4 + 4)
+                if j <= p and j // page in sel[t, h, :n_sel[t]].tolist():
+                    seen += 1
+                    assert not torch.isfinite(got[t, rows].float()).any()
+                else:
+                    assert torch.equal(got[t, rows], out[t, rows]), (j, t, h)
+        assert 0 < seen < 2 * len(d.pos)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_attn_pages_lists_of_the_caller(S, dt):  # noqa: F811
