@@ -809,6 +809,8 @@ sffn_status sffn_attn_pages(const void *q, int64_t q_stride, int T, int n_heads,
     a.cuts = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + p.off_cuts);
     a.runs = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + p.off_runs);
     a.unions = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + p.off_unions);
+    a.bits = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + p.off_bits);
+    a.union_bits = a.bits + p.union_words;
     a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.off_part);
     st = run_attn_pages(a, p, cache->dtype, cache->head_dim, (cudaStream_t)stream);
     if (st == SFFN_OK) st = cuda_status(cudaGetLastError());

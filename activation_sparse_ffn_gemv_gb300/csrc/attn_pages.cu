@@ -276,21 +276,28 @@ __global__ void __launch_bounds__(few::kThreads, 2)
 // ---------------------------------------------------------------------------
 // bf16, many tokens of a sequence: attn_tc.cuh over the union of their pages
 //
-// A row tile has TB = 128 / G consecutive tokens; a run of them that are of one sequence is an item (for each key head).
-// Neighbouring tokens choose mostly the same pages, so the item reads the union of their pages once, and a row's mask leaves
-// out the pages that its token has not chosen: with 18 tokens of 48 of 480 pages each, about 90 pages are read where
-// the tokens one by one read 864.  k_pages_runs finds the runs and counts each union; the loading warp merges the (ascending)
-// lists as it goes, a lane a token, and leaves each key tile's pages and the tokens that have them in a small ring.
+// Two row tiles have 2 TB = 2 (128 / G) consecutive tokens; a run of them that are of one sequence is an item (for each key
+// head).  Neighbouring tokens choose mostly the same pages, so the item reads the union of their pages once, and a row's mask
+// leaves out the pages that its token has not chosen: with 36 tokens of 48 of 480 pages each, about 120 pages are read
+// where the tokens one by one read 1728.  k_pages_runs finds the runs and writes each token's pages, and each run's, as a bit
+// set; the loading warp goes through a run's set and leaves each key tile's pages and the tokens that have them
+// in a small ring.  That and the loads (64 KB a key tile) take the loading warp about 3000 cycles, and two row tiles' products
+// as long (one row tile an item: 160 us for pieces of 1045 tokens).
 // ---------------------------------------------------------------------------
 
-constexpr int kUnionWidth = 32768;  // pages of a table row that the count's bit set holds
+constexpr int kUnionWidth = 4096;               // pages of a table row that a bit set holds
+constexpr int kUnionWords = kUnionWidth / 32;
 
-__global__ void __launch_bounds__(128) k_pages_runs(const PagesArgs a, int tokens, int d_bytes) {
-    __shared__ uint32_t s_set[kUnionWidth / 32];
-    __shared__ int s_seq[128], s_n[128], s_run[128], s_sum[4];
+constexpr int kRunThreads = 256;  // tokens of two row tiles at the most
+
+__global__ void __launch_bounds__(kRunThreads) k_pages_runs(const PagesArgs a, int tokens, int row_bytes) {
+    constexpr int kWarps = kRunThreads / 32;
+    __shared__ uint32_t s_set[kUnionWords], s_row[kWarps][kUnionWords];
+    __shared__ int s_seq[kRunThreads], s_n[kRunThreads], s_run[kRunThreads], s_sum[kWarps];
     griddep_wait();
     griddep_launch_dependents();
     const int t0 = blockIdx.x * tokens, nt = min(tokens, a.T - t0), h = blockIdx.y, tid = threadIdx.x;
+    const int lane = tid & 31, warp = tid >> 5;
     if (tid < nt) {
         s_n[tid] = pages_of(a, t0 + tid, h == 0);
         s_seq[tid] = a.at.seqs[t0 + tid];
@@ -304,91 +311,125 @@ __global__ void __launch_bounds__(128) k_pages_runs(const PagesArgs a, int token
         if (h == 0) a.runs[t0 + tid] = len;
         if (s_n[tid] == 0) {  // a token without pages has zeros
             uint4 *row = reinterpret_cast<uint4 *>(static_cast<unsigned char *>(a.out) +
-                                                   ((size_t)(t0 + tid) * a.n_heads + (size_t)h * a.group) * d_bytes);
-            for (int e = 0; e < a.group * d_bytes / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
+                                                   ((size_t)(t0 + tid) * a.n_heads + (size_t)h * a.group) * row_bytes);
+            for (int e = 0; e < a.group * row_bytes / 16; ++e) row[e] = make_uint4(0, 0, 0, 0);
         }
     }
     __syncthreads();
-    const int words = (min(a.at.table_width, kUnionWidth) + 31) / 32;
+    const int words = (a.at.table_width + 31) / 32;
     for (int i = 0; i < nt; ++i) {
         const int len = s_run[i];
         if (len == 0) continue;
-        for (int x = tid; x < words; x += 128) s_set[x] = 0;
+        for (int x = tid; x < words; x += kRunThreads) s_set[x] = 0;
         __syncthreads();
-        for (int x = tid; x < len * a.n_keep; x += 128) {
-            const int j = i + x / a.n_keep, k = x % a.n_keep;
-            if (k >= s_n[j]) continue;
-            const int page = list_of(a, t0 + j, h)[k];
-            if (page < 0 || page > a.at.positions[t0 + j] >> a.at.page_shift) record_error(a.err, SFFN_ERR_DEVICE);
-            else atomicOr(&s_set[page >> 5], 1u << (page & 31));
+        for (int j = i + warp; j < i + len; j += kWarps) {  // a warp a token
+            uint32_t *row = s_row[warp];
+            for (int x = lane; x < words; x += 32) row[x] = 0;
+            __syncwarp();
+            const int32_t *list = list_of(a, t0 + j, h);
+            const int mine = a.at.positions[t0 + j] >> a.at.page_shift;
+            for (int k = lane; k < s_n[j]; k += 32) {
+                const int page = list[k];
+                if (page < 0 || page > mine) record_error(a.err, SFFN_ERR_DEVICE);
+                else atomicOr(&row[page >> 5], 1u << (page & 31));
+            }
+            __syncwarp();
+            uint32_t *dst = a.bits + ((size_t)(t0 + j) * a.n_kv_heads + h) * kUnionWords;
+            for (int x = lane; x < words; x += 32) {
+                dst[x] = row[x];
+                if (row[x]) atomicOr(&s_set[x], row[x]);
+            }
+            __syncwarp();
         }
         __syncthreads();
+        const size_t at = (size_t)(t0 + i) * a.n_kv_heads + h;
         int n = 0;
-        for (int x = tid; x < words; x += 128) n += __popc(s_set[x]);
+        for (int x = tid; x < words; x += kRunThreads) {
+            a.union_bits[at * kUnionWords + x] = s_set[x];
+            n += __popc(s_set[x]);
+        }
         n = __reduce_add_sync(0xffffffffu, n);
-        if ((tid & 31) == 0) s_sum[tid >> 5] = n;
+        if (lane == 0) s_sum[warp] = n;
         __syncthreads();
-        if (tid == 0) a.unions[(size_t)(t0 + i) * a.n_kv_heads + h] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+        if (tid == 0) {
+            int all = 0;
+            for (int x = 0; x < kWarps; ++x) all += s_sum[x];
+            a.unions[at] = all;
+        }
         __syncthreads();
     }
 }
 
 template <int D>
-using TileCfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
+using TileCfg = atc::Cfg<D, D == 128 ? 4 : 8, true, false, false>;
 
-// A key tile's pages (16 at most) and, for each, the tokens of the run that have it.
+// A key tile's pages (16 at most) and, for each token of the run, which of them it has.
 struct TilePages {
-    int page[16];  // -1: none
-    uint32_t tokens[16][4];
+    int page[16];            // -1: none
+    uint16_t has[kRunThreads];
+    int own;                 // whether a page may be some token's own, which it sees in part
 };
 constexpr int kTileRing = 16;  // key tiles that the loading warp may be ahead of the last softmax warp, and more
+struct UnionSmem {
+    TilePages ring[kTileRing];
+    uint16_t pages[1024];  // of a run, in order: 32 words of its bit set at a time
+};
 
-// Q: tokens of a row tile / 32, rounded up.
+// Q: tokens of two row tiles / 32, rounded up.
 template <int D, int Q>
 struct UnionPolicy {
     static constexpr bool kReread = true;
+    static constexpr bool kWordMasks = true;
     const PagesArgs &a;
     TilePages *ring;
+    uint16_t *pages;
     int G, TB, box, ps;   // box: cache rows of one copy (a page's, 64 at most)
-    int piece, pieces;    // this CTA's next (row tile, key head), all of them
-    int t, t1, h, base;   // next token of the row tile, its end, key head; key tiles so far
-    // the loading warp's merge: of tokens lane + 32 q, the next page, the one after it, where that stands
-    int cur[Q], nxt[Q], at[Q], len[Q], mine[Q], left;
-    const int32_t *list[Q];
+    int piece, pieces;    // this CTA's next (pair of row tiles, key head), all of them
+    int t, t1, h, base;   // next token of the row tiles, their end, key head; key tiles so far
+    // the loading warp's place in a run's bit set (words, the stretch of 32 that is listed, how many are listed, the next of
+    // them), and of tokens lane + 32 q the bit set's words `word` and the one after it
+    int words, stretch, listed, upto, word;
+    const uint32_t *set, *bits[Q];
+    uint32_t now[Q], after[Q], got[Q];  // (got: which of the tile's pages the tokens have)
+    bool has[2];  // whether this lane's box of the tile before the last one placed, and of that one, has a page
+    int loaded, boxes, group;  // the tile whose boxes are known, how many, where this lane's lies
 
     struct RowInfo {
         int tok, page, off;  // token of the run; its own page and place in it
     };
 
-    SFFN_DEV UnionPolicy(const PagesArgs &args, TilePages *r)
-        : a(args), ring(r), G(args.group), TB(128 / args.group), box(min(64, 1 << args.at.page_shift)), ps(1 << args.at.page_shift) {}
+    SFFN_DEV UnionPolicy(const PagesArgs &args, UnionSmem &sm)
+        : a(args), ring(sm.ring), pages(sm.pages), G(args.group), TB(128 / args.group), box(min(64, 1 << args.at.page_shift)), ps(1 << args.at.page_shift) {}
 
     SFFN_DEV void start() {
         piece = blockIdx.x;
-        pieces = (a.T + TB - 1) / TB * a.n_kv_heads;
+        pieces = (a.T + 2 * TB - 1) / (2 * TB) * a.n_kv_heads;
         t = t1 = base = 0;
+        loaded = -1;
     }
-    // The last row tiles, whose contexts are the longest, first; forwards and backwards in turn.
+    // The last tokens, whose contexts are the longest, first; forwards and backwards in turn.
     SFFN_DEV bool next_tile() {
         const int W = gridDim.x, round = piece / W, p = round & 1 ? 2 * round * W + W - 1 - piece : piece;
         if (p >= pieces) return false;  // (true of the last round alone)
         piece += W;
         h = p % a.n_kv_heads;
-        t = (pieces / a.n_kv_heads - 1 - p / a.n_kv_heads) * TB;
-        t1 = min(a.T, t + TB);
+        t = (pieces / a.n_kv_heads - 1 - p / a.n_kv_heads) * 2 * TB;
+        t1 = min(a.T, t + 2 * TB);
         return true;
     }
-    SFFN_DEV int entry(int q, int k) const {  // a token's k-th page, past its end or out of range: none
-        if (k >= len[q]) return 0x7fffffff;
-        const int page = __ldg(list[q] + k);
-        return page < 0 || page > mine[q] ? -1 : page;
-    }
-    SFFN_DEV void advance(int q) {
+    // Lists the next pages of the run's set.
+    SFFN_DEV void list_more(int lane) {
         do {
-            cur[q] = nxt[q];
-            nxt[q] = entry(q, ++at[q]);
-        } while (cur[q] < 0);
+            uint32_t v = ++stretch * 32 + lane < words ? __ldg(set + stretch * 32 + lane) : 0u;
+            const int n = __popc(v), end = warp_incl_scan(n, lane);
+            listed = __shfl_sync(0xffffffffu, end, 31);
+            __syncwarp();
+            for (int i = end - n; v; v &= v - 1) pages[i++] = (uint16_t)((stretch * 32 + lane) * 32 + __ffs(v) - 1);
+            __syncwarp();
+        } while (listed == 0 && (stretch + 1) * 32 < words);
+        upto = 0;
     }
+    SFFN_DEV uint32_t bits_of(int q, int x) const { return bits[q] && x < words ? __ldg(bits[q] + x) : 0u; }
     SFFN_DEV bool next(atc::Work &w) {
         const int lane = threadIdx.x & 31;
         for (;;) {
@@ -402,23 +443,25 @@ struct UnionPolicy {
             break;
         }
         const int n = a.runs[t];
-        left = a.unions[(size_t)t * a.n_kv_heads + h];
-        int last = 0, most = 0;
+        const size_t head = (size_t)t * a.n_kv_heads + h;
+        const int all = a.unions[head];
+        set = a.union_bits + head * kUnionWords;
+        words = (a.at.table_width + 31) / 32;
+        stretch = word = -1;
+        listed = upto = 0;
+        int last = 0, first = 0x7fffffff, most = 0;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int i = lane + 32 * q;
-            cur[q] = nxt[q] = 0x7fffffff;
-            len[q] = at[q] = 0;
+            bits[q] = nullptr;
             if (i < n) {
-                const int pos = a.at.positions[t + i];
-                mine[q] = pos >> a.at.page_shift;
-                len[q] = a.n_sel[t + i];
-                list[q] = list_of(a, t + i, h);
-                nxt[q] = entry(q, 0);
-                last = max(last, pos);
-                most = max(most, len[q]);
-                advance(q);
+                bits[q] = a.bits + (head + (size_t)i * a.n_kv_heads) * kUnionWords;
+                last = max(last, a.at.positions[t + i]);
+                first = min(first, a.at.positions[t + i]);
+                most = max(most, a.n_sel[t + i]);
             }
+            now[q] = 0;
+            after[q] = bits_of(q, 0);
         }
         w.h = h;
         w.q_row = t;
@@ -426,11 +469,12 @@ struct UnionPolicy {
         w.k0 = 0;
         w.k1 = __reduce_max_sync(0xffffffffu, most) * ps;  // (places of a token's own list: value_row)
         w.ctx = __reduce_max_sync(0xffffffffu, last);
+        w.i0 = __reduce_min_sync(0xffffffffu, first) >> a.at.page_shift;
         w.seq = a.at.seqs[t];
         // (entries that are none of a table's pages are not counted: a run may have no page at all)
-        w.tiles = (int)max(1ll, ((long long)left * ps + atc::kKeys - 1) / atc::kKeys);
-        w.n[0] = (w.tiles + 1) / 2;
-        w.n[1] = w.tiles / 2;
+        w.tiles = (int)max(1ll, ((long long)all * ps + atc::kKeys - 1) / atc::kKeys);
+        w.n[0] = w.tiles;
+        w.n[1] = n > TB ? w.tiles : 0;
         w.mask_from[0] = w.mask_from[1] = 0;
         w.whole = true;
         w.base = base;
@@ -438,59 +482,90 @@ struct UnionPolicy {
         t += n;
         return true;
     }
-    // The pages of key tile j, merged in order; returns the cache's page of this lane's box.
+    // The pages of key tile j, and who has them; the table's entry of this lane's box.  (The loading warp has about as long
+    // for a tile as its products take, 1600 cycles: four pages at a time, so that their chains of loads and
+    // votes overlap.)
     SFFN_DEV int place(const atc::Work &w, int j, int lane) {
         TilePages &info = ring[(w.base + j) % kTileRing];
-        const int n = ps < atc::kKeys ? atc::kKeys / ps : 1;
-        __syncwarp();
-        if (ps > atc::kKeys && j % (ps / atc::kKeys) != 0) {  // the page goes on
-            const TilePages &old = ring[(w.base + j - 1) % kTileRing];
-            if (lane == 0) info.page[0] = old.page[0];
-            if (lane < 4) info.tokens[0][lane] = old.tokens[0][lane];
+        const int n = ps < atc::kKeys ? atc::kKeys >> a.at.page_shift : 1;
+        int mine = -1;  // this lane's box's page
+        if (ps > atc::kKeys && (j * atc::kKeys & (ps - 1)) != 0) {  // the page goes on
+            mine = ring[(w.base + j - 1) % kTileRing].page[0];
+            if (lane == 0) info.page[0] = mine;
         } else {
-            for (int x = 0; x < n; ++x) {
-                int page = cur[0];
+            const int my_x = (lane * box) >> a.at.page_shift;
 #pragma unroll
-                for (int q = 1; q < Q; ++q) page = min(page, cur[q]);
-                page = __reduce_min_sync(0xffffffffu, page);
-                if (left <= 0 || page == 0x7fffffff) page = -1;
-                --left;
-#pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    const bool has = page >= 0 && cur[q] == page;
-                    const uint32_t b = __ballot_sync(0xffffffffu, has);
-                    if (lane == 0) info.tokens[x][q] = b;
-                    if (has) advance(q);
+            for (int q = 0; q < Q; ++q) got[q] = 0;
+            for (int x0 = 0; x0 < n; x0 += 4) {
+                if (upto + 4 > listed) {  // near the end of what is listed: one at a time
+                    for (int x = x0; x < min(n, x0 + 4); ++x) {
+                        if (upto >= listed && (stretch + 1) * 32 < words) list_more(lane);
+                        const int page = upto < listed ? pages[upto] : -1;
+                        ++upto;
+                        note(x, page);
+                        if (lane == 0) info.page[x] = page;
+                        if (x == my_x) mine = page;
+                    }
+                    continue;
                 }
-                if (lane == 0) info.page[x] = page;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if (x0 + x >= n) break;
+                    const int page = pages[upto + x];
+                    note(x0 + x, page);
+                    if (lane == 0) info.page[x0 + x] = page;
+                    if (x0 + x == my_x) mine = page;
+                }
+                upto += min(4, n - x0);
             }
         }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) info.has[lane + 32 * q] = (uint16_t)got[q];
+        // (pages ascend: a box that lies at or behind the first token's own page)
+        const int own = __any_sync(0xffffffffu, lane * box < atc::kKeys && mine >= w.i0);
+        if (lane == 0) info.own = own;
         __syncwarp();
-        const int x = lane * box / ps;
-        if (lane * box >= atc::kKeys) return -1;
-        const int page = info.page[x];
-        if (page < 0) return -1;
-        const int pg = a.at.page_table[(size_t)w.seq * a.at.table_width + page];
-        if (pg >= 0 && pg < a.at.n_pages) return pg;
-        record_error(a.err, SFFN_ERR_DEVICE);
-        return a.at.n_pages;
+        has[0] = has[1];
+        has[1] = lane * box < atc::kKeys && mine >= 0;
+        // the table's entry as it is: looked at when the tile is loaded, not before it has come
+        return has[1] ? a.at.page_table[(size_t)w.seq * a.at.table_width + mine] : 0;
+    }
+    SFFN_DEV void to_word(int x) {
+        const bool near = x == word + 1;
+        word = x;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            now[q] = near ? after[q] : bits_of(q, x);
+            after[q] = bits_of(q, x + 1);
+        }
+    }
+    SFFN_DEV void note(int x, int page) {  // page (-1: none) is the tile's x-th
+        if (page < 0) return;
+        if (page >> 5 != word) to_word(page >> 5);
+#pragma unroll
+        for (int q = 0; q < Q; ++q) got[q] |= ((now[q] >> (page & 31)) & 1) << x;
     }
     SFFN_DEV void load_kv(const atc::Work &w, int j, int pg, const CUtensorMap *map, unsigned char *dst, uint64_t *bar,
-                          int lane, uint64_t pol) const {
+                          int lane, uint64_t pol) {
         constexpr int H = TileCfg<D>::kHalves;
-        const bool mine = lane * box < atc::kKeys && pg >= 0;  // (the boxes of a tile that has them are its first)
-        const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(boxes * box * 128 * H));
-        __syncwarp();
-        if (mine) {
-            const int at_row = (j * atc::kKeys + lane * box) & (ps - 1);
-            const int group = ((pg * a.n_kv_heads + (pg < a.at.n_pages ? w.h : 0)) << (a.at.page_shift - 3)) + (at_row >> 3);
-            tc::tma_load_4d(dst + lane * box * 128 * H, map, 0, 0, 0, group, bar, pol);
+        if (loaded != w.base + j) {  // K; V of the tile follows
+            loaded = w.base + j;
+            // (the boxes of a tile that has them are its first; the next tile, if there is one, has been placed already)
+            const bool mine = j + 1 < w.tiles ? has[0] : has[1], there = pg >= 0 && pg < a.at.n_pages;
+            boxes = __popc(__ballot_sync(0xffffffffu, mine));
+            if (!there && mine) record_error(a.err, SFFN_ERR_DEVICE);
+            // 8-row group of the cache, past its end if there is no such page
+            group = (((there ? pg : a.at.n_pages) * a.n_kv_heads + (there ? w.h : 0)) << (a.at.page_shift - 3)) +
+                    (((j * atc::kKeys + lane * box) & (ps - 1)) >> 3);
         }
+        const uint32_t to = smem_u32(dst), at = smem_u32(bar);
+        few::expect_warp(at, (uint32_t)(boxes * box * 128 * H));
+        for (int b = 0; b < boxes; ++b)
+            few::load_warp(to + b * box * 128 * H, map, __shfl_sync(0xffffffffu, group, b), at, pol);
     }
     SFFN_DEV bool exists(const atc::Work &w, int j, int row) const {
         const TilePages &info = ring[(w.base + j) % kTileRing];
-        const int page = info.page[ps < atc::kKeys ? row / ps : 0];
+        const int page = info.page[row >> a.at.page_shift];
         return page >= 0 && (long long)page * ps + ((j * atc::kKeys + row) & (ps - 1)) <= w.ctx;
     }
     SFFN_DEV RowInfo row_info(const atc::Work &w, int tok) const {
@@ -499,21 +574,36 @@ struct UnionPolicy {
     }
     SFFN_DEV void visible(const atc::Work &w, const RowInfo &r, int j, uint32_t (&vis)[4]) const {
         const TilePages &info = ring[(w.base + j) % kTileRing];
-        auto seen = [&](int x, int from) {  // keys of the tile's page x, from place `from` of the page on, that the row sees
-            const int page = info.page[x];
-            const bool has = (info.tokens[x][r.tok >> 5] >> (r.tok & 31)) & 1;
-            return !has ? 0 : (page == r.page ? max(0, r.off + 1 - from) : ps);
-        };
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t v = 0;
+        const uint32_t has = info.has[r.tok];  // which of the tile's pages
+        if (!info.own) {  // all of a page or nothing
             if (ps >= 32) {
-                v = atc::low_bits(seen(ps < atc::kKeys ? 32 * q / ps : 0, (j * atc::kKeys + 32 * q) & (ps - 1)));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) vis[q] = 0u - ((has >> (32 * q >> a.at.page_shift)) & 1);
             } else {
-                for (int x = 0; x < 32 / ps; ++x)
-                    v |= (atc::low_bits(seen((32 * q) / ps + x, 0)) & atc::low_bits(ps)) << (x * ps);
+                const uint32_t one = atc::low_bits(ps);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    vis[q] = 0;
+                    for (int x = 0; x < 32 >> a.at.page_shift; ++x)
+                        vis[q] |= (0u - ((has >> ((32 * q >> a.at.page_shift) + x)) & 1) & one) << (x << a.at.page_shift);
+                }
             }
-            vis[q] = v;
+            return;
+        }
+        // keys of the tile's page x, from place `from` of the page on, that the row sees (32 or more: all)
+        auto seen = [&](int x, int from) {
+            return !((has >> x) & 1) ? 0 : (info.page[x] == r.page ? max(0, r.off + 1 - from) : 32);
+        };
+        if (ps >= 32) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) vis[q] = atc::low_bits(seen(32 * q >> a.at.page_shift, (j * atc::kKeys + 32 * q) & (ps - 1)));
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                vis[q] = 0;
+                for (int x = 0; x < 32 >> a.at.page_shift; ++x)
+                    vis[q] |= (atc::low_bits(seen((32 * q >> a.at.page_shift) + x, 0)) & atc::low_bits(ps)) << (x << a.at.page_shift);
+            }
         }
     }
     SFFN_DEV const void *value_row(const atc::Work &w, const RowInfo &r, int key) const {
@@ -540,8 +630,8 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
     k_pages_union(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const PagesArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    __shared__ TilePages ring[kTileRing];
-    UnionPolicy<D, Q> policy(a, ring);
+    __shared__ UnionSmem sm;
+    UnionPolicy<D, Q> policy(a, sm);
     atc::attention_cta<TileCfg<D>, D>(policy, map_q, map_k, map_v, map_q, a.scale, a.group, a.err, smem_raw);
 }
 
@@ -606,7 +696,7 @@ cudaError_t launch_few(PagesArgs a, int grid, cudaStream_t s) {
 template <int D, int Q>
 cudaError_t launch_union(const PagesArgs &a, int grid, cudaStream_t s) {
     const int G = a.group, TB = 128 / G, ps = 1 << a.at.page_shift;
-    const unsigned tiles = (unsigned)((a.T + TB - 1) / TB);
+    const unsigned tiles = (unsigned)((a.T + 2 * TB - 1) / (2 * TB));
     CUtensorMap mq, mk, mv;
     const uint64_t dq[3] = {D, (uint64_t)a.n_heads, (uint64_t)a.T}, sq[2] = {D * 2, (uint64_t)a.q_stride * 2};
     const uint64_t dk[4] = {64, 8, D / 64, (uint64_t)a.at.n_pages * a.n_kv_heads * ps / 8}, sk[3] = {D * 2, 128, D * 16};
@@ -614,7 +704,7 @@ cudaError_t launch_union(const PagesArgs &a, int grid, cudaStream_t s) {
     if (!make_map_bf16(&mq, a.q, 3, dq, sq, bq) || !make_map_bf16(&mk, a.ck, 4, dk, sk, bk) ||
         !make_map_bf16(&mv, a.cv, 4, dk, sk, bk))
         return cudaErrorNotSupported;
-    cudaError_t e = launch_k(k_pages_runs, dim3(tiles, (unsigned)a.n_kv_heads), dim3(128), 0, s, a, TB, D * 2);
+    cudaError_t e = launch_k(k_pages_runs, dim3(tiles, (unsigned)a.n_kv_heads), dim3(kRunThreads), 0, s, a, 2 * TB, D * 2);
     if (e == cudaSuccess) e = set_max_smem((const void *)k_pages_union<D, Q>, TileCfg<D>::kSmem);
     return e == cudaSuccess ? launch_k(k_pages_union<D, Q>, dim3(grid), dim3(atc::kThreads), TileCfg<D>::kSmem, s, mq, mk, mv, a) : e;
 }
@@ -623,7 +713,7 @@ template <int D>
 cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
     // Half a row tile of tokens, or more, of the mean sequence: their union.
     if ((long long)a.T * a.group >= 64LL * a.at.n_seq && a.at.table_width <= kUnionWidth)
-        return a.group >= 4 ? launch_union<D, 1>(a, grid, s) : launch_union<D, 4>(a, grid, s);
+        return a.group >= 4 ? launch_union<D, 2>(a, grid, s) : launch_union<D, 8>(a, grid, s);
     if (a.group <= 8) return launch_few<D, 1>(a, grid, s);
     return a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, few::max_rows(D) / 8>(a, grid, s);
 }
@@ -646,6 +736,9 @@ PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim) {
     o = align_up(o + sizeof(int32_t) * (size_t)T);
     p.off_unions = o;
     o = align_up(o + sizeof(int32_t) * (size_t)T * n_kv_heads);
+    p.off_bits = o;
+    p.union_words = (size_t)T * n_kv_heads * kUnionWords;
+    o = align_up(o + sizeof(uint32_t) * 2 * p.union_words);
     p.total = o;
     return p;
 }

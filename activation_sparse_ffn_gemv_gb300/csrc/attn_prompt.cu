@@ -29,6 +29,7 @@ using Cfg = atc::Cfg<D, D == 128 ? 4 : 8, false, false>;  // 224 KB and 192 KB o
 template <int D>
 struct PromptPolicy {
     static constexpr bool kReread = true;
+    static constexpr bool kWordMasks = false;
     const PromptArgs &a;
     int G, TB;
     // The walk's place: blocks [nxt, top] of the `cnt` sequences that have them; `before` pairs

@@ -334,6 +334,7 @@ using Cfg = atc::Cfg<D, (D == 128 ? 1 : 2) * (ONE ? 5 : 4), true, ONE, false>;
 template <int D, bool ONE>
 struct SharedPolicy {
     static constexpr bool kReread = true;
+    static constexpr bool kWordMasks = false;
     const SharedArgs &a;
     const Line &line;
     Walk walk;

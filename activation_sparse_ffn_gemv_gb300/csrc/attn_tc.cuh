@@ -77,7 +77,7 @@ struct Work {
     int mask_from[2];   // first key tile with masked keys
     int k0, k1;         // keys [k0, k1) (logical positions)
     int exist;          // keys below this one exist
-    int i0;             // prompt: position of the first token
+    int i0;             // prompt: position of the first token; pages: least own page of the tokens
     int base;           // prompt: row of key 0; pages: key tiles of the items before
     int ctx;            // tree: committed positions
     int seq, tok0;      // tree: sequence, first token of the item within its new tokens
@@ -126,11 +126,19 @@ SFFN_DEV uint32_t pack_bf16(float lo, float hi) {
 // The bf16 halves of w that are infinite or NaN (their sign bits), as a mask of 0x8000s.
 SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 
+// 0 * w + sum, of two bf16: NaN once a factor was infinite or NaN.
+SFFN_DEV uint32_t zero_times(uint32_t w, uint32_t sum) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(sum));
+    return r;
+}
+
 // Low 32 bits with the first n set (n clamped to 0 .. 32).
 SFFN_DEV uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); }
 
 // P: the policy (prompts, tree, shared prefixes or chosen pages).  It gives
 //   start                  before the first item (every warp calls it)
+//   kWordMasks             whether masks often cover 32 keys alike
 //   kReread                whether other CTAs read the same keys again (the L2 hint of the loads)
 //   bool next(Work &)      the CTA's items in turn (the loading warp alone)
 //   place, load_kv         where a key tile lies, looked up a tile ahead; the load of its K or V
@@ -444,14 +452,17 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
 #pragma unroll 1
                         for (int i0 = quad * 32 + lane; i0 < C::kTile / 16; i0 += 512) {
                             uint4 x[4];
-                            uint32_t any = 0;
+                            uint32_t any[4] = {0, 0, 0, 0};
 #pragma unroll
                             for (int u = 0; u < 4; ++u) x[u] = v[i0 + u * 128];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)
-                                any |= nonfinite_bits(x[u].x) | nonfinite_bits(x[u].y) | nonfinite_bits(x[u].z) |
-                                       nonfinite_bits(x[u].w);
-                            if (any) {
+                            for (int u = 0; u < 4; ++u) {  // zero times it is NaN (one instruction a pair)
+                                any[0] = zero_times(x[u].x, any[0]);
+                                any[1] = zero_times(x[u].y, any[1]);
+                                any[2] = zero_times(x[u].z, any[2]);
+                                any[3] = zero_times(x[u].w, any[3]);
+                            }
+                            if (nonfinite_bits(any[0]) | nonfinite_bits(any[1]) | nonfinite_bits(any[2]) | nonfinite_bits(any[3])) {
 #pragma unroll 1
                                 for (int i = i0; i < i0 + 512; i += 128) {
                                     uint4 y = v[i];
@@ -497,7 +508,11 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                     policy.visible(w, ri, kt, vis);
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        if (__any_sync(0xffffffffu, vis[q] != 0xffffffffu)) {
+                        if (P::kWordMasks && __all_sync(0xffffffffu, vis[q] == 0 || vis[q] == 0xffffffffu)) {
+                            const bool on = vis[q] != 0;  // one test for the word
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) s[q][i] = on ? s[q][i] : 0xff800000u;  // -inf
+                        } else if (__any_sync(0xffffffffu, vis[q] != 0xffffffffu)) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 s[q][i] = (vis[q] >> i) & 1u ? s[q][i] : 0xff800000u;  // -inf
@@ -515,9 +530,11 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
                 const bool up = (mnew - m) * c > kLazyLog2;
                 if (__any_sync(0xffffffffu, up)) {
                     const float alpha = up ? ex2((m - mnew) * c) : 1.f;
+                    // (a row that has seen nothing yet has an accumulator of zeros)
+                    const bool rescale = __any_sync(0xffffffffu, up && m != -INFINITY);
                     if (up) m = mnew;
                     l *= alpha;
-                    if (j > 0) {
+                    if (j > 0 && rescale) {
                         // the product of tile j - 1 is complete: it was issued before S_t(j)
 #pragma unroll 1
                         for (int q = 0; q < D / 16; ++q) {

@@ -95,6 +95,7 @@ using Cfg = atc::Cfg<D, D == 128 ? 5 : 10, true, true>;
 template <int D>
 struct TreePolicy {
     static constexpr bool kReread = false;
+    static constexpr bool kWordMasks = false;
     const TreeArgs &a;
     long long *pre;         // length of the line before each sequence (shared memory)
     long long u, u1;        // this CTA's next place on the line, and the end of its range

@@ -283,11 +283,13 @@ struct PagesArgs {
     int4 *cuts;   // for each range: token, its item, first and last range of the item that its beginning cuts
     float *part;  // partial results of cut items
     int32_t *runs, *unions;  // of a token that begins a run: the run's tokens; the pages of their union, per key head
+    uint32_t *bits, *union_bits;  // a token's and a run's pages as bit sets, per key head
     int32_t *err;
 };
 struct PagesPlan {
     int grid;
-    size_t off_cuts, off_part, off_runs, off_unions, total;
+    size_t off_cuts, off_part, off_runs, off_unions, off_bits, total;
+    size_t union_words;  // words of the tokens' bit sets
 };
 PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim);
 sffn_status run_attn_pages(const PagesArgs &a, const PagesPlan &p, int dtype, int head_dim, cudaStream_t s);
