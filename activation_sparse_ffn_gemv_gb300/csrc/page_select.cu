@@ -243,10 +243,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
                     (half ? y : x)[k] = v;
                 }
             }
+            float *dst = a.scores + ((size_t)t0 * a.n_kv_heads + h) * a.at.table_width + pb + g;
+            const int step = a.n_kv_heads * a.at.table_width;  // (64 tokens of it at most: below 2^31)
             auto put = [&](int i, int half, float v) {  // token i of the tile
                 const int page = pb + g + 8 * half;
-                if (i >= r0 && i < r1 && page <= s_last[i] && page < end)
-                    a.scores[((size_t)(t0 + i) * a.n_kv_heads + h) * a.at.table_width + page] = v;
+                if (i >= r0 && i < r1 && page <= s_last[i] && page < end) dst[i * step + 8 * half] = v;
             };
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             const int n0 = r0 * rows / 8, n1 = (r1 * rows + 7) / 8;
@@ -264,6 +265,40 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
                     for (int j = 0; j < NB; ++j) mma_16x8x16(d[j], x[k].x, y[k].x, x[k].y, y[k].y, z[j].x, z[j].y);
 #pragma unroll
                     for (int j = 0; j < NB; ++j) mma_16x8x16(d[j], x[k].z, y[k].z, x[k].w, y[k].w, z[j].z, z[j].w);
+                }
+                if constexpr (NB == 4) {
+                    // Tokens of 8 or 4 rows: the four lanes of a page share the maxima of the four products out among
+                    // them (each sends what another keeps), so that every lane writes.
+                    auto best = [&](int half, float (&u)[4]) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) u[j] = fmaxf(d[j][2 * half], d[j][2 * half + 1]);
+                        // lane c keeps products j of its own parity
+#pragma unroll
+                        for (int j = 0; j < 4; j += 2) {
+                            const float other = __shfl_xor_sync(0xffffffffu, c & 1 ? u[j] : u[j + 1], 1);
+                            u[j / 2] = fmaxf(c & 1 ? u[j + 1] : u[j], other);
+                        }
+                    };
+                    if (rows == 8) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float u[4];
+                            best(half, u);
+                            const float other = __shfl_xor_sync(0xffffffffu, c & 2 ? u[0] : u[1], 2);
+                            put(nb + c, half, fmaxf(c & 2 ? u[1] : u[0], other));  // product c: its parity, and its half
+                        }
+                        continue;
+                    }
+                    if (rows == 4) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float u[4];
+                            best(half, u);
+                            put((nb + (c & 1)) * 2 + (c >> 1), half, u[0]);
+                            put((nb + 2 + (c & 1)) * 2 + (c >> 1), half, u[1]);
+                        }
+                        continue;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
@@ -440,7 +475,7 @@ cudaError_t launch_select(const SelectPagesArgs &a, cudaStream_t s) {
     const unsigned lists = (unsigned)a.T * (unsigned)a.n_kv_heads;
     if (width <= 1024) {  // a warp a list where there are enough of them
         if (lists >= 16u * (unsigned)device_sm_count())
-            return launch_k(k_page_choose<1, 32>, dim3((lists + 3) / 4), dim3(128), 0, s, a);
+            return launch_k(width <= 512 ? k_page_choose<1, 16> : k_page_choose<1, 32>, dim3((lists + 3) / 4), dim3(128), 0, s, a);
         return launch_k(k_page_choose<8, 4>, dim3(lists), dim3(256), 0, s, a);
     }
     if (width <= 4096) return launch_k(k_page_choose<16, 8>, dim3(lists), dim3(512), 0, s, a);
