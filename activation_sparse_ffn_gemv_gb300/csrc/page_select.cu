@@ -62,8 +62,56 @@ SFFN_DEV void load8(const float *p, float (&f)[8]) {
 
 constexpr int kBoundsWarps = 4;
 
+// Largest and least of eight columns, NaN once one is: bf16 stays packed (half the registers, a quarter of the instructions).
+template <typename T>
+struct Extremes;
+
+template <>
+struct Extremes<float> {
+    float hi[8], lo[8];
+    SFFN_DEV void clear() {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
+    }
+    SFFN_DEV void add(const float *p) {
+        float x[8];
+        load8(p, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) hi[e] = max_nan(hi[e], x[e]), lo[e] = min_nan(lo[e], x[e]);
+    }
+    SFFN_DEV void get(float (&h)[8], float (&l)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = hi[e], l[e] = lo[e];
+    }
+};
+
+template <>
+struct Extremes<__nv_bfloat16> {
+    uint32_t hi[4], lo[4];
+    SFFN_DEV void clear() {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) hi[e] = 0xff80ff80u, lo[e] = 0x7f807f80u;
+    }
+    SFFN_DEV void add(const __nv_bfloat16 *p) {
+        const uint4 u = ldg_stream(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi[e]) : "r"(w[e]));
+            asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo[e]) : "r"(w[e]));
+        }
+    }
+    SFFN_DEV void get(float (&h)[8], float (&l)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[2 * e] = bf16lo(hi[e]), h[2 * e + 1] = bf16hi(hi[e]);
+            l[2 * e] = bf16lo(lo[e]), l[2 * e + 1] = bf16hi(lo[e]);
+        }
+    }
+};
+
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kBoundsWarps) k_page_bounds(const BoundsArgs a) {
+__global__ void __launch_bounds__(32 * kBoundsWarps, sizeof(T) == 2 ? 16 : 10) k_page_bounds(const BoundsArgs a) {
     constexpr int LPK = D / 8, KPW = 32 / LPK;  // lanes of a key, keys of a warp at a time
     griddep_wait();
     griddep_launch_dependents();
@@ -77,16 +125,12 @@ __global__ void __launch_bounds__(32 * kBoundsWarps) k_page_bounds(const BoundsA
     }
     const int ps = 1 << a.page_shift, col = (lane % LPK) * 8;
     const T *k = static_cast<const T *>(a.ck) + ((((size_t)pg * a.n_kv_heads + h) << a.page_shift) + lane / LPK) * D + col;
-    float hi[8], lo[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) hi[e] = -INFINITY, lo[e] = INFINITY;
+    Extremes<T> x;
+    x.clear();
 #pragma unroll 4
-    for (int j = 0; j < ps; j += KPW) {
-        float x[8];
-        load8(k + (size_t)j * D, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) hi[e] = max_nan(hi[e], x[e]), lo[e] = min_nan(lo[e], x[e]);
-    }
+    for (int j = 0; j < ps; j += KPW) x.add(k + (size_t)j * D);
+    float hi[8], lo[8];
+    x.get(hi, lo);
     float most = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -158,9 +202,10 @@ SFFN_DEV void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, 
 }
 
 // tile: tokens of a CTA (tile * rows <= kScoreRows, or one token); rows: of a token, 1, 2, 4 or a multiple of 8;
-// stretch: pages of a CTA; NB: products of 8 rows at a time (several chains of sums for the tensor cores to work on).
-template <typename T, int D, int NB>
+// stretch: pages of a CTA.
+template <typename T, int D>
 __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPagesArgs a, int tile, int rows, int stretch) {
+    constexpr int NB = 4;                // products of 8 rows at a time (chains of sums for the tensor cores to work on)
     constexpr int kStride = 2 * D + 32;  // elements of a row (64 bytes apart mod 128: no bank conflicts)
     constexpr int KB = 2 * D / 32;       // blocks of 32 columns
     __shared__ __align__(16) __nv_bfloat16 s_code[kScoreRows][kStride];
@@ -179,17 +224,6 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
     bool any = false;
     for (int i = 0; i < nt; ++i) any |= s_last[i] >= p0;
     if (!any) return;
-    if (NB == 1) {  // a token alone: the first pages' bounds come to L2 while its codes are made
-        const int page = p0 + warp * 16 + (lane & 15);
-        if (page <= s_last[0] && page < p0 + stretch) {
-            const int pg = a.at.page_table[(size_t)s_seq[0] * a.at.table_width + page];
-            if (pg >= 0 && pg < a.at.n_pages) {
-                const char *b = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.bounds) +
-                                                               ((size_t)pg * a.n_kv_heads + h) * 2 * D);
-                for (int i = (lane >> 4) * 128; i < 4 * D; i += 256) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + i));
-            }
-        }
-    }
     // codes: a warp a token
     for (int i = warp; i < nt; i += kScoreWarps) {
         const T *q = static_cast<const T *>(a.q) + (size_t)(t0 + i) * a.q_stride + (size_t)h * a.group * D;
@@ -266,39 +300,37 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
 #pragma unroll
                     for (int j = 0; j < NB; ++j) mma_16x8x16(d[j], x[k].z, y[k].z, x[k].w, y[k].w, z[j].z, z[j].w);
                 }
-                if constexpr (NB == 4) {
-                    // Tokens of 8 or 4 rows: the four lanes of a page share the maxima of the four products out among
-                    // them (each sends what another keeps), so that every lane writes.
-                    auto best = [&](int half, float (&u)[4]) {
+                // Tokens of 8 or 4 rows: the four lanes of a page share the maxima of the four products out among
+                // them (each sends what another keeps), so that every lane writes.
+                auto best = [&](int half, float (&u)[4]) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) u[j] = fmaxf(d[j][2 * half], d[j][2 * half + 1]);
-                        // lane c keeps products j of its own parity
+                    for (int j = 0; j < 4; ++j) u[j] = fmaxf(d[j][2 * half], d[j][2 * half + 1]);
+                    // lane c keeps products j of its own parity
 #pragma unroll
-                        for (int j = 0; j < 4; j += 2) {
-                            const float other = __shfl_xor_sync(0xffffffffu, c & 1 ? u[j] : u[j + 1], 1);
-                            u[j / 2] = fmaxf(c & 1 ? u[j + 1] : u[j], other);
-                        }
-                    };
-                    if (rows == 8) {
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float u[4];
-                            best(half, u);
-                            const float other = __shfl_xor_sync(0xffffffffu, c & 2 ? u[0] : u[1], 2);
-                            put(nb + c, half, fmaxf(c & 2 ? u[1] : u[0], other));  // product c: its parity, and its half
-                        }
-                        continue;
+                    for (int j = 0; j < 4; j += 2) {
+                        const float other = __shfl_xor_sync(0xffffffffu, c & 1 ? u[j] : u[j + 1], 1);
+                        u[j / 2] = fmaxf(c & 1 ? u[j + 1] : u[j], other);
                     }
-                    if (rows == 4) {
+                };
+                if (rows == 8) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            float u[4];
-                            best(half, u);
-                            put((nb + (c & 1)) * 2 + (c >> 1), half, u[0]);
-                            put((nb + 2 + (c & 1)) * 2 + (c >> 1), half, u[1]);
-                        }
-                        continue;
+                    for (int half = 0; half < 2; ++half) {
+                        float u[4];
+                        best(half, u);
+                        const float other = __shfl_xor_sync(0xffffffffu, c & 2 ? u[0] : u[1], 2);
+                        put(nb + c, half, fmaxf(c & 2 ? u[1] : u[0], other));  // product c: its parity, and its half
                     }
+                    continue;
+                }
+                if (rows == 4) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float u[4];
+                        best(half, u);
+                        put((nb + (c & 1)) * 2 + (c >> 1), half, u[0]);
+                        put((nb + 2 + (c & 1)) * 2 + (c >> 1), half, u[1]);
+                    }
+                    continue;
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
@@ -331,6 +363,79 @@ __global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores(const SelectPa
                 }
             }
         }
+    }
+}
+
+// One token and a group of at most 8 heads: a warp makes the codes that its lanes need in registers (row g, columns 8 c and
+// on of each 32, for both bounds), while its pages' bounds are on their way; no warp waits for another.
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kScoreWarps) k_page_scores_one(const SelectPagesArgs a, int stretch) {
+    constexpr int KB = D / 32;  // blocks of 32 columns of a bound
+    griddep_wait();
+    griddep_launch_dependents();
+    const int t = blockIdx.x, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int p0 = blockIdx.y * stretch + warp * 16;
+    float q[KB][8];
+    const T *src = static_cast<const T *>(a.q) + (size_t)t * a.q_stride + ((size_t)h * a.group + min(g, a.group - 1)) * D + c * 8;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) load8(src + k * 32, q[k]);
+    const Token tok = token_of(a.at, t, nullptr);
+    const int last = tok.mine + 1 <= a.n_keep ? -1 : tok.mine - a.n_recent;  // with fewer pages all are taken
+    const int end = min((int)(blockIdx.y + 1) * stretch, last + 1);
+    if (p0 >= end) return;
+    const int32_t *table = a.at.page_table + (size_t)tok.seq * a.at.table_width;
+    uint4 x[2 * KB], y[2 * KB];  // the bounds of pages pb + g and pb + g + 8
+    auto load = [&](int pb) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int page = pb + g + 8 * half, pg = page < end ? table[page] : -1;
+            const bool there = pg >= 0 && pg < a.at.n_pages;
+            if (!there && c == 0 && page < end) record_error(a.err, SFFN_ERR_DEVICE);
+            const __nv_bfloat16 *b = static_cast<const __nv_bfloat16 *>(a.bounds) +
+                                     ((size_t)(there ? pg : 0) * a.n_kv_heads + h) * 2 * D + c * 8;
+#pragma unroll
+            for (int k = 0; k < 2 * KB; ++k) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (there) v = ldg_stream(b + k * 32);
+                (half ? y : x)[k] = v;
+            }
+        }
+    };
+    load(p0);
+    float most = 0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[k][e] = within(q[k][e], 0.f), most = fmaxf(most, fabsf(q[k][e]));
+    const float inv = pow2(-step_exponent(warp_max(most)));
+    uint32_t z[2 * KB][4];  // codes against the upper bounds, then the lower
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float u = rintf(q[k][2 * e] * inv), v = rintf(q[k][2 * e + 1] * inv);
+            __nv_bfloat162 up = __floats2bfloat162_rn(fmaxf(u, 0.f), fmaxf(v, 0.f)), dn = __floats2bfloat162_rn(fminf(u, 0.f), fminf(v, 0.f));
+            z[k][e] = *reinterpret_cast<uint32_t *>(&up);
+            z[KB + k][e] = *reinterpret_cast<uint32_t *>(&dn);
+        }
+    float *dst = a.scores + ((size_t)t * a.n_kv_heads + h) * a.at.table_width + g;
+    for (int pb = p0; pb < end; pb += kScorePages) {
+        if (pb != p0) load(pb);
+        float d[2][4] = {};
+#pragma unroll
+        for (int k = 0; k < 2 * KB; ++k) {
+            mma_16x8x16(d[0], x[k].x, y[k].x, x[k].y, y[k].y, z[k][0], z[k][1]);
+            mma_16x8x16(d[1], x[k].z, y[k].z, x[k].w, y[k].w, z[k][2], z[k][3]);
+        }
+        // (the sum of two exact sums is exact, too)
+        float u = fmaxf(d[0][0] + d[1][0], d[0][1] + d[1][1]), v = fmaxf(d[0][2] + d[1][2], d[0][3] + d[1][3]);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        }
+        if (c == 0 && pb + g < end) dst[pb] = u;
+        if (c == 1 && pb + g + 8 < end) dst[pb + 8] = v;
     }
 }
 
@@ -459,18 +564,17 @@ cudaError_t launch_select(const SelectPagesArgs &a, cudaStream_t s) {
     int rows = G > 4 ? (G + 7) / 8 * 8 : (G > 2 ? 4 : G);
     int tile = 1;  // as many tokens as a sequence has in the mean, as far as their rows go
     while (2 * tile * rows <= kScoreRows && 2 * tile * a.at.n_seq <= a.T) tile *= 2;
-    if (tile == 1 && rows < 8) rows = 8;  // (a token alone: whole products)
+    const bool alone = tile == 1 && G <= 8;
     // Stretches of pages so that every SM has several CTAs: many where a token is alone (its sequence may be short, and
     // most of them empty), fewer where the codes of many tokens are made for each.
-    const long long tiles = ((long long)a.T + tile - 1) / tile * a.n_kv_heads, fill = (tile == 1 ? 24LL : 4LL) * device_sm_count();
+    const long long tiles = ((long long)a.T + tile - 1) / tile * a.n_kv_heads, fill = (tile == 1 ? 24LL : 2LL) * device_sm_count();
     long long cut = (fill + tiles - 1) / tiles;
     const int most = (width + kScorePages - 1) / kScorePages;
     if (cut > most) cut = most;
     const int stretch = (most + (int)cut - 1) / (int)cut * kScorePages;
     const dim3 grid((unsigned)((a.T + tile - 1) / tile), (unsigned)((width + stretch - 1) / stretch), (unsigned)a.n_kv_heads);
-    cudaError_t e = tile * rows <= 8
-                        ? launch_k(k_page_scores<T, D, 1>, grid, dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch)
-                        : launch_k(k_page_scores<T, D, 4>, grid, dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch);
+    cudaError_t e = alone ? launch_k(k_page_scores_one<T, D>, grid, dim3(32 * kScoreWarps), 0, s, a, stretch)
+                          : launch_k(k_page_scores<T, D>, grid, dim3(32 * kScoreWarps), 0, s, a, tile, rows, stretch);
     if (e != cudaSuccess) return e;
     const unsigned lists = (unsigned)a.T * (unsigned)a.n_kv_heads;
     if (width <= 1024) {  // a warp a list where there are enough of them
