@@ -397,5 +397,242 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
     for (int i = landed; i < issued; ++i) mbar_wait(&full[warp][i % NS], (uint32_t)((i / NS) & 1));
 }
 
+// ---------------------------------------------------------------------------
+// fp32, on the CUDA cores: the same walk and ring, tiles of 8 keys (one bulk copy each of K and V: 8 rows of a page lie
+// together).  Scores: eight lanes a key, D / 8 columns of every row each, then the lanes share the rows out
+// among them; values: a lane has D / 32 columns of every row, the weights through shared memory.  Every product and
+// sum is fp32.  Bound: HBM for a row or two, the
+// multiply-adds (64 a key and lane for 8 rows of 128) beyond.  24 tokens of 1344 positions, 32/32 heads of 128: 67 us, 3.3 TB/s
+// (attn_rows.cuh, whose tiles have 64 rows: 575).
+// ---------------------------------------------------------------------------
+
+template <int D>
+struct Cfg32 {
+    static constexpr int kKeys = 8;
+    static constexpr int kTile = kKeys * D * 4;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kSmem = kWarps * kStages * 2 * kTile;
+};
+
+// R: rows of a tile at most: 1, 2, 4 or 8.  ck, cv: the cache.
+template <int D, int R, typename P>
+SFFN_DEV void attention_f32(P &policy, const void *ck, const void *cv, int page_shift, int n_pages, int n_kv_heads, float scale,
+                            int32_t *err, unsigned char *smem_raw) {
+    using C = Cfg32<D>;
+    constexpr int NS = C::kStages, KB = D / 32, K = C::kKeys, V = D / 32;
+    __shared__ uint64_t full[kWarps][NS];
+    __shared__ __align__(16) float s_p[kWarps][K][R < 4 ? 4 : R];
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, kg = lane >> 3, sub = lane & 7;
+    unsigned char *ring = smem_raw + warp * NS * 2 * C::kTile;
+    if (tid == 0) {
+        for (int w = 0; w < kWarps; ++w)
+            for (int i = 0; i < NS; ++i) mbar_init(&full[w][i], 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+
+    // ---- loads, as in attention() ----
+    P ahead = policy;
+    const uint64_t keep = l2_evict_first_policy();
+    Work lw, nw;
+    int li = 0, ln = 0, issued = 0, islot = 0, nn, page = 0, npage = 0;
+    bool dead = false;
+    auto tiles_of = [&](const Work &w) { return (w.k1 - w.k0 + K - 1) / K; };
+    auto look_up = [&](const Work &w, int i, int &pg) {
+        const int key = w.k0 + (i + lane) * K;
+        if (key < w.k1) pg = ahead.page_of(w, key);
+    };
+    auto fetch = [&]() {
+        nn = ahead.next(nw) ? tiles_of(nw) : -1;
+        if (nn > 0) look_up(nw, 0, npage);
+    };
+    fetch();
+    auto issue = [&]() {
+        while (li == ln && nn >= 0) {
+            lw = nw, li = 0, ln = nn, page = npage;
+            fetch();
+        }
+        if (li == ln || dead) return;
+        if ((li & 31) == 0 && li > 0) look_up(lw, li, page);
+        const int pg = __shfl_sync(0xffffffffu, page, li & 31), key = lw.k0 + li * K;
+        unsigned char *dst = ring + islot * 2 * C::kTile;
+        if (pg < n_pages) {
+            const size_t at = ((((size_t)pg * n_kv_heads + lw.h) << page_shift) + (key & ((1 << page_shift) - 1))) * (D * 4);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[warp][islot], 2 * C::kTile);
+                bulk_load(dst, static_cast<const char *>(ck) + at, C::kTile, &full[warp][islot], keep);
+                bulk_load(dst + C::kTile, static_cast<const char *>(cv) + at, C::kTile, &full[warp][islot], keep);
+            }
+        } else {  // no page of the cache: zeros
+            for (int i = lane; i < 2 * C::kTile / 16; i += 32) reinterpret_cast<uint4 *>(dst)[i] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();  // (before a later copy into the slot)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[warp][islot]);
+        }
+        ++li;
+        ++issued;
+        if (++islot == NS) islot = 0;
+    };
+    for (int i = 0; i < NS; ++i) issue();
+
+    const float cf = scale * 1.44269504088896341f;
+    int landed = 0, slot = 0;
+    uint32_t par = 0;
+    float4 q[R][KB];
+    auto load_q = [&](const Work &w) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float4 *src = reinterpret_cast<const float4 *>(policy.query(w, w.r0 + min(r, w.rows - 1)));
+#pragma unroll
+            for (int k = 0; k < KB; ++k) q[r][k] = __ldg(src + k * 8 + sub);
+        }
+    };
+    const int my = sub & (R - 1);  // the row whose scores this lane has
+    Work w, w2;
+    bool have = policy.next(w);
+    if (have) load_q(w);
+    for (; have; w = w2) {
+        float o[R][V], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int x = 0; x < V; ++x) o[r][x] = 0.f;
+        const int tiles = tiles_of(w);
+        for (int i = 0; i < tiles; ++i) {
+            const int kb = w.k0 + i * K;
+            if (!dead) {
+                bool came = __all_sync(0xffffffffu, mbar_try_wait(&full[warp][slot], par));
+                if (!came) {
+                    const uint64_t t0 = globaltimer_ns();
+                    while (!came && !__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs))
+                        came = __all_sync(0xffffffffu, mbar_try_wait_for(&full[warp][slot], par, kHoldNs));
+                }
+                if (came) {
+                    ++landed;
+                } else {
+                    dead = true;
+                    if (lane == 0) record_error(err, SFFN_ERR_TIMEOUT);
+                }
+            }
+            const float4 *kt = reinterpret_cast<const float4 *>(ring + slot * 2 * C::kTile);
+            const float *vt = reinterpret_cast<const float *>(ring + slot * 2 * C::kTile + C::kTile) + lane * V;
+            if (++slot == NS) slot = 0, par ^= 1;
+            float s[2];
+            const bool masked = kb + K > w.all;
+            bool seen[2] = {true, true};
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {  // key 4 j + kg
+                float a[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) a[r] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    const float4 x = kt[(4 * j + kg) * (D / 4) + k * 8 + sub];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) a[r] += x.x * q[r][k].x + x.y * q[r][k].y + x.z * q[r][k].z + x.w * q[r][k].w;
+                }
+                // sums over the eight lanes, lane `sub` ending with row sub % R: while there are several rows the lanes of
+                // a pair keep half of them each
+#pragma unroll
+                for (int f = 4, n = R; f > 0; f >>= 1) {
+                    if (n > f) {
+                        n >>= 1;
+#pragma unroll
+                        for (int r = 0; r < R / 2; ++r)
+                            if (r < n) {
+                                const bool up = sub & f;
+                                const float other = __shfl_xor_sync(0xffffffffu, up ? a[r] : a[r + n], f);
+                                a[r] = (up ? a[r + n] : a[r]) + other;
+                            }
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < R; ++r)
+                            if (r < n) a[r] += __shfl_xor_sync(0xffffffffu, a[r], f);
+                    }
+                }
+                s[j] = a[0];
+                if (masked) {
+                    const int key = kb + 4 * j + kg;
+                    seen[j] = key < w.k1 && (key < w.all || (my < w.rows && policy.sees(w, w.r0 + my, key)));
+                    if (!seen[j]) s[j] = -INFINITY;
+                }
+            }
+            float x = fmaxf(s[0], s[1]);
+            const bool up = (x - m) * cf > kLazyLog2;
+            if (__any_sync(0xffffffffu, up)) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                float f = 1.f;
+                if ((x - m) * cf > kLazyLog2) {
+                    f = ex2((m - x) * cf);
+                    m = x;
+                    l *= f;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float fr = __shfl_sync(0xffffffffu, f, r);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[r][e] *= fr;
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float p = ex2((s[j] - ref) * cf);
+                l += p;
+                // -1: a key that the row does not see, whose value is left out
+                if (sub < R) s_p[warp][4 * j + kg][my] = seen[j] ? p : -1.f;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int key = 0; key < K; ++key) {
+                float v[V], p[R];
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(vt + key * D);
+                    v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(vt + key * D);
+                    v[0] = y.x, v[1] = y.y;
+                }
+#pragma unroll
+                for (int r = 0; r < R; r += 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(&s_p[warp][key][r]);
+                    p[r] = y.x;
+                    if (R > 1) p[(r + 1) % R] = y.y;
+                    if (R > 2) p[(r + 2) % R] = y.z, p[(r + 3) % R] = y.w;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    if (masked && p[r] < 0.f) continue;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) o[r][e] += p[r] * v[e];
+                }
+            }
+            __syncwarp();  // every lane has read the tile
+            issue();
+        }
+        have = policy.next(w2);
+        if (have) load_q(w2);
+        if (dead) continue;
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const bool partial = policy.partial(w);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float lr = __shfl_sync(0xffffffffu, l, r), mr = __shfl_sync(0xffffffffu, m, r);
+            if (r >= w.rows) continue;
+            const float inv = partial ? 1.f : (lr == 0.f ? 0.f : 1.f / lr);
+            float *dst = (partial ? policy.part_row(w, w.r0 + r, r) : policy.out_row(w, w.r0 + r)) + lane * V;
+            if constexpr (V == 4)
+                *reinterpret_cast<float4 *>(dst) = make_float4(o[r][0] * inv, o[r][1] * inv, o[r][2] * inv, o[r][3] * inv);
+            else
+                *reinterpret_cast<float2 *>(dst) = make_float2(o[r][0] * inv, o[r][1] * inv);
+            if (partial && lane == 0) *policy.part_sums(w, w.r0 + r, r) = make_float2(mr * scale, lr);
+        }
+    }
+    for (int i = landed; i < issued; ++i) mbar_wait(&full[warp][i % NS], (uint32_t)((i / NS) & 1));
+}
+
 }  // namespace few
 }  // namespace sffn

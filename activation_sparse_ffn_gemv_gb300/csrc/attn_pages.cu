@@ -1,11 +1,10 @@
 // attn_pages.cu -- attention of each token over its chosen pages of the paged cache (sm_103a).
 //
-// An item is a (token, key head, row tile): up to 32 (16 of 128 elements) of the G rows against the n_sel chosen pages, taken one after the
-// other as if they were consecutive positions.  The work of all items is one line as in attn.cuh (units of 64
-// positions and kItemCost more per item), token by token and head by head, cut evenly over the
-// warps (fp32: the CTAs); items that lie in one range are finished there, the pieces of a cut item are joined by
-// k_pages_join.
-#include "attn_rows.cuh"
+// An item is a (token, key head, row tile): up to 32 of the G rows (of 128 elements 16; in fp32 8) against the
+// n_sel chosen pages, taken one after the other as if they were consecutive positions.  The work of all items is
+// one line as in attn.cuh (units of 64 or 16 positions and kItemCost more per item), token by token and head by
+// head, cut evenly over the warps; items that lie in one range are finished there, the pieces of a cut item are
+// joined by k_pages_join.
 #include "attn_few.cuh"
 #include "attn_tc.cuh"
 
@@ -13,7 +12,7 @@ namespace sffn {
 
 namespace {
 
-// Units (of 64 positions) that an item costs by itself (48 tokens of up to 2048 positions, 8 key heads: 55.5 us with 1,
+// Units that an item costs by itself (48 tokens of up to 2048 positions, 8 key heads: 55.5 us with 1,
 // 57.1 with 2, 57.5 with 4).
 constexpr int kItemCost = 1;
 
@@ -28,7 +27,9 @@ SFFN_DEV int pages_of(const PagesArgs &a, int t, bool record) {
     return n;
 }
 
-SFFN_DEV int pages_units(const PagesArgs &a, int n) { return (int)((((long long)n << a.at.page_shift) + kTreeUnit - 1) / kTreeUnit); }
+SFFN_DEV int pages_units(const PagesArgs &a, int n) {
+    return (int)((((long long)n << a.at.page_shift) + (1 << a.unit_shift) - 1) >> a.unit_shift);
+}
 SFFN_DEV int pages_span(const PagesArgs &a, int n) { return n > 0 ? pages_units(a, n) + kItemCost : 0; }
 
 // A piece of an item.
@@ -39,7 +40,7 @@ struct PagesPiece {
     bool whole;
 };
 
-// A CTA's (or a warp's) walk along the line.
+// A warp's walk along the line.
 struct PagesWalk {
     const PagesArgs &a;
     long long u, u1;  // next place, end of the range
@@ -50,10 +51,10 @@ struct PagesWalk {
 
     SFFN_DEV explicit PagesWalk(const PagesArgs &args) : a(args) {}
 
-    // Every thread of the CTA: its range (RANGES = 1), or its warp's, and the token at the range's beginning; rows of
-    // tokens without pages are zeroed (dealt to the CTAs by token); tells the join which item the beginning cuts.
-    template <typename T, int D, int RANGES>
+    // Every thread of the CTA: its warp's range, and the token at the range's beginning; rows of tokens without pages are zeroed (dealt to the CTAs by token); tells the join which item the beginning cuts.
+    template <typename T, int D>
     SFFN_DEV void start() {
+        constexpr int RANGES = few::kWarps;
         __shared__ long long s_scan[33], s_at[RANGES];
         __shared__ int s_t[RANGES];
         const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
@@ -99,7 +100,7 @@ struct PagesWalk {
             }
         }
         __syncthreads();
-        const int r = RANGES == 1 ? 0 : warp, b = blockIdx.x * RANGES + r;
+        const int b = blockIdx.x * RANGES + warp;
         range = b;
         u = u1 = 0;
         h = tile = 0;
@@ -107,17 +108,17 @@ struct PagesWalk {
         if (b < W) {
             u = tree_cut(total, b, W);
             u1 = tree_cut(total, b + 1, W);
-            t = s_t[r];
+            t = s_t[warp];
             n = pages_of(a, t, false);
             span = pages_span(a, n);
-            const int item = (int)((u - s_at[r]) / span);
-            at = s_at[r] + (long long)item * span;
+            const int item = (int)((u - s_at[warp]) / span);
+            at = s_at[warp] + (long long)item * span;
             h = item / a.tiles;
             tile = item - h * a.tiles;
             const int w0 = tree_owner(total, at + kItemCost, W), w1 = tree_owner(total, at + span - 1, W);
             if (w0 < b && b <= w1) cut = make_int4(t, item, w0, w1);
         }
-        if (RANGES == 1 ? tid == 0 : lane == 0) a.cuts[b] = cut;
+        if (lane == 0) a.cuts[b] = cut;
     }
 
     // The next piece with units (false: none is left).
@@ -165,64 +166,10 @@ SFFN_DEV int cache_page(const PagesArgs &a, int t, int h, int j) {
 // Partial result slots as sffn_attn_tree's, of G rows.
 
 // ---------------------------------------------------------------------------
-// fp32: attn_rows.cuh
+// attn_few.cuh over the paged cache
 // ---------------------------------------------------------------------------
 
-template <int D>
-__global__ void __launch_bounds__(rows::kThreads, 1) k_pages_rows(const PagesArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    rows::Smem<D> &sm = *reinterpret_cast<rows::Smem<D> *>(smem_raw);
-    griddep_wait();
-    griddep_launch_dependents();
-    PagesWalk walk(a);
-    walk.start<float, D, 1>();
-    const int tid = threadIdx.x, G = a.group, ps = 1 << a.at.page_shift;
-    PagesPiece p;
-    while (walk.next(p)) {
-        const int k0 = p.un0 * kTreeUnit, k1 = min(seen(a, p.t, p.h, p.n), p.un1 * kTreeUnit);
-        rows::Acc<D> acc;
-        if (k0 < k1) {
-            rows::attend<D>(
-                sm, acc, G, k0, k1, k1, a.scale,
-                [&](int r) { return static_cast<const float *>(a.q) + (size_t)p.t * a.q_stride + (size_t)(p.h * G + r) * D; },
-                [&](int j, int which) -> const float * {
-                    const int pg = cache_page(a, p.t, p.h, j);
-                    if (pg < 0) return nullptr;
-                    return static_cast<const float *>(which ? a.cv : a.ck) +
-                           ((((size_t)pg * a.n_kv_heads + p.h) << a.at.page_shift) + (size_t)(j & (ps - 1))) * D;
-                },
-                [&](int, int) { return false; });
-        } else {  // behind the last position that the token sees
-            __syncthreads();
-            if (tid < G) sm.m[tid] = -INFINITY, sm.l[tid] = 0.f;
-#pragma unroll
-            for (int i = 0; i < rows::Acc<D>::RPT; ++i) acc.o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            __syncthreads();
-        }
-        float *slot = a.part + tree_slot_floats(a.row_tile, D) * (size_t)(2 * blockIdx.x + (p.un0 > 0 ? 0 : 1));
-        const int c = (tid % rows::Acc<D>::CT) * 4, g = (tid / rows::Acc<D>::CT) * rows::Acc<D>::RPT;
-#pragma unroll
-        for (int i = 0; i < rows::Acc<D>::RPT; ++i) {
-            const int r = g + i;
-            if (r >= G) continue;
-            const float4 o = acc.o[i];
-            if (p.whole) {
-                const float l = sm.l[r], inv = l == 0.f ? 0.f : 1.f / l;
-                float *dst = static_cast<float *>(a.out) + ((size_t)p.t * a.n_heads + (size_t)(p.h * G + r)) * D + c;
-                *reinterpret_cast<float4 *>(dst) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-            } else {
-                *reinterpret_cast<float4 *>(slot + (size_t)r * D + c) = o;
-                if (c == 0) *reinterpret_cast<float2 *>(slot + (size_t)a.row_tile * D + 2 * r) = make_float2(sm.m[r], sm.l[r]);
-            }
-        }
-    }
-}
-
-// ---------------------------------------------------------------------------
-// bf16: attn_few.cuh over the paged cache
-// ---------------------------------------------------------------------------
-
-template <int D>
+template <typename T, int D>
 struct PagesPolicy {
     const PagesArgs &a;
     PagesWalk walk;
@@ -236,8 +183,8 @@ struct PagesPolicy {
         w.h = p.h;
         w.r0 = p.tile * a.row_tile;
         w.rows = min(a.row_tile, a.group - w.r0);
-        w.k0 = p.un0 * kTreeUnit;
-        w.k1 = w.all = max(w.k0, min(seen(a, p.t, p.h, p.n), p.un1 * kTreeUnit));  // (none behind the last that it sees)
+        w.k0 = p.un0 << a.unit_shift;
+        w.k1 = w.all = max(w.k0, min(seen(a, p.t, p.h, p.n), p.un1 << a.unit_shift));  // (none behind the last that it sees)
         w.whole = p.whole;
         w.slot = 2 * walk.range + (p.un0 > 0 ? 0 : 1);
         return true;
@@ -246,12 +193,12 @@ struct PagesPolicy {
         const int pg = cache_page(a, w.q_row, w.h, j);
         return pg < 0 ? a.at.n_pages : pg;
     }
-    SFFN_DEV const __nv_bfloat16 *query(const few::Work &w, int row) const {
-        return static_cast<const __nv_bfloat16 *>(a.q) + (size_t)w.q_row * a.q_stride + (size_t)(w.h * a.group + row) * D;
+    SFFN_DEV const T *query(const few::Work &w, int row) const {
+        return static_cast<const T *>(a.q) + (size_t)w.q_row * a.q_stride + (size_t)(w.h * a.group + row) * D;
     }
     SFFN_DEV bool sees(const few::Work &, int, int) const { return false; }
-    SFFN_DEV __nv_bfloat16 *out_row(const few::Work &w, int row) const {
-        return static_cast<__nv_bfloat16 *>(a.out) + ((size_t)w.q_row * a.n_heads + (size_t)w.h * a.group + row) * D;
+    SFFN_DEV T *out_row(const few::Work &w, int row) const {
+        return static_cast<T *>(a.out) + ((size_t)w.q_row * a.n_heads + (size_t)w.h * a.group + row) * D;
     }
     SFFN_DEV bool partial(const few::Work &w) const { return !w.whole; }
     SFFN_DEV float *part_row(const few::Work &w, int, int r) const {
@@ -268,9 +215,19 @@ __global__ void __launch_bounds__(few::kThreads, 2)
     extern __shared__ __align__(16) unsigned char smem_raw[];
     griddep_wait();
     griddep_launch_dependents();
-    PagesPolicy<D> policy(a);
-    policy.walk.template start<__nv_bfloat16, D, few::kWarps>();
+    PagesPolicy<__nv_bfloat16, D> policy(a);
+    policy.walk.template start<__nv_bfloat16, D>();
     few::attention<D, NT>(policy, map_k, map_v, a.at.page_shift, a.n_kv_heads, a.scale, a.err, smem_raw);
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(few::kThreads, 2) k_pages_few32(const PagesArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    griddep_wait();
+    griddep_launch_dependents();
+    PagesPolicy<float, D> policy(a);
+    policy.walk.template start<float, D>();
+    few::attention_f32<D, R>(policy, a.ck, a.cv, a.at.page_shift, a.at.n_pages, a.n_kv_heads, a.scale, a.err, smem_raw);
 }
 
 // ---------------------------------------------------------------------------
@@ -668,17 +625,32 @@ cudaError_t launch_join(const PagesArgs &a, int ranges, cudaStream_t s) {
     return launch_k(k_pages_join<T, D>, dim3((unsigned)((ranges - 1) * parts)), dim3(32 * kJoinWarps), 0, s, a, parts);
 }
 
+template <int D, int R>
+cudaError_t launch_few32(PagesArgs a, int grid, cudaStream_t s) {
+    a.row_tile = a.group < R ? a.group : R;
+    a.tiles = (a.group + a.row_tile - 1) / a.row_tile;
+    // Units of 16 positions balance the warps better where there are more of 64 than warps (27 tokens of 512 positions, 64/8
+    // heads: 26.6 us, with 64 36.5), and give a short list to more warps (4 tokens of 320: 13.6 and 16.6); between the two they
+    // only make more pieces to join (5 tokens of 576: 21.7 and 17.5).
+    const long long list = (long long)a.n_keep << a.at.page_shift;
+    const long long units = (list + 63) / 64 * a.T * a.n_kv_heads * a.tiles;
+    a.unit_shift = list <= 320 || units >= 2LL * grid * few::kWarps ? 4 : 6;
+    constexpr int smem = few::Cfg32<D>::kSmem;
+    cudaError_t e = set_max_smem((const void *)k_pages_few32<D, R>, smem);
+    if (e == cudaSuccess) e = launch_k(k_pages_few32<D, R>, dim3(2 * grid), dim3(few::kThreads), smem, s, a);
+    return e == cudaSuccess ? launch_join<float, D>(a, 2 * grid * few::kWarps, s) : e;
+}
+
 template <int D>
-cudaError_t launch_f32(PagesArgs a, int grid, cudaStream_t s) {
-    a.row_tile = a.group;
-    a.tiles = 1;
-    cudaError_t e = set_max_smem((const void *)k_pages_rows<D>, (int)sizeof(rows::Smem<D>));
-    if (e == cudaSuccess) e = launch_k(k_pages_rows<D>, dim3(grid), dim3(rows::kThreads), sizeof(rows::Smem<D>), s, a);
-    return e == cudaSuccess ? launch_join<float, D>(a, grid, s) : e;
+cudaError_t launch_f32(const PagesArgs &a, int grid, cudaStream_t s) {
+    if (a.group == 1) return launch_few32<D, 1>(a, grid, s);
+    if (a.group == 2) return launch_few32<D, 2>(a, grid, s);
+    return a.group <= 4 ? launch_few32<D, 4>(a, grid, s) : launch_few32<D, 8>(a, grid, s);
 }
 
 template <int D, int NT>
 cudaError_t launch_few(PagesArgs a, int grid, cudaStream_t s) {
+    a.unit_shift = 6;
     const int ps = 1 << a.at.page_shift;
     a.row_tile = a.group < 8 * NT ? a.group : 8 * NT;
     a.tiles = (a.group + a.row_tile - 1) / a.row_tile;
@@ -728,10 +700,8 @@ PagesPlan make_pages_plan(int T, int n_heads, int n_kv_heads, int head_dim) {
     const size_t ranges = 2 * few::kWarps * (size_t)p.grid;
     o = align_up(o + sizeof(int4) * ranges);
     p.off_part = o;
-    // bf16: a slot pair a warp, of a row tile; fp32: a CTA, of all rows
     const int G = n_heads / n_kv_heads, most = few::max_rows(head_dim);
-    const size_t b = ranges * tree_slot_floats(G < most ? G : most, head_dim), f = p.grid * tree_slot_floats(G, head_dim);
-    o = align_up(o + sizeof(float) * 2 * (b > f ? b : f));
+    o = align_up(o + sizeof(float) * 2 * ranges * tree_slot_floats(G < most ? G : most, head_dim));
     p.off_runs = o;
     o = align_up(o + sizeof(int32_t) * (size_t)T);
     p.off_unions = o;

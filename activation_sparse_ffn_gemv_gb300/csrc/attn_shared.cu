@@ -15,6 +15,7 @@
 //                         first on as many SMs as its share of the work asks for (its other CTAs leave
 //                         at once), the second on the rest, two CTAs an SM;
 //   else                  attn_tc.cuh takes the line (large draft trees).
+// In fp32 attn_rows.cuh has the place of attn_tc.cuh.
 // Each cuts its part of the line evenly over its CTAs (attn_few.cuh: its warps).  An item leaves its result in `home` rows (one set for
 // prefixes, one for own positions), the pieces of a cut item in the range's slots; k_shared_join adds both parts of
 // each row.  Rows of a sequence without a shared page that no cut touches are written at once.
@@ -31,6 +32,12 @@ constexpr int kCostTc = 5, kCostFew = 1, kCostRows = 5;
 // Time of a prefix's place in attn_tc.cuh on an SM, in that of a place in attn_few.cuh: kPlaceTc / kPlaceFew (96 sequences
 // on 24576 shared positions: 131 us with 9 / 4, 122 with 12 / 4, 127 with 16 / 4).
 constexpr int kPlaceTc = 11, kPlaceFew = 4;
+// The same in fp32 (64 sequences on 8192: 464 us with 8 / 4, 407 with 16 / 4, 374 with 32 / 4).
+constexpr int kPlaceRows = 32, kPlaceFew32 = 4;
+// fp32: rows of the mean sequence that attn_few.cuh takes, and of the mean group beside them.  The other way took: 1 row a
+// sequence, 16 a group 337 us (few 118); 4 and 64 174 (73); 8 and 64 80 (40); 14 and 48 34 (45); 19 and 48 27 (28).  Groups of 64
+// and 128 rows with prefixes by the row tiles of 64 67 and 204 us (few 73 and 259), of 16 153 (118).
+constexpr int kFew32Own = 8, kFew32Pre = 64;
 // Places of a range of attn_few.cuh at the least: shorter ones have more pieces to join (4 sequences on 1024 shared positions:
 // 18.8 us with 1, 17.9 with 2, 19.3 with 3).
 constexpr int kLeastFew = 2;
@@ -145,17 +152,18 @@ struct Stretch {
     int ranges;
     SFFN_DEV long long cut(int w) const { return first + tree_cut(length, w, ranges); }
 };
-// which: kLine...; sms: SMs; per: ranges an SM has of the kernel that takes it.
-SFFN_DEV Stretch stretch_of(const Line &line, int which, int sms, int per) {
+// which: kLine...; per: ranges an SM has of the kernel that takes it.
+SFFN_DEV Stretch stretch_of(const SharedArgs &a, const Line &line, int which, int per) {
+    const int sms = a.sms;
     const long long all = line.pre[line.entries], pre = line.pre[line.n_groups], own = all - pre;
-    if (which == kLineAll) return Stretch{0, all, tree_ctas((all + kLeastFew - 1) / kLeastFew, sms * per)};
+    if (which == kLineAll) return Stretch{0, all, tree_ctas((all + a.least - 1) / a.least, sms * per)};
     // SMs of the prefixes by their share of the time; the own positions always have one
-    const long long tp = pre * kPlaceTc, to = own * kPlaceFew;
+    const long long tp = pre * a.place[0], to = own * a.place[1];
     int n = pre == 0 ? 0 : (int)(sms * tp / (tp + to));
     if (pre > 0 && n < 1) n = 1;
     if (own > 0 && n > sms - 1) n = sms - 1;
     if (which == kLinePrefixes) return Stretch{0, pre, tree_ctas(pre, n * per)};
-    return Stretch{pre, own, tree_ctas((own + kLeastFew - 1) / kLeastFew, (sms - n) * per)};
+    return Stretch{pre, own, tree_ctas((own + a.least - 1) / a.least, (sms - n) * per)};
 }
 
 // A piece of an item.
@@ -219,7 +227,7 @@ struct alignas(16) Entry {
 };
 SFFN_DEV Half half_of(const SharedArgs &a, const Line &line, int entry, const Part &p) {
     const int kind = p.prefix ? 0 : 1;
-    const Stretch st = stretch_of(line, a.split ? kind + 1 : kLineAll, a.sms, a.per[kind]);
+    const Stretch st = stretch_of(a, line, a.split ? kind + 1 : kLineAll, a.per[kind]);
     return Half{a.parts[kind], line.pre[entry] - st.first, st.length, st.ranges, a.rows_max[kind], p.t0, p.rows, p.tiles, p.units, p.cost, 0};
 }
 SFFN_DEV void write_entries(const SharedArgs &a, const Line &line) {
@@ -257,11 +265,11 @@ SFFN_DEV uint64_t token_mask(const SharedArgs &a, int token, int i) {
 }
 
 // ---------------------------------------------------------------------------
-// fp32: attn_rows.cuh
+// fp32, many rows: attn_rows.cuh
 // ---------------------------------------------------------------------------
 
 template <int D>
-__global__ void __launch_bounds__(rows::kThreads, 1) k_shared_rows(const SharedArgs a) {
+__global__ void __launch_bounds__(rows::kThreads, 1) k_shared_rows(const SharedArgs a, int which) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     rows::Smem<D> &sm = *reinterpret_cast<rows::Smem<D> *>(smem_raw);
     const Line line(a, smem_raw + sizeof(rows::Smem<D>));
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) k_shared_rows(const SharedA
     line.build(a, blockIdx.x == 0);
     write_entries(a, line);
     Walk walk;
-    walk.start(a, line, stretch_of(line, kLineAll, a.sms, a.per[0]), blockIdx.x);
+    walk.start(a, line, stretch_of(a, line, which, a.per[0]), blockIdx.x);
     const int tid = threadIdx.x, G = a.group, ps = 1 << a.page_shift;
     while (walk.next(a, line)) {
         const Piece &c = walk.c;
@@ -350,7 +358,7 @@ struct SharedPolicy {
     SFFN_DEV void start() {
         line.build(a, blockIdx.x == 0);
         write_entries(a, line);
-        walk.start(a, line, stretch_of(line, which, a.sms, 1), blockIdx.x);
+        walk.start(a, line, stretch_of(a, line, which, 1), blockIdx.x);
     }
     SFFN_DEV bool next(atc::Work &w) {
         if (!walk.next(a, line)) return false;
@@ -460,10 +468,10 @@ __global__ void __launch_bounds__(atc::kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// bf16, few rows: attn_few.cuh
+// Few rows: attn_few.cuh
 // ---------------------------------------------------------------------------
 
-template <int D>
+template <typename T, int D>
 struct FewPolicy {
     const SharedArgs &a;
     const Line &line;
@@ -498,16 +506,16 @@ struct FewPolicy {
     SFFN_DEV size_t row_of(const few::Work &w, int row) const {  // row of q and out, in heads
         return (size_t)(w.q_row + row / a.group) * a.n_heads + (size_t)w.h * a.group + row % a.group;
     }
-    SFFN_DEV const __nv_bfloat16 *query(const few::Work &w, int row) const {
-        return static_cast<const __nv_bfloat16 *>(a.q) + (size_t)(w.q_row + row / a.group) * a.q_stride +
+    SFFN_DEV const T *query(const few::Work &w, int row) const {
+        return static_cast<const T *>(a.q) + (size_t)(w.q_row + row / a.group) * a.q_stride +
                (size_t)(w.h * a.group + row % a.group) * D;
     }
     SFFN_DEV bool sees(const few::Work &w, int row, int key) const {
         const int i = row / a.group;
         return (token_mask(a, w.q_row + i, i) >> (key - w.ctx)) & 1;
     }
-    SFFN_DEV __nv_bfloat16 *out_row(const few::Work &w, int row) const {
-        return static_cast<__nv_bfloat16 *>(a.out) + row_of(w, row) * D;
+    SFFN_DEV T *out_row(const few::Work &w, int row) const {
+        return static_cast<T *>(a.out) + row_of(w, row) * D;
     }
     SFFN_DEV bool partial(const few::Work &w) const { return !w.whole || w.kind != 0; }
     SFFN_DEV float *slot(const few::Work &w) const {
@@ -535,10 +543,25 @@ __global__ void __launch_bounds__(few::kThreads, 2)
     griddep_launch_dependents();
     line.build(a, which == kLineAll && blockIdx.x == 0);
     if (which == kLineAll) write_entries(a, line);
-    FewPolicy<D> policy(a, line);
-    policy.walk.start(a, line, stretch_of(line, which, a.sms, kFewRanges), blockIdx.x * few::kWarps + (threadIdx.x >> 5));
+    FewPolicy<__nv_bfloat16, D> policy(a, line);
+    policy.walk.start(a, line, stretch_of(a, line, which, kFewRanges), blockIdx.x * few::kWarps + (threadIdx.x >> 5));
     few::attention<D, NT>(policy, map_k, map_v, a.page_shift, a.n_kv_heads, a.scale, a.err,
                           smem_raw + Line::bytes(a.n_groups, a.n_seq));
+    if (which != kLineAll) griddep_wait();
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(few::kThreads, 2) k_shared_few32(const SharedArgs a, int which) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    const Line line(a, smem_raw);
+    if (which == kLineAll) griddep_wait();
+    griddep_launch_dependents();
+    line.build(a, which == kLineAll && blockIdx.x == 0);
+    if (which == kLineAll) write_entries(a, line);
+    FewPolicy<float, D> policy(a, line);
+    policy.walk.start(a, line, stretch_of(a, line, which, kFewRanges), blockIdx.x * few::kWarps + (threadIdx.x >> 5));
+    few::attention_f32<D, R>(policy, a.ck, a.cv, a.page_shift, a.n_pages, a.n_kv_heads, a.scale, a.err,
+                             smem_raw + Line::bytes(a.n_groups, a.n_seq));
     if (which != kLineAll) griddep_wait();
 }
 
@@ -657,17 +680,41 @@ cudaError_t launch_join(const SharedArgs &a, cudaStream_t s) {
     return launch_k(k_shared_join<T, D>, dim3((unsigned)(blocks < most ? blocks : most)), dim3(32 * kJoinWarps), 0, s, a);
 }
 
+template <int D, int R>
+cudaError_t launch_few32(const SharedArgs &a, int which, cudaStream_t s) {
+    const size_t smem = few::Cfg32<D>::kSmem + Line::bytes(a.n_groups, a.n_seq);
+    const cudaError_t e = set_max_smem((const void *)k_shared_few32<D, R>, (int)smem);
+    return e == cudaSuccess ? launch_k(k_shared_few32<D, R>, dim3(2 * a.sms), dim3(few::kThreads), smem, s, a, which) : e;
+}
+
 template <int D>
 cudaError_t launch_f32(SharedArgs a, cudaStream_t s) {
+    const long long rows = (long long)a.T * a.group, per_group = rows / a.n_groups, per_seq = rows / a.n_seq;
+    const bool few_own = per_seq <= kFew32Own, few_pre = few_own && per_group <= kFew32Pre;
+    const long long most = few_pre ? per_group : per_seq;
+    const int R = most <= 1 ? 1 : (most <= 2 ? 2 : (most <= 4 ? 4 : 8));
+    const bool few_kind[2] = {few_pre, few_own};
     for (int k = 0; k < 2; ++k) {
-        a.tile_rows[k] = rows::kRows / a.group * a.group;
-        a.cost[k] = kCostRows;
-        a.per[k] = 1;
+        a.tile_rows[k] = few_kind[k] ? R : rows::kRows / a.group * a.group;
+        a.cost[k] = few_kind[k] ? kCostFew : kCostRows;
+        a.per[k] = few_kind[k] ? kFewRanges : 1;
+        if (few_kind[k]) a.parts[k] = a.part_few, a.rows_max[k] = few::max_rows(D);
     }
-    a.split = 0;
-    const size_t smem = sizeof(rows::Smem<D>) + Line::bytes(a.n_groups, a.n_seq);
-    cudaError_t e = set_max_smem((const void *)k_shared_rows<D>, (int)smem);
-    if (e == cudaSuccess) e = launch_k(k_shared_rows<D>, dim3(a.sms), dim3(rows::kThreads), smem, s, a);
+    a.split = few_own && !few_pre;
+    a.least = 1;  // (16 sequences on 1024: 26.6 us, with 2 29.9)
+    a.place[0] = kPlaceRows, a.place[1] = kPlaceFew32;
+    cudaError_t e = cudaSuccess;
+    if (!few_pre) {
+        const size_t smem = sizeof(rows::Smem<D>) + Line::bytes(a.n_groups, a.n_seq);
+        e = set_max_smem((const void *)k_shared_rows<D>, (int)smem);
+        if (e == cudaSuccess) e = launch_k(k_shared_rows<D>, dim3(a.sms), dim3(rows::kThreads), smem, s, a, a.split ? kLinePrefixes : kLineAll);
+    }
+    if (e == cudaSuccess && few_own) {
+        const int which = a.split ? kLineOwn : kLineAll;
+        if (R == 1) e = launch_few32<D, 1>(a, which, s);
+        else if (R == 2) e = launch_few32<D, 2>(a, which, s);
+        else e = R == 4 ? launch_few32<D, 4>(a, which, s) : launch_few32<D, 8>(a, which, s);
+    }
     return e == cudaSuccess ? launch_join<float, D>(a, s) : e;
 }
 
@@ -718,6 +765,8 @@ cudaError_t launch_bf16(SharedArgs a, cudaStream_t s) {
         if (few_kind[k]) a.parts[k] = a.part_few, a.rows_max[k] = kFewRows;
     }
     a.split = few_own && !few_pre;
+    a.least = kLeastFew;
+    a.place[0] = kPlaceTc, a.place[1] = kPlaceFew;
     cudaError_t e = cudaSuccess;
     if (!few_pre) {
         const int which = a.split ? kLinePrefixes : kLineAll;

@@ -224,6 +224,8 @@ struct SharedArgs : TreeArgs {
     float *parts[2];        // slots for the pieces of cut items
     int rows_max[2];        // rows of a slot
     int split;              // two kernels
+    int place[2];           // time of a place of each on an SM
+    int least;              // places of a range at the least
     float *part_few;        // attn_few.cuh's slots
     float *home;            // rows of whole items, of prefixes and of own positions
     void *entries;          // what the join has to know of the sequences
@@ -280,6 +282,7 @@ struct PagesArgs {
     float scale;
     void *out;
     int row_tile, tiles;  // rows of a row tile, row tiles of a key head's rows
+    int unit_shift;       // log2 of the positions of a unit of work
     int4 *cuts;   // for each range: token, its item, first and last range of the item that its beginning cuts
     float *part;  // partial results of cut items
     int32_t *runs, *unions;  // of a token that begins a run: the run's tokens; the pages of their union, per key head

@@ -282,6 +282,20 @@ def test_attn_pages(S, lens, at, hq, hkv, D, page, dt, keep):  # noqa: F811
     assert torch.equal(out, c.attend(S, sel, n_sel, workspace=ws))  # equal calls, equal bits
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,at,hq,hkv,D,page,keep", [
+    ([900, 77], [[899], [76]], 3, 3, 128, 8, 40),
+    ([900, 77], [[899, 3], [76, 75, 74]], 8, 4, 64, 16, 12),
+    ([1300], [[1299, 1298]], 20, 5, 128, 32, 21),
+    ([640, 64], [[500, 639], [63]], 64, 1, 64, 64, 3),
+    ([1700], [list(range(1500, 1620))], 28, 4, 128, 16, 30),          # more units than warps
+    ([3000] * 30, [[2999 - i] for i in range(30)], 32, 32, 64, 128, 7),
+    ([4096], [[4095]], 2, 1, 128, 1024, 2),
+])
+def test_attn_pages_in_fp32(S, lens, at, hq, hkv, D, page, keep):  # noqa: F811
+    test_attn_pages(S, lens, at, hq, hkv, D, page, "f32", keep)
+
+
 MANY = [
     # positions, tokens of each sequence (many of one: they share what they read), hq, hkv, D, page, keep
     ([900, 700], [list(range(500, 640)), list(range(70))], 4, 4, 64, 8, 20),
@@ -533,6 +547,32 @@ def test_attn_shared(S, groups, prefix, own, n, hq, hkv, D, page, dt):  # noqa: 
     p.check(out)
     assert torch.equal(out, call_shared(S, p, groups, prefix, workspace=ws))  # equal calls, equal bits
     p.check(call_shared(S, p, groups, prefix, masks=None, workspace=ws), masks=None)  # a chain
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("groups,prefix,own,n,hq,hkv,D,page", [
+    ([3], [600], [1, 70, 200], [1, 1, 1], 3, 3, 64, 8),
+    ([4, 4], [300, 129], [i * 31 for i in range(8)], [1] * 8, 8, 4, 128, 16),
+    ([5], [77], [0, 1, 2, 130, 64], [2, 1, 1, 2, 1], 20, 5, 128, 32),
+    ([7, 2], [900, 0], [11 * i for i in range(9)], [1] * 9, 14, 2, 64, 64),
+    ([40], [1000], [3 * i for i in range(40)], [1 + i % 2 for i in range(40)], 10, 2, 128, 16),  # a group of many rows
+    ([90, 1], [520, 8], [i % 70 for i in range(91)], [1] * 91, 4, 4, 64, 8),                     # and of single ones
+    ([33], [2000], [50] * 33, [2] * 33, 8, 2, 64, 128),
+])
+def test_attn_shared_few_rows_in_fp32(S, groups, prefix, own, n, hq, hkv, D, page):  # noqa: F811
+    of = [x for m, x in zip(groups, prefix) for _ in range(m)]
+    args = ([a + b for a, b in zip(of, own)], n, hq, hkv, D, page, "f32", sum(own) + hq)
+    p, hurt = Paged(S, *args), Paged(S, *args, fill=float("inf"))
+    for x in (p, hurt):
+        share(x, groups, prefix, page)
+    ws = S.alloc_attn_workspace(S.WS_ATTN_SHARED, sum(n), len(n), hq, hkv, D)
+    out = call_shared(S, p, groups, prefix, workspace=ws)
+    assert S.read_device_error(ws) == 0
+    p.check(out)
+    assert torch.equal(out, call_shared(S, hurt, groups, prefix, workspace=ws))
+    masks = [0 if t % 3 == 0 else m for t, m in enumerate(p.masks)]  # some see the prefix alone, or nothing
+    p.check(call_shared(S, p, groups, prefix, masks, workspace=ws), masks)
+    assert S.read_device_error(ws) == 0
 
 
 @pytest.mark.gpu
