@@ -683,8 +683,12 @@ cudaError_t launch_union(const PagesArgs &a, int grid, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
-    // Half a row tile of tokens, or more, of the mean sequence: their union.
-    if ((long long)a.T * a.group >= 64LL * a.at.n_seq && a.at.table_width <= kUnionWidth)
+    // The union where the mean sequence has half a row tile of rows or more and the lists may hold 3 million positions: by
+    // themselves the tokens take about 35 us a million, items 75 to 130 us for the first 152 of them.  Chunks of 28/4 heads, 1536
+    // positions a token: 256 tokens 68 us by themselves and 102 by unions, 512 119 and 110, 2048 427 and 234; 32/8 heads,
+    // 2048 positions: 256 tokens 146 and 125, 2048 1067 and 285; 33 sequences of 13 tokens, 1760 positions: 40 and 191.
+    if ((long long)a.T * a.group >= 64LL * a.at.n_seq && a.at.table_width <= kUnionWidth &&
+        (((long long)a.T * a.n_kv_heads * a.n_keep) << a.at.page_shift) >= 3000000)
         return a.group >= 4 ? launch_union<D, 2>(a, grid, s) : launch_union<D, 8>(a, grid, s);
     if (a.group <= 8) return launch_few<D, 1>(a, grid, s);
     return a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, few::max_rows(D) / 8>(a, grid, s);

@@ -306,14 +306,22 @@ MANY = [
     ([300, 77], [list(range(300)), list(range(77))], 28, 4, 128, 32, 4),
     ([260], [[3 * i for i in range(80)]], 12, 12, 128, 16, 7),
     ([40], [list(range(40))], 128, 2, 64, 8, 2),
+    ([50], [list(range(50))], 128, 2, 64, 8, 2),
 ]
 
 
+def widen(sel, keep):
+    """The lists in rows of `keep` entries (many, that may hold much: the tokens are taken together)."""
+    return torch.nn.functional.pad(sel, (0, keep - sel.shape[2]), value=-1)
+
+
 @pytest.mark.gpu
+@pytest.mark.parametrize("room", [0, 4096])
 @pytest.mark.parametrize("lens,at,hq,hkv,D,page,keep", MANY)
-def test_attn_pages_many_tokens_of_a_sequence(S, lens, at, hq, hkv, D, page, keep):  # noqa: F811
+def test_attn_pages_many_tokens_of_a_sequence(S, lens, at, hq, hkv, D, page, keep, room):  # noqa: F811
     c = Tokens(S, lens, at, hq, hkv, D, page, "bf16", sum(lens) + hq)
     sel, n_sel = c.select(S, keep, 1 if keep > 1 else 0)
+    sel = widen(sel, max(room, keep))
     ws = S.alloc_attn_workspace(S.WS_ATTN_PAGES, len(c.pos), len(lens), hq, hkv, D)
     out = c.attend(S, sel, n_sel, workspace=ws)
     assert S.read_device_error(ws) == 0
@@ -322,11 +330,13 @@ def test_attn_pages_many_tokens_of_a_sequence(S, lens, at, hq, hkv, D, page, kee
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("room", [6, 4096])
 @pytest.mark.parametrize("hq,D", [(8, 128), (2, 64)])
-def test_attn_pages_many_tokens_padding_and_contract_errors(S, hq, D):  # noqa: F811
+def test_attn_pages_many_tokens_padding_and_contract_errors(S, hq, D, room):  # noqa: F811
     """Padding, tokens without pages, tokens and list entries out of range among many tokens of two sequences."""
     c = Tokens(S, [400, 200], [list(range(250, 380)), list(range(100, 190))], hq, 2, D, 16, "bf16", 9)
     sel, n_sel = c.select(S, 6)
+    sel = widen(sel, room)
     T, pos, seqs, n = len(c.pos), list(c.pos), list(c.seqs), n_sel.tolist()
     ws = S.alloc_attn_workspace(S.WS_ATTN_PAGES, T, 2, hq, 2, D)
 
@@ -354,7 +364,7 @@ def test_attn_pages_many_tokens_padding_and_contract_errors(S, hq, D):  # noqa: 
         getattr(c, what)[50] = bad
         assert (run(S.ERR_DEVICE, [50])[50] == 9).all()
     c.pos, c.seqs = pos, seqs
-    assert (run(S.ERR_DEVICE, [33], [7 if t == 33 else x for t, x in enumerate(n)])[33] == 9).all()
+    assert (run(S.ERR_DEVICE, [33], [room + 1 if t == 33 else x for t, x in enumerate(n)])[33] == 9).all()
     for bad in (25, -1, 1 << 20, -(1 << 31)):  # list entries past the token's own page or outside the table
         hurt = sel.clone()
         hurt[20, 1, 0] = bad
@@ -368,11 +378,12 @@ def test_attn_pages_many_tokens_padding_and_contract_errors(S, hq, D):  # noqa: 
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("D,page", [(128, 32), (64, 16)])
-def test_attn_pages_many_tokens_unseen_places_have_no_influence(S, bad, D, page):  # noqa: F811
+@pytest.mark.parametrize("D,page,room", [(128, 32, 4096), (64, 16, 4096), (64, 16, 3)])
+def test_attn_pages_many_tokens_unseen_places_have_no_influence(S, bad, D, page, room):  # noqa: F811
     args = ([400], [list(range(200, 330))], 8, 2, D, page, "bf16", 6)
     c = Tokens(S, *args, fill=0.0)
     sel, n_sel = c.select(S, 3)
+    sel = widen(sel, room)
     out = c.attend(S, sel, n_sel)
     c.check_attention(out, sel, n_sel)
     d = Tokens(S, *args, fill=bad)
