@@ -585,7 +585,7 @@ SFFN_DEV Pieces pieces_of(const SharedArgs &a, const Half &e, bool prefix, int t
     const int at = (t - e.t0) * a.group + head % a.group, tile = at / e.rows, r = at - tile * e.rows;
     const long long u = e.at + ((long long)(head / a.group) * e.tiles + tile) * (e.units + e.cost) + e.cost;
     int w0, w1;  // ranges of its pieces
-    if ((u + e.units) * e.ranges < (1ll << 32)) {  // (tree_owner)
+    if ((u + e.units) * e.ranges < (1ll << 32) && e.length < (1ll << 32)) {  // (tree_owner)
         w0 = (int)(((uint32_t)(u + 1) * (uint32_t)e.ranges - 1u) / (uint32_t)e.length);
         w1 = (int)(((uint32_t)(u + e.units) * (uint32_t)e.ranges - 1u) / (uint32_t)e.length);
     } else {

@@ -567,15 +567,17 @@ sffn_status sffn_page_select(const void *q, int64_t q_stride, int T, int n_heads
 
 /* Attention of T tokens, each over the positions up to its own in its chosen pages, per key head:
  *   out_t = sum_j softmax_j(scale * q_t . k_j) v_j,  j <= positions[t] in the pages sel[t, h, 0 .. n_sel[t] - 1].
- *   sel, n_sel   as sffn_page_select writes them, or made by the caller: 0 <= n_sel[t] <= n_keep; pages ascending, none
- *                past the token's own.  An entry that is, or is outside the table, reads as a page of zeros and is
- *                recorded, as is a page outside the cache.
+ *   sel, n_sel   as sffn_page_select writes them, or made by the caller: 0 <= n_sel[t] <= n_keep; pages ascending, each
+ *                once, none past the token's own.  An entry that is, or is outside the table, is recorded, as is a page
+ *                outside the cache: that head's rows of the token then stand for nothing, those of others are not touched
+ *                by it.  Lists in another order are not looked for; their rows stand for nothing either.
  *   page_table, seqs, positions  as sffn_page_select.  A token of negative position is padding: its row of out
  *                is left as it is.  One whose sequence, position or n_sel is out of range is skipped (likewise)
  *                and recorded.  With n_sel 0 the row is zeros.
  *   scale        finite, > 0.   out  [T, n_heads, head_dim].
  * Precision as sffn_attn_tree; what a token does not see has no influence, whatever it holds; equal calls give
- * equal bits.  0 <= T <= 65536 (0: a no-op), n_seq >= 1, 1 <= n_keep <= 4096. */
+ * equal bits.  0 <= T <= 65536 (0: a no-op), n_seq >= 1, 1 <= n_keep <= 4096.
+ * (The workspace has 1 KB for each token and key head, the pages that neighbouring tokens share.) */
 sffn_status sffn_attn_pages(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
                             const int32_t *page_table, int table_width, int n_seq, const int32_t *seqs,
                             const int32_t *positions, const int32_t *sel, const int32_t *n_sel, int n_keep,

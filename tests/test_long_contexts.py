@@ -747,6 +747,42 @@ def test_calls_together_in_a_cuda_graph_and_on_another_stream(S):  # noqa: F811
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_two_calls_at_once(S, dt):  # noqa: F811
+    """On two streams, a workspace each: what each call gives alone, bit for bit."""
+    groups, prefix, own = [40, 3], [700, 128], [9 * i % 250 for i in range(43)]
+    of = [x for m, x in zip(groups, prefix) for _ in range(m)]
+    p = Paged(S, [a + b for a, b in zip(of, own)], [2] * 43, 16, 4, 128, 32, dt, 8)
+    share(p, groups, prefix, 32)
+    c = Tokens(S, [900, 700], [list(range(500, 640)), list(range(70))], 16, 4, 128, 32, dt, 5)
+    sel, n_sel = c.select(S, 9)
+    sel = widen(sel, 1024)
+    calls = [lambda ws, out: call_shared(S, p, groups, prefix, workspace=ws, out=out),
+             lambda ws, out: c.attend(S, sel, n_sel, workspace=ws, out=out)]
+    sizes = [(S.WS_ATTN_SHARED, 86, 43), (S.WS_ATTN_PAGES, len(c.pos), 2)]
+    jobs = []
+    for i in range(4):  # each call twice, on its own stream
+        which, T, n_seq = sizes[i % 2]
+        ws = S.alloc_attn_workspace(which, T, n_seq, 16, 4, 128)
+        jobs.append((calls[i % 2], ws, torch.empty(T, 16, 128, dtype=dtype_of(dt), device="cuda"), torch.cuda.Stream()))
+    alone = []
+    for call, ws, out, _ in jobs:
+        call(ws, out)
+        torch.cuda.synchronize()
+        alone.append(out.clone())
+    p.check(alone[0])
+    c.check_attention(alone[1], sel, n_sel)
+    for _ in range(5):
+        for call, ws, out, stream in jobs:
+            with torch.cuda.stream(stream):
+                out.zero_()
+                call(ws, out)
+        torch.cuda.synchronize()
+        for (_, ws, out, _), want in zip(jobs, alone):
+            assert torch.equal(out, want) and S.read_device_error(ws) == 0
+
+
+@pytest.mark.gpu
 def test_pages_past_32_bit_offsets(S):  # noqa: F811
     """Pages whose elements lie past 2^32, for every call."""
     hkv, page, D = 8, 64, 128
