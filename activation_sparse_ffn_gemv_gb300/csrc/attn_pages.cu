@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(few::kThreads, 2) k_pages_few32(const PagesArg
 // where the tokens one by one read 1728.  k_pages_runs finds the runs and writes each token's pages, and each run's, as a bit
 // set; the loading warp goes through a run's set and leaves each key tile's pages and the tokens that have them
 // in a small ring.  That and the loads (64 KB a key tile) take the loading warp about 3000 cycles, and two row tiles' products
-// as long (one row tile an item: 160 us for pieces of 1045 tokens).
+// as long (one row tile an item: 160 us for pieces of 1045 tokens).  Those, of 28/4 heads of 128, 48 pages of 32 each, take 151 us: 23 GFLOP
+// for the pairs that tokens see, 28 % of an SM's tensor cycles over the whole unions, 29 MB of DRAM (one by one: 232 us).
 // ---------------------------------------------------------------------------
 
 constexpr int kUnionWidth = 4096;               // pages of a table row that a bit set holds
@@ -690,6 +691,7 @@ cudaError_t launch_bf16(const PagesArgs &a, int grid, cudaStream_t s) {
     if ((long long)a.T * a.group >= 64LL * a.at.n_seq && a.at.table_width <= kUnionWidth &&
         (((long long)a.T * a.n_kv_heads * a.n_keep) << a.at.page_shift) >= 3000000)
         return a.group >= 4 ? launch_union<D, 2>(a, grid, s) : launch_union<D, 8>(a, grid, s);
+    // (row tiles of as few rows as the group needs: the products of 8 more cost as much as the first)
     if (a.group <= 8) return launch_few<D, 1>(a, grid, s);
     return a.group <= 16 ? launch_few<D, 2>(a, grid, s) : launch_few<D, few::max_rows(D) / 8>(a, grid, s);
 }

@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(few::kThreads, 2) k_shared_few32(const SharedA
 
 // ---------------------------------------------------------------------------
 // Join: half a warp a row.  What costs is latency, a row's own chain of loads (6 us) several times over: so the pieces of
-// both parts are one list, and the rows of most calls are in flight at once.
+// both parts are one list, and the rows of most calls are in flight at once.  6144 rows of 128 in 10 pieces: 13 us alone, 22 MB read.
 // ---------------------------------------------------------------------------
 
 constexpr int kJoinWarps = 4;
@@ -701,7 +701,7 @@ cudaError_t launch_f32(SharedArgs a, cudaStream_t s) {
         if (few_kind[k]) a.parts[k] = a.part_few, a.rows_max[k] = few::max_rows(D);
     }
     a.split = few_own && !few_pre;
-    a.least = 1;  // (16 sequences on 1024: 26.6 us, with 2 29.9)
+    a.least = few_own ? 1 : kLeastFew;  // (16 sequences of 8 rows on 1024: 26.6 us, with 2 29.9; 5 of 19 rows 29.2 and 29.0)
     a.place[0] = kPlaceRows, a.place[1] = kPlaceFew32;
     cudaError_t e = cudaSuccess;
     if (!few_pre) {
@@ -750,7 +750,10 @@ cudaError_t launch_few(const SharedArgs &a, int which, cudaStream_t s) {
 
 template <int D>
 cudaError_t launch_bf16(SharedArgs a, cudaStream_t s) {
-    // rows of the mean group and of the mean sequence
+    // Rows of the mean group and of the mean sequence.  Few-row warps for own positions: 96 sequences on 24576 shared positions
+    // 126 us, all on the tensor cores 153; for a small group's prefix too: 4 sequences of one row on 1024 positions 18.6 us, the prefix on
+    // the tensor cores 23.1.  One row tile an item: those 96 sequences' 768 rows 147 us, draft trees of 33 tokens 63 (two: 54); groups of 96 rows
+    // on 16384 positions 40.0 us (two, the second empty: 40.9), of 84 on 30000 51.2 (52.6).
     const long long rows = (long long)a.T * a.group, per_group = rows / a.n_groups, per_seq = rows / a.n_seq;
     const bool one = per_group <= 128;
     constexpr int kFewRows = few::max_rows(D);
