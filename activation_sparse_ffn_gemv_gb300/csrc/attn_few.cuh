@@ -16,8 +16,9 @@
 // 16 products of D = 128 for every 8 rows.  48 tokens of up to 2048 chosen positions, 32/8 heads of 128: 298 MB in 54 us with the
 // join, 5.5 TB/s, 0.82 of a copy's rate (a tcgen05 tile an item: 68); 14 % of the issue slots.
 //
-// A weight of zero times an infinite or NaN value would be NaN: where a tile has keys that some row does not see and
-// V holds such a value, its product is made value by value, leaving out what a row does not see.
+// A weight of zero times an infinite or NaN value would be NaN: where a tile has keys that some row does not see, such
+// values become zeros before the product and are added by themselves to the rows that see them.  The sums of a row
+// are then the same whatever lies in places that it does not see, or in the half of a tile that a lone page of 8 leaves as it was.
 #pragma once
 
 #include "attn.cuh"
@@ -83,7 +84,10 @@ SFFN_DEV void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-SFFN_DEV bool nonfinite2(uint32_t w) { return (((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0; }
+// The halves of two bf16 that are infinite or NaN (their sign bits), whether there is one, and zeros in their place.
+SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+SFFN_DEV bool nonfinite2(uint32_t w) { return nonfinite_bits(w) != 0; }
+SFFN_DEV uint32_t finite2(uint32_t w) { return w & ~((nonfinite_bits(w) >> 15) * 0xffffu); }
 
 // A tile load and the announcement of its bytes, issued by one lane of a converged warp: the operands are the same in every
 // lane, and as the compiler sees that, they go straight to the uniform registers that the instruction takes.
@@ -312,48 +316,51 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
                 pt[n][0] = transpose8(pack_bf16(p[n][0], p[n][1]));
                 pt[n][1] = transpose8(pack_bf16(p[n][2], p[n][3]));
             }
-            bool plain = true;
             if (masked) {
+                // One product, whatever a row does not see: non-finite values become zeros in the tile, and are added by
+                // themselves to the rows that see them.
+                uint4 *v = reinterpret_cast<uint4 *>(ring + st * 2 * C::kTile + C::kTile);
                 bool bad = false;
-                const uint4 *v = reinterpret_cast<const uint4 *>(ring + st * 2 * C::kTile + C::kTile);
                 for (int e = lane; e < C::kTile / 16; e += 32) {
                     const uint4 x = v[e];
                     bad |= nonfinite2(x.x) || nonfinite2(x.y) || nonfinite2(x.z) || nonfinite2(x.w);
                 }
-                plain = !__any_sync(0xffffffffu, bad);
-            }
-            if (plain) {
-#pragma unroll
-                for (int k = 0; k < KB; ++k) {
-                    uint32_t a[4];
-                    ldmatrix4_trans(((vt + v_lane) ^ ((k & 3) << 5)) + (k >> 2) * 1024, a);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma(o[n][k], a, pt[n][0], pt[n][1]);
-                }
-            } else {
+                if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll 1
-                for (int j = 0; j < kKeys; ++j) {
-                    const int src = (j & 7) * 4 + c;
+                    for (int j = 0; j < kKeys; ++j) {
+                        const int src = (j & 7) * 4 + c;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const bool hi = j >= 8;
-                        const float x0 = __shfl_sync(0xffffffffu, hi ? p[n][2] : p[n][0], src),
-                                    x1 = __shfl_sync(0xffffffffu, hi ? p[n][3] : p[n][1], src);
-                        const uint32_t vis = __shfl_sync(0xffffffffu, seen, src) >> (4 * n + (hi ? 2 : 0));
-                        const float w0 = __bfloat162float(__float2bfloat16_rn(x0)), w1 = __bfloat162float(__float2bfloat16_rn(x1));
+                        for (int n = 0; n < NT; ++n) {
+                            const uint32_t vis = __shfl_sync(0xffffffffu, seen, src) >> (4 * n + (j >> 3) * 2);
 #pragma unroll
-                        for (int k = 0; k < KB; ++k)
+                            for (int k = 0; k < KB; ++k)
 #pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const int d = k * 16 + g + half * 8;
-                                const uint16_t b = *reinterpret_cast<const uint16_t *>(ring + st * 2 * C::kTile + C::kTile +
-                                                                                       at(j, d & ~7) + (d & 7) * 2);
-                                const float v = __uint_as_float((uint32_t)b << 16);
-                                if (vis & 1) o[n][k][half * 2] += w0 * v;
-                                if (vis & 2) o[n][k][half * 2 + 1] += w1 * v;
-                            }
+                                for (int half = 0; half < 2; ++half) {
+                                    const int d = k * 16 + g + half * 8;
+                                    const uint16_t b = *reinterpret_cast<const uint16_t *>(
+                                        reinterpret_cast<const unsigned char *>(v) + at(j, d & ~7) + (d & 7) * 2);
+                                    if ((b & 0x7f80u) != 0x7f80u) continue;
+                                    const float x = __uint_as_float((uint32_t)b << 16);
+                                    if (vis & 1) o[n][k][half * 2] += x;
+                                    if (vis & 2) o[n][k][half * 2 + 1] += x;
+                                }
+                        }
                     }
+                    __syncwarp();
+                    for (int e = lane; e < C::kTile / 16; e += 32) {
+                        const uint4 x = v[e];
+                        v[e] = make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+                    }
+                    fence_proxy_async_smem();  // (before a later copy into the slot)
+                    __syncwarp();
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                uint32_t a[4];
+                ldmatrix4_trans(((vt + v_lane) ^ ((k & 3) << 5)) + (k >> 2) * 1024, a);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma(o[n][k], a, pt[n][0], pt[n][1]);
             }
             __syncwarp();  // every lane has read the tile
             issue();
