@@ -150,11 +150,11 @@ struct JoinedRow {
 #pragma unroll
         for (int i = 0; i < C; ++i) o[i] = 0.f;
     }
-    // Pieces 0 .. n - 1: sums_of(i) points to a piece's (maximum, sum), row_of(i) to its unnormalised row.
+    // Pieces i0 .. i1: sums_of(i) points to a piece's (maximum, sum), row_of(i) to its unnormalised row.
     template <typename Sums, typename Row>
-    SFFN_DEV void add(int n_all, int lane, Sums sums_of, Row row_of) {
-        for (int b = 0; b < n_all; b += 32) {  // 32 pieces at a time
-            const int n = min(32, n_all - b);
+    SFFN_DEV void add(int i0, int i1, int lane, Sums sums_of, Row row_of) {
+        for (int b = i0; b <= i1; b += 32) {  // 32 pieces at a time
+            const int n = min(32, i1 - b + 1);
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(sums_of(b + lane)));
             const float Mn = fmaxf(M, warp_max(ml.x)), ref = Mn == -INFINITY ? 0.f : Mn;

@@ -610,11 +610,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_pages_join(const PagesArgs 
     const int w0 = cut.z, w1 = cut.w, blocks = (w1 - w0) * parts, b = (w - w0 - 1) * parts + part;
     const size_t sf = tree_slot_floats(a.row_tile, D);
     const int h = cut.y / a.tiles, r0 = cut.y % a.tiles * a.row_tile, rows = min(a.row_tile, a.group - r0);
-    auto slot = [&](int k) { return a.part + sf * (size_t)(2 * (w0 + k) + (k == 0 ? 1 : 0)); };
+    auto slot = [&](int w) { return a.part + sf * (size_t)(2 * w + (w == w0 ? 1 : 0)); };
     for (int r = b * kJoinWarps + (threadIdx.x >> 5); r < rows; r += blocks * kJoinWarps) {
         JoinedRow<D / 32> j;
-        j.add(w1 - w0 + 1, lane, [&](int k) { return slot(k) + (size_t)a.row_tile * D + 2 * r; },
-              [&](int k) { return slot(k) + (size_t)r * D; });
+        j.add(w0, w1, lane, [&](int w) { return slot(w) + (size_t)a.row_tile * D + 2 * r; },
+              [&](int w) { return slot(w) + (size_t)r * D; });
         j.write(static_cast<T *>(a.out) + ((size_t)cut.x * a.n_heads + (size_t)h * a.group + r0 + r) * D, lane);
     }
 }

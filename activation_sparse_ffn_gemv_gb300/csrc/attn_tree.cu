@@ -238,8 +238,8 @@ SFFN_DEV void join_row(const TreeArgs &a, long long row, int w0, int w1, int r, 
     const size_t sf = tree_slot_floats(a.rows_max, D);
     auto slot = [&](int w) { return a.part + sf * (size_t)(2 * w + (w == w0 ? 1 : 0)); };
     JoinedRow<D / 32> j;
-    j.add(w1 - w0 + 1, lane, [&](int i) { return slot(w0 + i) + (size_t)a.rows_max * D + 2 * r; },
-          [&](int i) { return slot(w0 + i) + (size_t)r * D; });
+    j.add(w0, w1, lane, [&](int w) { return slot(w) + (size_t)a.rows_max * D + 2 * r; },
+          [&](int w) { return slot(w) + (size_t)r * D; });
     j.write(static_cast<T *>(a.out) + (size_t)row * D, lane);
 }
 
