@@ -498,6 +498,13 @@ def _vec(t, n: int, dtype, where: str):
     return t.data_ptr()
 
 
+def _shaped(t: torch.Tensor, shape, where: str):
+    """An array of at least shape[0] entries whose other sizes are exactly `shape`'s: what the next call takes
+    its rows by."""
+    if t.dim() != len(shape) or t.shape[0] < shape[0] or t.shape[1:] != tuple(shape[1:]):
+        raise SffnError(ERR_SHAPE, where)
+
+
 def _space(workspace, where: str):
     """Address and bytes of a workspace: contiguous device memory of any type."""
     if not workspace.is_cuda or not workspace.is_contiguous():
@@ -699,6 +706,8 @@ def page_bounds(cache: KVCache, pages: torch.Tensor, bounds=None, workspace=None
     where = "sffn_page_bounds"
     _here(cache.k, where)
     n, hkv, D = pages.numel(), cache.n_kv_heads, cache.head_dim
+    if bounds is not None:
+        _shaped(bounds, (cache.n_pages, hkv, 2, D), where)
     with _made_on(stream):
         if bounds is None:
             bounds = torch.zeros((cache.n_pages, hkv, 2, D), dtype=torch.bfloat16, device=cache.k.device)
@@ -722,8 +731,9 @@ def page_select(q: torch.Tensor, cache: KVCache, bounds: torch.Tensor, page_tabl
                 positions: torch.Tensor, n_keep: int, n_first: int = 1, n_recent: int = 1, sel=None, n_sel=None,
                 workspace=None, stream=None):
     """The n_keep pages that each token of q [T, n_heads, D] reads, per key head: the first n_first, the last n_recent
-    and those with the largest scores against their key bounds.  seqs, positions int32 [T]: each token's row
-    of page_table [n_seq, width] and its position.  Returns (sel [T, n_kv_heads, n_keep] ascending, then -1; n_sel [T])."""
+    and those with the largest scores against their key bounds.  bounds: [n_pages, n_kv_heads, 2, D] as page_bounds makes it;
+    seqs, positions int32 [T]: each token's row of page_table [n_seq, width] and its position; sel: int32 [T or more,
+    n_kv_heads, n_keep], n_sel: int32 [T or more].  Returns (sel [T, n_kv_heads, n_keep] ascending, then -1; n_sel [T])."""
     where = "sffn_page_select"
     qshape, dt = q.shape, q.dtype
     qs = _rows(q, qshape, where)
@@ -735,6 +745,9 @@ def page_select(q: torch.Tensor, cache: KVCache, bounds: torch.Tensor, page_tabl
     _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
     n_seq, width = page_table.shape
     i32 = torch.int32
+    _shaped(bounds, (cache.n_pages, hkv, 2, D), where)
+    if sel is not None:
+        _shaped(sel, (T, hkv, n_keep), where)
     with _made_on(stream):
         if sel is None:
             sel = torch.empty((T, hkv, max(n_keep, 0)), dtype=i32, device=q.device)
