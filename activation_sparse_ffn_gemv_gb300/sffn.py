@@ -489,11 +489,13 @@ def _rows(t: torch.Tensor, shape, where: str) -> int:
     return st if T > 1 else H * D
 
 
-def _vec(t, n: int, dtype, where: str):
-    """Address of a contiguous device array of n (or more) elements of one type, or None."""
+def _vec(t, n: int, dtype, where: str, dev=None):
+    """Address of a contiguous device array of n (or more) elements of one type, or None.  dev: the device that it has
+    to be on."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() < n or not t.is_cuda or not t.is_contiguous():
+    if (t.dtype is not dtype or t.numel() < n or not (t.is_cuda if dev is None else t.get_device() == dev)
+            or not t.is_contiguous()):
         raise SffnError(ERR_INVALID_ARG, where)
     return t.data_ptr()
 
@@ -505,9 +507,9 @@ def _shaped(t: torch.Tensor, shape, where: str):
         raise SffnError(ERR_SHAPE, where)
 
 
-def _space(workspace, where: str):
-    """Address and bytes of a workspace: contiguous device memory of any type."""
-    if not workspace.is_cuda or not workspace.is_contiguous():
+def _space(workspace, where: str, dev=None):
+    """Address and bytes of a workspace: contiguous device memory of any type (dev: of that device)."""
+    if not (workspace.is_cuda if dev is None else workspace.get_device() == dev) or not workspace.is_contiguous():
         raise SffnError(ERR_WORKSPACE, where)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
@@ -530,10 +532,12 @@ def _made_on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
 
-def _here(t: torch.Tensor, where: str):
-    """A call runs on the current device: its tensors have to be there."""
-    if t.device.index != torch.cuda.current_device():
+def _here(t: torch.Tensor, where: str) -> int:
+    """A call runs on the current device: its tensors have to be there.  Returns that device."""
+    dev = torch.cuda.current_device()
+    if t.device.index != dev:
         raise SffnError(ERR_INVALID_ARG, where)
+    return dev
 
 
 class KVCache:
@@ -542,7 +546,7 @@ class KVCache:
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.dtype in _TDTYPE and k.is_cuda
-              and v.is_cuda and k.is_contiguous() and v.is_contiguous(), ERR_INVALID_ARG, "KVCache")
+              and v.is_cuda and k.device == v.device and k.is_contiguous() and v.is_contiguous(), ERR_INVALID_ARG, "KVCache")
         self.k, self.v = k, v
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
         self.c = KVCacheStruct(_TDTYPE[k.dtype], self.n_kv_heads, self.head_dim, self.page_size, self.n_pages,
@@ -678,8 +682,8 @@ def attn_shared(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_l
     where = "sffn_attn_shared"
     qshape, dt = q.shape, q.dtype
     qs = _rows(q, qshape, where)
-    _here(q, where)
-    _here(cache.k, where)
+    dev = _here(q, where)
+    _need(cache.k.get_device() == dev, ERR_INVALID_ARG, where)
     T, hq, D = qshape
     _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
     _need(page_table.dim() == 2, ERR_INVALID_ARG, where)
@@ -691,11 +695,13 @@ def attn_shared(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_l
         if workspace is None:
             workspace = alloc_attn_workspace(WS_ATTN_SHARED, T, n_seq, hq, cache.n_kv_heads, D, q.device)
     i32 = torch.int32
-    st = lib().sffn_attn_shared(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where), width,
-                                _vec(ctx_lens, n_seq, i32, where), _vec(cu_tokens, n_seq + 1, i32, where), n_seq,
-                                _vec(group_seqs, n_groups + 1, i32, where), _vec(prefix_lens, 0, i32, where), n_groups,
-                                _vec(tree_mask, T, torch.int64, where), D ** -0.5 if scale is None else scale,
-                                _vec(out, T * hq * D, dt, where), *_space(workspace, where), _launch_stream(stream))
+    st = lib().sffn_attn_shared(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where, dev), width,
+                                _vec(ctx_lens, n_seq, i32, where, dev), _vec(cu_tokens, n_seq + 1, i32, where, dev), n_seq,
+                                _vec(group_seqs, n_groups + 1, i32, where, dev),
+                                _vec(prefix_lens, 0, i32, where, dev), n_groups,
+                                _vec(tree_mask, T, torch.int64, where, dev), D ** -0.5 if scale is None else scale,
+                                _vec(out, T * hq * D, dt, where, dev), *_space(workspace, where, dev),
+                                _launch_stream(stream))
     _check(st, where)
     return out
 
@@ -704,7 +710,7 @@ def page_bounds(cache: KVCache, pages: torch.Tensor, bounds=None, workspace=None
     """Key bounds of the pages listed (int32 [n]; -1: nothing to do), into bounds: bf16 [n_pages, n_kv_heads, 2, D],
     largest keys, then least (zeros where not listed, if none are given).  Returns bounds."""
     where = "sffn_page_bounds"
-    _here(cache.k, where)
+    dev = _here(cache.k, where)
     n, hkv, D = pages.numel(), cache.n_kv_heads, cache.head_dim
     if bounds is not None:
         _shaped(bounds, (cache.n_pages, hkv, 2, D), where)
@@ -713,9 +719,9 @@ def page_bounds(cache: KVCache, pages: torch.Tensor, bounds=None, workspace=None
             bounds = torch.zeros((cache.n_pages, hkv, 2, D), dtype=torch.bfloat16, device=cache.k.device)
         if workspace is None:
             workspace = alloc_attn_workspace(WS_PAGE_BOUNDS, n, 1, hkv, hkv, D, cache.k.device)
-    st = lib().sffn_page_bounds(cache.ref(), _vec(pages, 0, torch.int32, where), n,
-                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where),
-                                *_space(workspace, where), _launch_stream(stream))
+    st = lib().sffn_page_bounds(cache.ref(), _vec(pages, 0, torch.int32, where, dev), n,
+                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where, dev),
+                                *_space(workspace, where, dev), _launch_stream(stream))
     _check(st, where)
     return bounds
 
@@ -737,8 +743,8 @@ def page_select(q: torch.Tensor, cache: KVCache, bounds: torch.Tensor, page_tabl
     where = "sffn_page_select"
     qshape, dt = q.shape, q.dtype
     qs = _rows(q, qshape, where)
-    _here(q, where)
-    _here(cache.k, where)
+    dev = _here(q, where)
+    _need(cache.k.get_device() == dev, ERR_INVALID_ARG, where)
     T, hq, D = qshape
     hkv = cache.n_kv_heads
     _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
@@ -756,11 +762,11 @@ def page_select(q: torch.Tensor, cache: KVCache, bounds: torch.Tensor, page_tabl
         if workspace is None:
             workspace = alloc_page_select_workspace(T, hkv, width, q.device)
     st = lib().sffn_page_select(q.data_ptr(), qs, T, hq, cache.ref(),
-                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where),
-                                _vec(page_table, 0, i32, where), width, n_seq, _vec(seqs, T, i32, where),
-                                _vec(positions, T, i32, where), n_first, n_recent, n_keep,
-                                _vec(sel, T * hkv * n_keep, i32, where), _vec(n_sel, T, i32, where),
-                                *_space(workspace, where), _launch_stream(stream))
+                                _vec(bounds, cache.n_pages * hkv * 2 * D, torch.bfloat16, where, dev),
+                                _vec(page_table, 0, i32, where, dev), width, n_seq, _vec(seqs, T, i32, where, dev),
+                                _vec(positions, T, i32, where, dev), n_first, n_recent, n_keep,
+                                _vec(sel, T * hkv * n_keep, i32, where, dev), _vec(n_sel, T, i32, where, dev),
+                                *_space(workspace, where, dev), _launch_stream(stream))
     _check(st, where)
     return sel, n_sel
 
@@ -772,8 +778,8 @@ def attn_pages(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seqs: 
     where = "sffn_attn_pages"
     qshape, dt = q.shape, q.dtype
     qs = _rows(q, qshape, where)
-    _here(q, where)
-    _here(cache.k, where)
+    dev = _here(q, where)
+    _need(cache.k.get_device() == dev, ERR_INVALID_ARG, where)
     T, hq, D = qshape
     hkv = cache.n_kv_heads
     _need(dt is cache.k.dtype and D == cache.head_dim, ERR_INVALID_ARG, where)
@@ -787,9 +793,10 @@ def attn_pages(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seqs: 
             out = torch.empty((T, hq, D), dtype=dt, device=q.device)
         if workspace is None:
             workspace = alloc_attn_workspace(WS_ATTN_PAGES, T, n_seq, hq, hkv, D, q.device)
-    st = lib().sffn_attn_pages(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where), width, n_seq,
-                               _vec(seqs, T, i32, where), _vec(positions, T, i32, where), _vec(sel, 0, i32, where),
-                               _vec(n_sel, T, i32, where), n_keep, D ** -0.5 if scale is None else scale,
-                               _vec(out, T * hq * D, dt, where), *_space(workspace, where), _launch_stream(stream))
+    st = lib().sffn_attn_pages(q.data_ptr(), qs, T, hq, cache.ref(), _vec(page_table, 0, i32, where, dev), width, n_seq,
+                               _vec(seqs, T, i32, where, dev), _vec(positions, T, i32, where, dev),
+                               _vec(sel, 0, i32, where, dev), _vec(n_sel, T, i32, where, dev), n_keep,
+                               D ** -0.5 if scale is None else scale, _vec(out, T * hq * D, dt, where, dev),
+                               *_space(workspace, where, dev), _launch_stream(stream))
     _check(st, where)
     return out
