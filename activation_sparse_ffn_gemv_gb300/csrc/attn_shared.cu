@@ -127,6 +127,7 @@ struct Line {
         return i < n_groups ? prefix_part(a, i) : own_part(a, i - n_groups, record);
     }
     SFFN_DEV void build(const SharedArgs &a, bool record) const {
+        bool falls = false;
         for (int g = threadIdx.x; g <= n_groups; g += blockDim.x) {
             const int s0 = a.group_seqs[g];
             seqs[g] = s0;
@@ -134,11 +135,16 @@ struct Line {
             const int s1 = a.group_seqs[g + 1], p = a.prefix_lens[g];
             const bool ok = s0 >= 0 && s1 >= s0 && s1 <= a.n_seq && p >= 0 && (p >> a.page_shift) <= a.table_width &&
                             p <= kTreeMaxCtx;
+            falls |= s1 < s0;
             whole[g] = ok ? (p >> a.page_shift) << a.page_shift : -1;
             tok0[g] = ok ? min(max(a.cu_tokens[s0], 0), a.T) : 0;
             tok1[g] = ok ? min(max(a.cu_tokens[s1], 0), a.T) : 0;
         }
-        __syncthreads();
+        // Where group_seqs falls, other groups may have the same sequences, and both would write their tokens' rows: none counts.
+        if (__syncthreads_or(falls)) {
+            for (int g = threadIdx.x; g < n_groups; g += blockDim.x) whole[g] = -1;
+            __syncthreads();
+        }
         line_prefix(entries, pre, scratch, [&](int i) {
             const Part p = part(a, i, record);
             return (long long)p.tiles * a.n_kv_heads * p.span();

@@ -517,7 +517,7 @@ sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, 
  *                page are read from each sequence's own row.
  * A sequence of a group that is not a range of sequences, whose prefix is negative or longer than its table's row, or
  * whose whole prefix pages hold more than its ctx_lens positions, is skipped and recorded like one that breaks
- * sffn_attn_tree's rules.
+ * sffn_attn_tree's rules; where group_seqs is not ascending, all sequences are.
  * 0 <= T <= 65536 (0: a no-op), 1 <= n_seq <= 1024, 1 <= n_groups <= 256. */
 sffn_status sffn_attn_shared(const void *q, int64_t q_stride, int T, int n_heads, const sffn_kv_cache *cache,
                              const int32_t *page_table, int table_width, const int32_t *ctx_lens,
