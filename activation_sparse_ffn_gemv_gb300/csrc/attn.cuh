@@ -31,15 +31,13 @@ constexpr int kTreeItemCost = 5;
 constexpr int kTreeMaxTokens = 64;
 constexpr int kTreeMaxCtx = 0x7fff0000;  // positions stay below 2^31 with room for a tile
 
-struct TreeSeq {
+struct SeqTokens {
     int t0, n, ctx;   // first new token, new tokens, committed positions
-    int tiles, units; // row tiles, units of each item
-    SFFN_DEV int span() const { return units + kTreeItemCost; }  // an item's length on the line
 };
 
-// A sequence's numbers, checked; one that breaks the contract has no rows.
-SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
-    TreeSeq q;
+// A sequence's numbers, checked; one that breaks the contract has no tokens.
+SFFN_DEV SeqTokens seq_tokens(const SeqArgs &a, int s, bool record) {
+    SeqTokens q;
     q.t0 = a.cu_tokens[s];
     const int t1 = a.cu_tokens[s + 1];
     q.ctx = a.ctx_lens[s];
@@ -48,12 +46,22 @@ SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
                     q.ctx + n <= ((long long)a.table_width << a.page_shift) && q.ctx <= kTreeMaxCtx;
     if (!ok) {
         if (record) record_error(a.err, SFFN_ERR_DEVICE);
-        q.t0 = q.n = q.ctx = q.tiles = q.units = 0;
+        q.t0 = q.n = q.ctx = 0;
         return q;
     }
     q.n = (int)n;
+    return q;
+}
+
+struct TreeSeq : SeqTokens {
+    int tiles, units; // row tiles, units of each item
+    SFFN_DEV int span() const { return units + kTreeItemCost; }  // an item's length on the line
+};
+SFFN_DEV TreeSeq tree_seq(const TreeArgs &a, int s, bool record) {
+    TreeSeq q;
+    static_cast<SeqTokens &>(q) = seq_tokens(a, s, record);
     q.tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens;
-    q.units = (int)((q.ctx + n + kTreeUnit - 1) / kTreeUnit);
+    q.units = (int)(((long long)q.ctx + q.n + kTreeUnit - 1) / kTreeUnit);
     return q;
 }
 

@@ -105,7 +105,7 @@ struct Line {
         p.row = s;
         p.rows = a.tile_rows[1];
         p.cost = a.cost[1];
-        const TreeSeq q = tree_seq(a, s, record);
+        const SeqTokens q = seq_tokens(a, s, record);
         const int g = group_of(s), w = whole[g];
         p.group = g;
         if (s < seqs[g] || s >= seqs[g + 1] || w < 0 || a.ctx_lens[s] < w ||

@@ -183,7 +183,8 @@ struct PromptArgs {
 sffn_status run_attn_prompt(const PromptArgs &a, int head_dim, cudaStream_t s);
 
 constexpr int kTreeMaxSeq = 1024;  // sequences of one sffn_attn_tree call
-struct TreeArgs {
+// New tokens of sequences whose context is in the paged cache (sffn_attn_tree, sffn_attn_shared).
+struct SeqArgs {
     const void *q;
     long long q_stride;
     int T, n_heads, n_kv_heads, group;
@@ -196,10 +197,12 @@ struct TreeArgs {
     const uint64_t *tree_mask;
     float scale;
     void *out;
+    int32_t *err;
+};
+struct TreeArgs : SeqArgs {
     float *part;       // partial results of cut items
     int tile_tokens;   // new tokens of a row tile
     int rows_max;      // rows of a partial result slot
-    int32_t *err;
 };
 struct TreePlan {
     int grid, tile_tokens, rows_max;
@@ -213,7 +216,7 @@ sffn_status run_attn_tree(const TreeArgs &a, const TreePlan &p, int dtype, int h
 // ---------------------------------------------------------------------------
 
 constexpr int kSharedMaxGroups = 256;  // groups of one sffn_attn_shared call
-struct SharedArgs : TreeArgs {
+struct SharedArgs : SeqArgs {
     const int32_t *group_seqs, *prefix_lens;
     int n_groups;
     int sms;                // SMs
