@@ -89,24 +89,13 @@ SFFN_DEV uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x008
 SFFN_DEV bool nonfinite2(uint32_t w) { return nonfinite_bits(w) != 0; }
 SFFN_DEV uint32_t finite2(uint32_t w) { return w & ~((nonfinite_bits(w) >> 15) * 0xffffu); }
 
-// A tile load and the announcement of its bytes, issued by one lane of a converged warp: the operands are the same in every
-// lane, and as the compiler sees that, they go straight to the uniform registers that the instruction takes.
-SFFN_DEV void load_warp(uint32_t dst, const CUtensorMap *map, int group, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;\n\t}\n" ::"r"(dst),
-        "l"(map), "r"(0), "r"(group), "r"(bar), "l"(policy)
-        : "memory");
-}
-SFFN_DEV void expect_warp(uint32_t bar, uint32_t bytes) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
-        "r"(bytes)
-        : "memory");
+// At a warp's end: where it gave up, copies of its own may be in flight, and the CTA waits for those before it exits (one more
+// second for all of them together).  A wait that runs out ends its own warp's loads and stores; the other warps have rings and
+// waits of their own.
+template <int NS>
+SFFN_DEV void drain(uint64_t (&full)[NS], int landed, int issued) {
+    uint64_t end = 0;
+    for (int i = landed; i < issued; ++i) mbar_wait_until(&full[i % NS], (uint32_t)((i / NS) & 1), end);
 }
 
 // P: the policy.  It gives
@@ -175,12 +164,12 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
         const int g0 = group(__shfl_sync(0xffffffffu, pages[0], li & 31), key), two = box < kKeys && key + box < lw.k1;
         const int g1 = two ? group(__shfl_sync(0xffffffffu, pages[1], li & 31), key + box) : 0;
         const uint32_t bar = smem_u32(&full[warp][islot]), dst = ring_addr + (uint32_t)(islot * 2 * C::kTile);
-        expect_warp(bar, (uint32_t)((1 + two) * box * D * 4));
-        load_warp(dst, &map_k, g0, bar, keep);
-        load_warp(dst + C::kTile, &map_v, g0, bar, keep);
+        tc::mbar_expect_tx_warp(bar, (uint32_t)((1 + two) * box * D * 4));
+        tc::tma_load_rows_warp(dst, &map_k, g0, bar, keep);
+        tc::tma_load_rows_warp(dst + C::kTile, &map_v, g0, bar, keep);
         if (two) {
-            load_warp(dst + box * D * 2, &map_k, g1, bar, keep);
-            load_warp(dst + C::kTile + box * D * 2, &map_v, g1, bar, keep);
+            tc::tma_load_rows_warp(dst + box * D * 2, &map_k, g1, bar, keep);
+            tc::tma_load_rows_warp(dst + C::kTile + box * D * 2, &map_v, g1, bar, keep);
         }
         ++li;
         ++issued;
@@ -401,8 +390,7 @@ SFFN_DEV void attention(P &policy, const CUtensorMap &map_k, const CUtensorMap &
             }
         }
     }
-    // no copy is in flight when the CTA exits, whoever gave up
-    for (int i = landed; i < issued; ++i) mbar_wait(&full[warp][i % NS], (uint32_t)((i / NS) & 1));
+    drain<NS>(full[warp], landed, issued);
 }
 
 // ---------------------------------------------------------------------------
@@ -639,7 +627,7 @@ SFFN_DEV void attention_f32(P &policy, const void *ck, const void *cv, int page_
             if (partial && lane == 0) *policy.part_sums(w, w.r0 + r, r) = make_float2(mr * scale, lr);
         }
     }
-    for (int i = landed; i < issued; ++i) mbar_wait(&full[warp][i % NS], (uint32_t)((i / NS) & 1));
+    drain<NS>(full[warp], landed, issued);
 }
 
 }  // namespace few

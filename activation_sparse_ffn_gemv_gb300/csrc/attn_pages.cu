@@ -517,9 +517,9 @@ struct UnionPolicy {
                     (((j * atc::kKeys + lane * box) & (ps - 1)) >> 3);
         }
         const uint32_t to = smem_u32(dst), at = smem_u32(bar);
-        few::expect_warp(at, (uint32_t)(boxes * box * 128 * H));
+        tc::mbar_expect_tx_warp(at, (uint32_t)(boxes * box * 128 * H));
         for (int b = 0; b < boxes; ++b)
-            few::load_warp(to + b * box * 128 * H, map, __shfl_sync(0xffffffffu, group, b), at, pol);
+            tc::tma_load_rows_warp(to + b * box * 128 * H, map, __shfl_sync(0xffffffffu, group, b), at, pol);
     }
     SFFN_DEV bool exists(const atc::Work &w, int j, int row) const {
         const TilePages &info = ring[(w.base + j) % kTileRing];

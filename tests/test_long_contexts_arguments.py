@@ -1,5 +1,5 @@
-"""sffn_attn_shared's kernels have no tile size of sffn_attn_tree's to divide by (it is zero in such a call): the arguments that both
-share hold none, and so does what checks a sequence's numbers for both."""
+"""sffn_attn_shared's kernels have no tile size of sffn_attn_tree's to divide by (it is zero in such a call): the
+arguments that both share hold none, and so does what checks a sequence's numbers for both."""
 from __future__ import annotations
 
 import os

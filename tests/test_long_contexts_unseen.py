@@ -47,6 +47,9 @@ def test_attn_pages_partial_results(S, lens, at, hq, hkv, D, page, dt, bad):  # 
     ([3, 1], [500, 0], [10, 333, 0, 700], [1, 2, 1, 1], 8, 4, 128, 16),
     ([2, 2], [64, 129], [1001, 3, 60, 515], [3, 1, 2, 2], 4, 2, 64, 8),
     ([5], [900], [5, 1, 300, 2, 90], [1, 1, 1, 1, 1], 32, 2, 64, 64),
+    ([30], [530], [(17 * i) % 90 for i in range(30)], [1] * 30, 16, 2, 128, 32),   # the prefix on the tensor cores
+    ([2, 1], [640, 0], [7, 100, 900], [40, 33, 64], 8, 2, 64, 16),                 # all of it
+    ([1], [300], [1700], [20], 7, 1, 128, 128),
 ])
 def test_attn_shared_partial_results(S, groups, prefix, own, n, hq, hkv, D, page, dt, bad):  # noqa: F811
     of = [x for m, x in zip(groups, prefix) for _ in range(m)]
