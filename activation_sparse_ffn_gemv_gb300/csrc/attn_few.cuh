@@ -90,12 +90,11 @@ SFFN_DEV bool nonfinite2(uint32_t w) { return nonfinite_bits(w) != 0; }
 SFFN_DEV uint32_t finite2(uint32_t w) { return w & ~((nonfinite_bits(w) >> 15) * 0xffffu); }
 
 // At a warp's end: where it gave up, copies of its own may be in flight, and the CTA waits for those before it exits (one more
-// second for all of them together).  A wait that runs out ends its own warp's loads and stores; the other warps have rings and
+// second for all of them, in equal shares).  A wait that runs out ends its own warp's loads and stores; the other warps have rings and
 // waits of their own.
 template <int NS>
 SFFN_DEV void drain(uint64_t (&full)[NS], int landed, int issued) {
-    uint64_t end = 0;
-    for (int i = landed; i < issued; ++i) mbar_wait_until(&full[i % NS], (uint32_t)((i / NS) & 1), end);
+    for (int i = landed; i < issued; ++i) mbar_wait(&full[i % NS], (uint32_t)((i / NS) & 1), kWaitLimitNs / NS);
 }
 
 // P: the policy.  It gives

@@ -274,11 +274,11 @@ SFFN_DEV void attention_cta(P &policy, const CUtensorMap &map_q, const CUtensorM
             __syncwarp();
             if (!more || !load(w)) break;
         }
-        if (lane == 0) {  // no copy is in flight when the CTA exits, whoever gave up (one more second for all of them)
-            uint64_t end = 0;
-            for (int j = max(0, it - NS); j < it; ++j) mbar_wait_until(&kv_full[j % NS], (uint32_t)((j / NS) & 1), end);
+        if (lane == 0) {  // no copy is in flight when the CTA exits, whoever gave up (one more second for all, in equal shares)
+            constexpr uint64_t share = kWaitLimitNs / (NS + 2);
+            for (int j = max(0, it - NS); j < it; ++j) mbar_wait(&kv_full[j % NS], (uint32_t)((j / NS) & 1), share);
             for (int t = 0; t < 2; ++t)
-                if (qn[t]) mbar_wait_until(&q_full[t], (uint32_t)((qn[t] - 1) & 1), end);
+                if (qn[t]) mbar_wait(&q_full[t], (uint32_t)((qn[t] - 1) & 1), share);
         }
     } else if (warp == 1) {
         // ---------------- tensor cores ----------------

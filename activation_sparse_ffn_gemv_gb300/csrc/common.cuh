@@ -106,15 +106,6 @@ SFFN_DEV bool mbar_wait(uint64_t *bar, uint32_t parity, uint64_t limit_ns = kWai
     return true;
 }
 
-// The same for one of several phases that have kWaitLimitNs together: `end` (0 before the first) is when they are over.
-SFFN_DEV bool mbar_wait_until(uint64_t *bar, uint32_t parity, uint64_t &end) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (end == 0) end = globaltimer_ns() + kWaitLimitNs;
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() >= end) return false;
-    return true;
-}
-
 // L2 policy for data read exactly once (weights): evict first.
 SFFN_DEV uint64_t l2_evict_first_policy() {
     uint64_t pol;
