@@ -163,7 +163,7 @@ SFFN_DEV int cache_page(const PagesArgs &a, int t, int h, int j) {
     return -1;
 }
 
-// Partial result slots as sffn_attn_tree's, of G rows.
+// Partial result slots as sffn_attn_tree's, two a range, of a row tile's rows.
 
 // ---------------------------------------------------------------------------
 // attn_few.cuh over the paged cache

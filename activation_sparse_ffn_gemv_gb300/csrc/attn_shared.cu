@@ -29,8 +29,9 @@ namespace {
 
 // Units (of 64 positions) that an item costs by itself.
 constexpr int kCostTc = 5, kCostFew = 1, kCostRows = 5;
-// Time of a prefix's place in attn_tc.cuh on an SM, in that of a place in attn_few.cuh: kPlaceTc / kPlaceFew (96 sequences
-// on 24576 shared positions: 131 us with 9 / 4, 122 with 12 / 4, 127 with 16 / 4).
+// Time of a prefix's place in attn_tc.cuh on an SM, in that of a place in attn_few.cuh: kPlaceTc / kPlaceFew.  With 9, 11, 12 and
+// 16 / 4: 96 sequences on 24576 shared positions, 64/8 heads, 132, 127, 129, 124 us; 48 on 8192 63, 65, 65, 63; two groups of 32 on
+// 16384, 32/8 heads, 64, 64, 66, 74; 64 of two tokens on 32768, 40/8 heads, 163, 172, 178, 206.
 constexpr int kPlaceTc = 11, kPlaceFew = 4;
 // The same in fp32 (64 sequences on 8192: 464 us with 8 / 4, 407 with 16 / 4, 374 with 32 / 4).
 constexpr int kPlaceRows = 32, kPlaceFew32 = 4;

@@ -8,6 +8,12 @@
 // Every term is a whole multiple, of at most 127 * 127, of the page's step, and there are at most 128
 // that are not zero: below 2^21 of them, so any sum of terms is exact in 32 bits.  The choice
 // therefore does not depend on the order in which a kernel adds, and equal scores are equal.
+//
+// What the 8 bits cost: one step for all columns of a page and head (and for all query heads of a key head) is coarse
+// where a few columns are much larger than the others.  Of 123 chosen among 1000 pages of 16 keys (8 query heads of 128,
+// random keys) 0.97 are those that the same score without rounding chooses, 0.76 with two columns of 10 times the
+// size, 0.93 with two of 30 times, 0.95 with one of 100 times; the softmax weight of the chosen pages was as large in each
+// (0.165 and 0.165, 0.31 and 0.30, 0.66 and 0.63, 0.78 and 0.77): rounding outwards leans to pages of large keys.
 #include "common.cuh"
 #include "internal.h"
 

@@ -503,7 +503,9 @@ sffn_status sffn_attn_tree(const void *q, int64_t q_stride, int T, int n_heads, 
  *   sffn_page_bounds, sffn_page_select, sffn_attn_pages
  *                      each token reads the few pages whose keys can matter to it: the pages' key
  *                      bounds are kept beside the cache, a cheap score of the queries against
- *                      them picks the pages, and the attention runs over those alone.
+ *                      them picks the pages, and the attention runs over those alone.  A step: the new rows go to
+ *                      the cache (sffn_qk_norm_rope), pages that they filled get their bounds, the
+ *                      tokens choose their pages, and attend.
  * Heads, rows and the cache as above; workspaces from sffn_attn_workspace_size (which: 4 = sffn_attn_shared,
  * 5 = sffn_page_bounds with T pages, 6 = sffn_attn_pages) and sffn_page_select_workspace_size. */
 
@@ -549,7 +551,8 @@ size_t sffn_page_select_workspace_size(int T, int n_kv_heads, int table_width);
  * ties to the lower page; c is the query rounded to whole multiples of a step (found as in
  * sffn_page_bounds, over the query heads of the key head; in units of that step; NaN counts as 0).  But for that rounding
  * the score bounds every key's score in the page from above.  The sums are exact in 32 bits, so the choice
- * does not depend on the order in which they are made.
+ * does not depend on the order in which they are made.  (Both roundings are to 8 bits: where a few of the keys' columns are ten
+ * times the others, a quarter of the pages may be others than the unrounded score would choose.)
  *   q          [T, n_heads, head_dim] in the cache's dtype, token stride q_stride.
  *   cache      shape and type (keys and values are not read).
  *   bounds     as written by sffn_page_bounds, for every page below each token's n_recent last ones.
