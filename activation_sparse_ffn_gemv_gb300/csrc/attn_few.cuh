@@ -22,7 +22,7 @@
 #pragma once
 
 #include "attn.cuh"
-#include "tcgen05.cuh"
+#include "tma_warp.cuh"
 
 namespace sffn {
 namespace few {

@@ -39,27 +39,6 @@ SFFN_DEV void tma_load_4d(void *smem_dst, const CUtensorMap *map, int x, int y, 
         : "memory");
 }
 
-// A 4-D tile load (of whole rows of the other dimensions) and the announcement of its bytes, issued by one lane of a
-// converged warp: the operands are the same in every lane, and as the compiler sees that, they go straight to the
-// uniform registers that the instruction takes.
-SFFN_DEV void tma_load_rows_warp(uint32_t dst, const CUtensorMap *map, int u, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %2, %2, %3}], [%4], %5;\n\t}\n" ::"r"(dst),
-        "l"(map), "r"(0), "r"(u), "r"(bar), "l"(policy)
-        : "memory");
-}
-SFFN_DEV void mbar_expect_tx_warp(uint32_t bar, uint32_t bytes) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(bar),
-        "r"(bytes)
-        : "memory");
-}
-
 // 3-D tile store from shared memory (the box's start inside the tensor), in the thread's current
 // bulk group; bulk_commit closes the group, bulk_wait_read waits until the closed groups have been
 // read out of shared memory, bulk_wait until they are complete.

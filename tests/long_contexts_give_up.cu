@@ -1,7 +1,7 @@
 // The long-context attention kernels with a stretch of the cache whose loads are left out: the waits for them run out, and the
 // kernels have to report that and end.  SHARED selects sffn_attn_shared's source.  Built together with the library's other
 // objects, so that the calls are the library's own.
-#include "tcgen05.cuh"
+#include "tma_warp.cuh"
 
 namespace sffn {
 namespace {
